@@ -129,7 +129,7 @@ def prepare(case, seed):
 # ------------------------------------------------------------------ plain forms
 def _codes(x):
     """Rows as whole numbers of -127..127 and their scales; the border between two codes is told in 64 bits."""
-    scale = x.float().abs().amax(1) / 127
+    scale = (x.abs().amax(1).double() / 127).float()   # (a tensor over a number in 32 bits is not rounded right)
     return torch.round(x.double() / scale[:, None].double()), scale
 
 
