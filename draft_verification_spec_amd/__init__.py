@@ -1,5 +1,6 @@
-"""Python binding of the library's C ABI: spec_verify (include/spec_verify.h)
-and sv_kd (include/sv_kd.h).
+"""Python binding of the library's C ABI: spec_verify (include/spec_verify.h),
+sv_kd (include/sv_kd.h) and the vocabulary-head operators (include/sv_head.h, in
+head.py).
 
 Argument marshalling only: every step of the verification runs in the HIP
 library libspec_verify.so built next to this file.  PyTorch supplies device
@@ -14,6 +15,10 @@ import os
 import re
 from collections import namedtuple
 from typing import Optional
+
+from .head import (Act8, GRAD_HIDDEN, GRAD_WEIGHT, HEAD_BAD_TARGET, HEAD_BAD_WEIGHT, HEAD_EMPTY, HEAD_NAN,  # noqa: F401
+                   HEAD_POSINF, HeadCEResult, HeadKDResult, SV_I8, act8_pack, act8_unpack, bind as _bind_head, head_ce,
+                   head_kd, head_logits, sv_head_shape_t, sv_logits_shape_t)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspec_verify.so")
@@ -90,6 +95,7 @@ def load_library() -> ctypes.CDLL:
         lib.sv_kd_workspace_bytes.restype = ctypes.c_size_t
         lib.sv_kd.argtypes = [ctypes.POINTER(sv_kd_shape_t), P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         lib.sv_kd.restype = ctypes.c_int
+        _bind_head(lib)
         _lib = lib
     return _lib
 

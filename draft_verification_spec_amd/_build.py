@@ -1,12 +1,12 @@
 """Compile the HIP library for gfx950 in-tree (libspec_verify.so next to this file):
-the verification kernel and the distillation kernel."""
+the verification kernel, the distillation kernel and the vocabulary-head kernels."""
 import os
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "spec_verify.hip")
-SRCS = [SRC, os.path.join(HERE, "csrc", "sv_kd.hip")]
+SRCS = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("sv_kd.hip", "sv_head.hip", "sv_logits8.hip")]
 LIB = os.path.join(HERE, "libspec_verify.so")
 HEADER = os.path.join(ROOT, "include", "spec_verify.h")
 # the benchmark's stream-read reference (measurement only; not part of the library)

@@ -1,0 +1,122 @@
+// sv_act8.h -- hidden rows to 8-bit codes and back, shared by sv_act8_pack,
+// sv_act8_unpack and the token side of sv_head_logits.  gfx950 (MI355X).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sv_device.h"
+#include "sv_head.h"
+
+namespace sv_act8 {
+
+using sv_dev::u32x4;
+
+template <int DT> struct In;
+template <> struct In<SV_BF16> {
+  static constexpr int E = 2;
+  static __device__ __forceinline__ float one(const char *p) {
+    return __uint_as_float((uint32_t)*(const uint16_t *)p << 16);
+  }
+  static __device__ __forceinline__ float of(u32x4 v, int i) {
+    const uint32_t w = v[i >> 1];
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+};
+template <> struct In<SV_F32> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ float one(const char *p) { return *(const float *)p; }
+  static __device__ __forceinline__ float of(u32x4 v, int i) { return __uint_as_float(v[i]); }
+};
+
+// The code of x under scale s > 0: x / s rounded to even as if it were exact.
+// The fp32 quotient may round across a border k + 1/2; the remainder
+// x - (k +- 1/2) s is exact in sign as one fused step, and puts the code back.
+__device__ __forceinline__ int code_of(float x, float s) {
+  float r = __builtin_rintf(x / s);
+  if (fmaf(-(r + 0.5f), s, x) > 0.f) r += 1.f;
+  else if (fmaf(-(r - 0.5f), s, x) < 0.f) r -= 1.f;
+  else if (((int)r & 1) && (fmaf(-(r + 0.5f), s, x) == 0.f)) r += 1.f;
+  else if (((int)r & 1) && (fmaf(-(r - 0.5f), s, x) == 0.f)) r -= 1.f;
+  return (int)fminf(fmaxf(r, -127.f), 127.f);
+}
+
+// The scale of a row from the largest magnitude's bits (a NaN's or an
+// infinity's are at or above those of infinity).
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  return top >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(top) / 127.f;
+}
+
+struct Pack {
+  const char *x;
+  int64_t x_ld;                          // bytes
+  int8_t *codes;
+  int64_t c_ld;                          // bytes
+  float *scale;
+  int32_t H, Hp;                         // columns; columns written (zeros past H)
+  int32_t vec;                           // 16-byte aligned x rows, codes rows aligned for their stores
+};
+
+// One workgroup per row: the largest magnitude (its bit pattern, as an integer
+// maximum, keeps NaN and infinity above every number), then the codes.  HBM
+// bound: the row is read twice, the second time from the caches.
+template <int DT> __global__ __launch_bounds__(256) void pack_kernel(Pack P) {
+  constexpr int E = In<DT>::E, W = 16 / E;
+  __shared__ uint32_t top_of[4];
+  const int tid = threadIdx.x;
+  const int64_t n = blockIdx.x;
+  const char *x = P.x + n * P.x_ld;
+  int8_t *c = P.codes + n * P.c_ld;
+  const int nv = P.vec ? P.H / W : 0;
+  uint32_t top = 0;
+  for (int q = tid; q < nv; q += 256) {
+    const u32x4 v = *(const u32x4 *)(x + (int64_t)q * 16);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t u = __float_as_uint(In<DT>::of(v, i)) & 0x7fffffffu;
+      top = u > top ? u : top;
+    }
+  }
+  for (int i = nv * W + tid; i < P.H; i += 256) {
+    const uint32_t u = __float_as_uint(In<DT>::one(x + (int64_t)i * E)) & 0x7fffffffu;
+    top = u > top ? u : top;
+  }
+  top = (uint32_t)sv_dev::wave_max_i((int)top);
+  if ((tid & 63) == 0) top_of[tid >> 6] = top;
+  __syncthreads();
+  top = top_of[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) top = top_of[w] > top ? top_of[w] : top;
+  const float s = scale_of(top);
+  const bool none = !(s > 0.f);          // a row of zeros, of magnitudes whose scale rounds to 0, or NaN
+  if (tid == 0) P.scale[n] = s;
+  for (int q = tid; q < nv; q += 256) {
+    const u32x4 v = *(const u32x4 *)(x + (int64_t)q * 16);
+    uint32_t o[W / 4];
+#pragma unroll
+    for (int w = 0; w < W / 4; ++w) {
+      o[w] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!none) o[w] |= (uint32_t)(code_of(In<DT>::of(v, 4 * w + i), s) & 0xff) << (8 * i);
+    }
+    if constexpr (W == 8) *(uint64_t *)(c + (int64_t)q * 8) = ((uint64_t)o[1] << 32) | o[0];
+    else *(uint32_t *)(c + (int64_t)q * 4) = o[0];
+  }
+  for (int i = nv * W + tid; i < P.Hp; i += 256)
+    c[i] = (i < P.H && !none) ? (int8_t)code_of(In<DT>::one(x + (int64_t)i * E), s) : (int8_t)0;
+}
+
+inline bool pack_vec(int E, const void *x, int64_t x_ld, const void *c, int64_t c_ld) {
+  const int st = 16 / E;                 // bytes of codes of one vector
+  return ((uintptr_t)x & 15) == 0 && (x_ld & 15) == 0 && ((uintptr_t)c & (st - 1)) == 0 && (c_ld & (st - 1)) == 0;
+}
+
+inline void pack(int dtype, int N, Pack P, hipStream_t st) {
+  const int E = dtype == SV_BF16 ? 2 : 4;
+  P.vec = pack_vec(E, P.x, P.x_ld, P.codes, P.c_ld) ? 1 : 0;
+  if (dtype == SV_BF16) hipLaunchKernelGGL((pack_kernel<SV_BF16>), dim3(N), dim3(256), 0, st, P);
+  else hipLaunchKernelGGL((pack_kernel<SV_F32>), dim3(N), dim3(256), 0, st, P);
+}
+
+}  // namespace sv_act8

@@ -1,0 +1,834 @@
+// sv_head.hip -- cross entropy and top-32 distillation from hidden rows under a
+// vocabulary head, with the gradients of rows and head, for gfx950 (MI355X).
+//
+// With z = (1/T) x W^T, lse = ln sum exp z and u the row's weight,
+//   loss = sum u (lse - z_t)              (or sum u KL over the stored 32)
+//   dz = u (exp(z - lse) - pt),  dx = (1/T) dz W,  dW = (1/T) dz^T x.
+// The logits are never stored.  Forward: one product whose tiles keep only each
+// row's maximum and sum of exps; a small gather forms the z of the targets.
+// Backward: a piece of the vocabulary at a time, the product again, its tiles
+// turned into dz in the operands' type, then two products with dz.  A piece is
+// complete for dW and adds to dx in fp32.  That is four products for the three
+// that stored logits would need, and memory for a piece in place of N x V.
+//
+// Rows are put in an order first: those with a gradient, then those with a loss
+// only, then those left out (ignored or with bad inputs); each product covers
+// its front part and stops there, so padding and prompt positions cost nothing.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "sv_device.h"
+#include "sv_gemm.h"
+#include "sv_head.h"
+#include "sv_head_host.h"
+#include "sv_kd.h"
+
+namespace {
+
+using namespace sv_gemm;
+using sv_dev::NEG_INF;
+using sv_dev::wave_max_f;
+using sv_dev::wave_or;
+using sv_dev::wave_sum_d;
+using sv_dev::wave_sum_f;
+using sv_head_host::cdiv;
+using sv_head_host::Plan;
+using sv_head_host::TOP;
+
+constexpr float LOG2E = 1.44269504f;
+constexpr double LN2 = 0.6931471805599453;
+
+template <int DT> __device__ __forceinline__ float load_real(const char *p, int64_t i) {
+  if constexpr (DT == SV_BF16) return __uint_as_float((uint32_t)((const uint16_t *)p)[i] << 16);
+  else if constexpr (DT == SV_F32) return ((const float *)p)[i];
+  else return (float)((const int8_t *)p)[i];
+}
+template <int DT> __device__ __forceinline__ void store_real(char *p, int64_t i, float v) {
+  if constexpr (DT == SV_BF16) ((__bf16 *)p)[i] = (__bf16)v;
+  else ((float *)p)[i] = v;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+}
+// four consecutive elements
+template <int DT> __device__ __forceinline__ void store4(char *p, int64_t i, const float (&v)[4]) {
+  if constexpr (DT == SV_BF16) *(u32x2 *)(p + i * 2) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+  else *(f32x4 *)(p + i * 4) = f32x4{v[0], v[1], v[2], v[3]};
+}
+
+// What the kernels share: the call's arrays and the workspace.
+struct Head {
+  int32_t N, H, V, T;                    // T: targets per row
+  int32_t grads;
+  int32_t ignore;
+  float inv_t;
+  int64_t Kp, Np;
+  const char *hidden;
+  int64_t h_ld;                          // bytes
+  const float *h_scale;
+  const char *weight;
+  int64_t w_ld;                          // bytes
+  // cross entropy
+  const int32_t *targets;
+  const float *row_weight;
+  // distillation
+  const float *tval;
+  const int32_t *tidx, *row_sample;
+  const float *rewards;
+  int32_t S, G;
+  float w_max;
+  // results
+  float *rows, *lse, *weight_out, *loss;
+  int32_t *status;
+  char *gh, *gw;
+  // workspace (per place in the order unless said otherwise)
+  int32_t *counts;                       // rows with a gradient, rows with a loss
+  int32_t *perm;                         // the row at a place
+  float *alpha;                          // factor of the product: scale / T
+  float *ga, *gb;                        // factor of dz in dx and in dW (with the row's scale)
+  float *lse2;                           // base-2 normaliser, rounded; the rest of it is in ga, gb
+  float *w;                              // per row: u (distillation)
+  int32_t *flags;                        // per row: data-error bits (distillation)
+  float *zt;                             // [.., T] logits of the targets
+  float *pt;                             // [.., T] their probabilities (distillation)
+  double *term;                          // loss terms
+  float2 *part;                          // [column tiles][N] base-2 maximum and sum of exps
+  char *xs, *xt, *dz, *dzt, *wt;
+  float *acc;
+};
+
+// ---------------------------------------------------------------- rows' inputs
+// The distillation's weight and data errors of a row: one wave per row.
+__global__ __launch_bounds__(256) void kd_rows_kernel(Head P) {
+  const int lane = threadIdx.x & 63;
+  const int n = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (n >= P.N) return;
+  const int s = P.row_sample[n];
+  const bool badw = s < 0 || s >= P.S;
+  double w = 0.0;
+  if (!badw) {
+    const int g0 = s / P.G * P.G;
+    double sum = 0.0;
+    for (int l = 0; l < P.G; l += 64) sum += wave_sum_d(l + lane < P.G ? (double)P.rewards[g0 + l + lane] : 0.0);
+    w = sum > 0.0 ? (double)P.rewards[s] / sum : 0.0;
+    w = w > 0.0 ? w : 0.0;               // negative and NaN weights count as 0
+    w = w < (double)P.w_max ? w : (double)P.w_max;
+  }
+  const float v = lane < TOP ? P.tval[(int64_t)n * TOP + lane] : NEG_INF;
+  const int x = lane < TOP ? P.tidx[(int64_t)n * TOP + lane] : -1;
+  const bool pad = v == NEG_INF || x == -1;
+  int F = 0;
+  if (!pad && (x < 0 || x >= P.V)) F |= SV_KD_BAD_INDEX;
+  if (lane < TOP && !(v == v)) F |= SV_KD_NAN;
+  if (lane < TOP && v == __builtin_inff()) F |= SV_KD_POSINF;
+  const int mine = pad ? -1 : x, in = (!pad && x >= 0 && x < P.V) ? x : -1;
+  bool dup = false;
+  for (int e = 0; e < TOP; ++e) dup |= e < lane && in >= 0 && __builtin_amdgcn_readlane(mine, e) == in;
+  if (dup) F |= SV_KD_DUP_INDEX;
+  F = wave_or(F) | (badw ? SV_KD_BAD_INDEX : 0);
+  if (!F && wave_max_f(pad ? NEG_INF : v) == NEG_INF) F = SV_KD_EMPTY;
+  if (lane == 0) {
+    P.w[n] = (float)w;
+    P.flags[n] = F;
+    if (P.weight_out) P.weight_out[n] = (float)w;
+  }
+}
+
+// 0: a gradient, 1: a loss only, 2: left out
+template <bool KD> __device__ __forceinline__ int class_of(const Head &P, int n, int &bits) {
+  bits = 0;
+  if constexpr (KD) {
+    bits = P.flags[n];
+    return (P.grads && !bits && P.w[n] > 0.f) ? 0 : 1;
+  } else {
+    const int t = P.targets[n];
+    if (t == P.ignore) return 2;
+    if (t < 0 || t >= P.V) bits |= SV_HEAD_BAD_TARGET;
+    const float w = P.row_weight ? P.row_weight[n] : 1.f;
+    if (!(fabsf(w) < __builtin_inff())) bits |= SV_HEAD_BAD_WEIGHT;
+    if (bits) return 2;
+    return (P.grads && w != 0.f) ? 0 : 1;
+  }
+}
+
+// The order of rows: by class, by index within a class.  One workgroup; two
+// passes over N small entries (a few microseconds at the largest batches).
+template <bool KD> __global__ __launch_bounds__(1024) void order_kernel(Head P) {
+  __shared__ int cnt[3][16];
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  int c[3] = {0, 0, 0};
+  for (int n = tid; n < P.N; n += 1024) {
+    int bits;
+    const int k = class_of<KD>(P, n, bits);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) c[q] += k == q;
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const int s = sv_dev::wave_sum_i(c[q]);
+    if (lane == 0) cnt[q][wid] = s;
+  }
+  __syncthreads();
+  int base[3] = {0, 0, 0}, tot[3] = {0, 0, 0};
+  for (int w = 0; w < 16; ++w)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) tot[q] += cnt[q][w];
+  base[1] = tot[0];
+  base[2] = tot[0] + tot[1];
+  if (tid == 0) { P.counts[0] = tot[0]; P.counts[1] = tot[0] + tot[1]; }
+  for (int n0 = 0; n0 < P.N; n0 += 1024) {
+    const int n = n0 + tid;
+    int bits = 0;
+    const int k = n < P.N ? class_of<KD>(P, n, bits) : 3;
+    int at = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint64_t b = __ballot(k == q);
+      if (k == q) at = __popcll(b & ((1ull << lane) - 1));
+      if (lane == 0) cnt[q][wid] = __popcll(b);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      int before = 0, all = 0;
+      for (int w = 0; w < 16; ++w) { before += w < wid ? cnt[q][w] : 0; all += cnt[q][w]; }
+      if (k == q) P.perm[base[q] + before + at] = n;
+      base[q] += all;
+    }
+    if (k == 2) {                        // left out: its results are known
+      const float r = bits ? __builtin_nanf("") : 0.f;
+      P.rows[n] = r;
+      if (P.lse) P.lse[n] = r;
+      if (P.status) P.status[n] = bits;
+    }
+  }
+}
+
+// Rows with a loss, in order, in the operands' type, zeros up to whole steps.
+// 8-bit codes are exact in bf16 and fp32; their scale goes into alpha.
+template <int HT, int DT> __global__ __launch_bounds__(256) void stage_rows_kernel(Head P) {
+  const int at = blockIdx.x;
+  if (at >= P.counts[1]) return;
+  const int n = P.perm[at];
+  const char *src = P.hidden + (int64_t)n * P.h_ld;
+  char *dst = P.xs + (int64_t)at * P.Kp * Mma<DT>::E;
+  for (int k = threadIdx.x; k < (int)P.Kp; k += 256) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
+  if (threadIdx.x == 0) P.alpha[at] = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
+}
+
+// z of the targets: one wave per (row, target), fp32 sums.
+template <int DT> __global__ __launch_bounds__(256) void targets_kernel(Head P) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int at = (int)(i / P.T), j = (int)(i - (int64_t)at * P.T);
+  if (at >= P.counts[1]) return;
+  const int n = P.perm[at];
+  const int id = P.T == 1 ? P.targets[n] : P.tidx[(int64_t)n * P.T + j];
+  float s = 0.f;
+  if (id >= 0 && id < P.V) {
+    constexpr int E = Mma<DT>::E, W = 16 / E;
+    const char *x = P.xs + (int64_t)at * P.Kp * E;
+    const char *w = P.weight + (int64_t)id * P.w_ld;
+    const bool vec = (((uintptr_t)P.weight | (uintptr_t)P.w_ld) & 15) == 0;
+    const int nv = P.H / W;
+    for (int q = lane; q < nv; q += 64) {  // (the same order of terms whatever the alignment)
+      const u32x4 a = *(const u32x4 *)(x + (int64_t)q * 16);
+      if (vec) {
+        const u32x4 b = *(const u32x4 *)(w + (int64_t)q * 16);
+#pragma unroll
+        for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), sv_dev::unpack<DT>(b, e), s);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), load_real<DT>(w, q * W + e), s);
+      }
+    }
+    for (int k = nv * W + lane; k < P.H; k += 64) s = fmaf(load_real<DT>(x, k), load_real<DT>(w, k), s);
+    s = wave_sum_f(s);
+  }
+  if (lane == 0) P.zt[i] = s * P.alpha[at];
+}
+
+// -------------------------------------------------------------------- products
+struct Prod {
+  const char *x;
+  int64_t x_ld;
+  const char *y;
+  int64_t y_ld;
+  int64_t v0;                            // first vocabulary entry
+  int32_t M, N;                          // rows and columns of the result
+  int32_t mt, nt, band, nk;
+  int32_t tile0;                         // column tile of the row statistics at column 0
+  int64_t piece;                         // row length of dz
+  int32_t split, first, vec;
+};
+
+// Forward tile: each row's maximum m (base 2) and sum of 2^(z log2 e - m) over
+// the tile's columns.  A NaN makes both NaN, +inf alone only the sum.
+template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kernel(Head P, Prod G) {
+  __shared__ __align__(16) char lds[T::LDS];
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[1];
+  if (m0 >= M) return;
+  typename Mma<DT>::Acc acc[T::FM][T::FN];
+  clear<DT, T>(acc);
+  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
+  product<DT, T>(acc, lds, X, Y, 0, G.nk);
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+  __syncthreads();                       // the tiles are done with: their LDS takes the waves' results
+  float2 *red = (float2 *)lds;           // [WN][BM]
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) {
+    const int r = (wm * T::FM + f) * 16 + (lane & 15);
+    const float a = m0 + r < M ? P.alpha[m0 + r] : 0.f;
+    float m = NEG_INF;
+#pragma unroll
+    for (int g = 0; g < T::FN; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4 + i;
+        const float z = n < G.N ? acc[f][g][i] * a : NEG_INF;
+        acc[f][g][i] = z;
+        m = sv_dev::fmax_nan(m, z);
+      }
+    m = sv_dev::fmax_nan(m, __shfl_xor(m, 16));
+    m = sv_dev::fmax_nan(m, __shfl_xor(m, 32));
+    const float hi = m == NEG_INF ? NEG_INF : m * LOG2E, ref = hi == NEG_INF ? 0.f : hi;
+    float s = 0.f;
+#pragma unroll
+    for (int g = 0; g < T::FN; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(fmaf(acc[f][g][i], LOG2E, -ref));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) red[wn * T::BM + r] = make_float2(hi, s);
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r < T::BM; r += T::TPB) {
+    if (m0 + r >= M) break;
+    float2 t = red[r];
+    for (int q = 1; q < T::WN; ++q) {
+      const float2 o = red[q * T::BM + r];
+      const float m = sv_dev::fmax_nan(t.x, o.x), ref = m == NEG_INF ? 0.f : m;
+      t.y = t.y * __builtin_amdgcn_exp2f(t.x - ref) + o.y * __builtin_amdgcn_exp2f(o.x - ref);
+      t.x = m;
+    }
+    P.part[(int64_t)(G.tile0 + in) * P.N + m0 + r] = t;
+  }
+}
+
+// Backward tile of a piece: dz = u (2^(z log2 e - lse2)), rounded to the
+// operands' type, as rows (for dx) and transposed (for dW); zeros where the row
+// or the column does not exist, so that both can be summed in whole steps.
+template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
+  __shared__ __align__(16) char lds[T::LDS];
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[0];
+  constexpr int E = Mma<DT>::E;
+  const int Mp = (M + STEP / E - 1) / (STEP / E) * (STEP / E);
+  if (m0 >= Mp) return;
+  typename Mma<DT>::Acc acc[T::FM][T::FN];
+  clear<DT, T>(acc);
+  if (m0 < M && n0 < G.N) {
+    const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+    const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
+    product<DT, T>(acc, lds, X, Y, 0, G.nk);
+  }
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) {
+    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    const bool on = m < M;
+    const float a = on ? P.alpha[m] : 0.f, l2 = on ? P.lse2[m] : 0.f;
+    const float ga = on ? P.ga[m] : 0.f, gb = on ? P.gb[m] : 0.f;
+#pragma unroll
+    for (int g = 0; g < T::FN; ++g) {
+      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
+      float p[4], d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2));
+        if (!(n + i < G.N) || ga == 0.f) p[i] = 0.f;
+        d[i] = p[i] * ga;
+      }
+      if (on) store4<DT>(P.dz, (int64_t)m * G.piece + n, d);
+      if (P.dzt && m < Mp) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_real<DT>(P.dzt, (int64_t)(n + i) * P.Np + m, p[i] * gb);
+      }
+    }
+  }
+}
+
+// dz at the targets of a piece: u (p - pt), from the targets' own logits, over
+// what the tiles stored there.
+template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod G) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int at = (int)(i / P.T), j = (int)(i - (int64_t)at * P.T);
+  if (at >= P.counts[0]) return;
+  const float ga = P.ga[at];
+  if (ga == 0.f) return;
+  const int n = P.perm[at];
+  const int id = P.T == 1 ? P.targets[n] : P.tidx[(int64_t)n * P.T + j];
+  const int64_t c = id - G.v0;
+  if (c < 0 || c >= G.N) return;
+  if (P.T != 1 && !(P.tval[(int64_t)n * P.T + j] > NEG_INF)) return;   // padding: no target
+  const float p = __builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at]));
+  // ga and gb hold the normaliser's part beyond fp32, which is p's alone
+  const float u = (P.T == 1 ? (P.row_weight ? P.row_weight[n] : 1.f) : P.w[n] * P.pt[i]) * P.inv_t;
+  store_real<DT>(P.dz, (int64_t)at * G.piece + c, fmaf(p, ga, -u));
+  if (P.dzt) store_real<DT>(P.dzt, c * P.Np + at, fmaf(p, P.gb[at], -(P.h_scale ? u * P.h_scale[n] : u)));
+}
+
+// dx of a piece: sums of the piece's parts, added to the earlier pieces' in fp32.
+template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(Head P, Prod G) {
+  __shared__ __align__(16) char lds[T::LDS];
+  const int tiles = G.mt * G.nt, part = blockIdx.x / tiles;
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x - part * tiles, tiles), G.mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[0];
+  if (m0 >= M) return;
+  typename Mma<DT>::Acc acc[T::FM][T::FN];
+  clear<DT, T>(acc);
+  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
+  const int per = (G.nk + G.split - 1) / G.split, s0 = part * per;
+  const int ns = G.nk - s0 < per ? G.nk - s0 : per;
+  product<DT, T>(acc, lds, X, Y, s0 * STEP, ns > 0 ? ns : 0);
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+  float *out = P.acc + (int64_t)part * P.N * P.H;
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) {
+    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    if (m >= M) continue;
+#pragma unroll
+    for (int g = 0; g < T::FN; ++g) {
+      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
+      float *o = out + (int64_t)m * P.H + n;
+      if (G.vec && n + 4 <= G.N) {
+        f32x4 v = acc[f][g];
+        if (!G.first) v += *(const f32x4 *)o;
+        *(f32x4 *)o = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < G.N) o[i] = G.first ? acc[f][g][i] : o[i] + acc[f][g][i];
+      }
+    }
+  }
+}
+
+// dW of a piece: complete, in the weight's type.
+template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(Head P, Prod G) {
+  __shared__ __align__(16) char lds[T::LDS];
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN;
+  typename Mma<DT>::Acc acc[T::FM][T::FN];
+  clear<DT, T>(acc);
+  constexpr int q = STEP / Mma<DT>::E;
+  const int nk = (P.counts[0] + q - 1) / q;
+  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, G.M - m0 < T::BM ? G.M - m0 : T::BM, (int64_t)nk * STEP};
+  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)nk * STEP};
+  product<DT, T>(acc, lds, X, Y, 0, nk);
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+  char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) {
+    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    if (m >= G.M) continue;
+#pragma unroll
+    for (int g = 0; g < T::FN; ++g) {
+      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
+      const int64_t o = (int64_t)m * P.H + n;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = acc[f][g][i];
+      if (G.vec && n + 4 <= G.N) {
+        store4<DT>(out, o, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < G.N) store_real<DT>(out, o + i, v[i]);
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------- rows' results
+// The normaliser of each row from its tiles, in a fixed order: lanes take
+// (row, part of the tiles), waves take parts too; then one thread per row.
+template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Head P, int tiles, int per) {
+  __shared__ double ms[1024], ss[1024];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int M = P.counts[1], r0 = blockIdx.x * per;
+  if (r0 >= M) return;
+  const int r = lane & (per - 1), parts = 16 * (64 / per), q = wid * (64 / per) + lane / per;
+  const int at = r0 + r;
+  double m = -__builtin_inf(), s = 0.0;
+  if (at < M)
+    for (int t = q; t < tiles; t += parts) {
+      const float2 v = P.part[(int64_t)t * P.N + at];
+      if (!(v.x == v.x)) m = s = __builtin_nan("");
+      else if (v.x > (float)m) {
+        s = s * (double)__builtin_amdgcn_exp2f((float)m - v.x) + (double)v.y;
+        m = v.x;
+      } else if (v.x != NEG_INF) {
+        s += (double)v.y * (double)__builtin_amdgcn_exp2f(v.x - (float)m);
+      }
+    }
+  ms[q * per + r] = m;
+  ss[q * per + r] = s;
+  __syncthreads();
+  if (threadIdx.x >= (unsigned)per || at >= M) return;
+  m = -__builtin_inf();
+  bool nan = false;
+  for (int t = 0; t < parts; ++t) {
+    const double v = ms[t * per + r];
+    nan |= !(v == v);
+    m = v > m ? v : m;
+  }
+  s = 0.0;
+  for (int t = 0; t < parts; ++t) {
+    const double v = ms[t * per + r];
+    if (v > -__builtin_inf()) s += ss[t * per + r] * (double)__builtin_amdgcn_exp2f((float)(v - m));
+  }
+  int F = nan ? SV_HEAD_NAN : m == __builtin_inf() ? SV_HEAD_POSINF : m == -__builtin_inf() ? SV_HEAD_EMPTY : 0;
+  static_assert(SV_HEAD_NAN == SV_KD_NAN && SV_HEAD_POSINF == SV_KD_POSINF && SV_HEAD_EMPTY == SV_KD_EMPTY, "one set");
+  const double l2 = F ? 0.0 : m + log2(s);
+  const int n = P.perm[at];
+  const float hi = (float)l2;
+  P.lse2[at] = hi;
+  float u;
+  if constexpr (KD) {
+    // the part of the normaliser beyond fp32, for the distillation's rows kernel
+    P.term[at] = l2;
+    P.flags[n] |= F;
+    u = P.w[n];
+  } else {
+    u = P.row_weight ? P.row_weight[n] : 1.f;
+    const double lse = l2 * LN2;
+    const float nll = F ? __builtin_nanf("") : (float)(lse - (double)P.zt[at]);
+    P.rows[n] = nll;
+    if (P.lse) P.lse[n] = F ? __builtin_nanf("") : (float)lse;
+    if (P.status) P.status[n] = F;
+    P.term[at] = (!F && u != 0.f) ? (double)u * (double)nll : 0.0;
+  }
+  if (P.grads) {
+    const float c = F ? 0.f : u * (float)(1.0 - (l2 - (double)hi) * LN2) * P.inv_t;
+    P.ga[at] = c;
+    P.gb[at] = (P.h_scale && !F) ? c * P.h_scale[n] : c;
+  }
+}
+
+// KL of a row over its stored entries: one wave per row.
+__global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
+  const int lane = threadIdx.x & 63;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= P.counts[1]) return;
+  const int n = P.perm[at];
+  const int F = P.flags[n];
+  const float v = lane < TOP ? P.tval[(int64_t)n * TOP + lane] : NEG_INF;
+  const int x = lane < TOP ? P.tidx[(int64_t)n * TOP + lane] : -1;
+  const bool use = !F && v != NEG_INF && x != -1;
+  const float mv = wave_max_f(use ? v : NEG_INF);
+  const double a = use ? (double)v - (double)mv : 0.0;
+  const double e = use ? exp(a) : 0.0;
+  const double sv = wave_sum_d(e);
+  const double pt = use ? e / sv : 0.0;
+  const double l2 = P.term[at];
+  double t = 0.0;
+  if (use && pt > 0.0) t = pt * (a - log(sv) - ((double)P.zt[(int64_t)at * TOP + lane] - l2 * LN2));
+  const double kl = wave_sum_d(t);
+  if (lane < TOP) P.pt[(int64_t)at * TOP + lane] = (float)pt;
+  if (lane == 0) {
+    const float w = P.w[n];
+    P.rows[n] = F ? __builtin_nanf("") : (float)kl;
+    if (P.status) P.status[n] = F;
+    P.term[at] = (!F && w > 0.f) ? (double)w * kl : 0.0;
+  }
+}
+
+// The loss terms, in order: a fixed run per thread, then the waves.
+__global__ __launch_bounds__(1024) void loss_kernel(Head P) {
+  __shared__ double red[16];
+  const int M = P.counts[1], per = (M + 1023) / 1024;
+  double s = 0.0;
+  for (int i = threadIdx.x * per; i < M && i < (int)(threadIdx.x + 1) * per; ++i) s += P.term[i];
+  s = wave_sum_d(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int w = 0; w < 16; ++w) t += red[w];
+    P.loss[0] = (float)t;
+  }
+}
+
+// dst[c][r] = src[r][c] for r < rows, zeros for rows .. pad-1: 64 x 64 blocks
+// through LDS.  limit: rows from counts[0] when not null, and rows whose gradient
+// factor is 0 (no gradient, or a data error: its values may be NaN) read as zeros.
+template <int DT> __global__ __launch_bounds__(256) void transpose_kernel(const char *src, int64_t s_ld, int rows,
+                                                                          int cols, char *dst, int64_t d_ld, int pad,
+                                                                          const int32_t *limit, const float *factor) {
+  typedef typename std::conditional<DT == SV_BF16, uint16_t, uint32_t>::type U;
+  __shared__ U t[64][65];
+  const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
+  if (limit) {
+    rows = *limit;
+    pad = (rows + STEP / (int)sizeof(U) - 1) / (STEP / (int)sizeof(U)) * (STEP / (int)sizeof(U));
+  }
+  if (r0 >= pad) return;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = r0 + y + i * 4, c = c0 + x;
+    U v = 0;
+    if (r < rows && c < cols && !(factor && factor[r] == 0.f)) v = *(const U *)(src + r * s_ld + (int64_t)c * sizeof(U));
+    t[y + i * 4][x] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = c0 + y + i * 4, r = r0 + x;
+    if (c < cols && r < pad) *(U *)(dst + c * d_ld + (int64_t)r * sizeof(U)) = t[x][y + i * 4];
+  }
+}
+
+// rows of the weight into rows of whole steps, zeros behind them
+template <int DT> __global__ __launch_bounds__(256) void copy_weight_kernel(const char *src, int64_t ld, int H, char *dst,
+                                                                            int64_t Kp) {
+  const char *s = src + (int64_t)blockIdx.x * ld;
+  char *d = dst + (int64_t)blockIdx.x * Kp * Mma<DT>::E;
+  for (int k = threadIdx.x; k < (int)Kp; k += 256) store_real<DT>(d, k, k < H ? load_real<DT>(s, k) : 0.f);
+}
+
+// dx of every row: its parts summed in order, rounded once; zeros without a gradient.
+template <int DT> __global__ __launch_bounds__(256) void dx_rows_kernel(Head P, int split) {
+  const int at = blockIdx.x;
+  const int64_t n = P.perm[at];
+  const bool on = at < P.counts[0] && P.ga[at] != 0.f;
+  for (int k = threadIdx.x; k < P.H; k += 256) {
+    float v = 0.f;
+    if (on)
+      for (int s = 0; s < split; ++s) v += P.acc[((int64_t)s * P.N + at) * P.H + k];
+    store_real<DT>(P.gh, n * P.H + k, v);
+  }
+}
+
+// ------------------------------------------------------------------------ host
+typedef Tile<8, 4, 2, 4> Big;            // 256 x 256
+typedef Tile<4, 4, 2, 2> Mid;            // 128 x 128
+typedef Tile<2, 2, 1, 4> Few;            // 32 x 128
+
+template <class T> Prod tiled(Prod G, int64_t M, int64_t N) {
+  G.M = (int32_t)M;
+  G.N = (int32_t)N;
+  G.mt = (int32_t)cdiv(M, T::BM);
+  G.nt = (int32_t)cdiv(N, T::BN);
+  G.band = 8;
+  return G;
+}
+
+template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, bool kd, bool direct, hipStream_t st) {
+  constexpr int E = Mma<DT>::E;
+  const dim3 b256(256), b1024(1024);
+  if (kd) hipLaunchKernelGGL(kd_rows_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
+  if (kd) hipLaunchKernelGGL((order_kernel<true>), dim3(1), b1024, 0, st, P);
+  else hipLaunchKernelGGL((order_kernel<false>), dim3(1), b1024, 0, st, P);
+  if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT>), dim3(P.N), b256, 0, st, P);
+  else hipLaunchKernelGGL((stage_rows_kernel<DT, DT>), dim3(P.N), b256, 0, st, P);
+  hipLaunchKernelGGL((targets_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 4)), b256, 0, st, P);
+
+  const int64_t row = L.Kp * E;
+  Prod F = {};
+  F.x = P.xs;
+  F.x_ld = row;
+  F.nk = (int32_t)(row / STEP);
+  auto weight_piece = [&](Prod &G, int64_t v0, int64_t cnt) {
+    G.v0 = v0;
+    if (direct) {
+      G.y = P.weight + v0 * P.w_ld;
+      G.y_ld = P.w_ld;
+    } else {
+      hipLaunchKernelGGL((copy_weight_kernel<DT>), dim3((unsigned)cnt), b256, 0, st, P.weight + v0 * P.w_ld, P.w_ld,
+                         P.H, P.wt, L.Kp);
+      G.y = P.wt;
+      G.y_ld = row;
+    }
+  };
+  const int64_t fstep = direct ? P.V : L.piece;
+  int tiles = 0;
+  for (int64_t v0 = 0; v0 < P.V; v0 += fstep) {
+    const int64_t cnt = P.V - v0 < fstep ? P.V - v0 : fstep;
+    Prod G = tiled<T>(F, P.N, cnt);
+    weight_piece(G, v0, cnt);
+    G.tile0 = tiles;
+    hipLaunchKernelGGL((stats_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
+    tiles += G.nt;
+  }
+  int per = 1;                           // rows of a normaliser workgroup: 64, fewer when there are fewer
+  while (per < 64 && per < P.N) per *= 2;
+  const dim3 ng((unsigned)cdiv(P.N, per));
+  if (kd) {
+    hipLaunchKernelGGL((normaliser_kernel<true>), ng, b1024, 0, st, P, tiles, per);
+    hipLaunchKernelGGL(kd_loss_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
+  } else {
+    hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
+  }
+  hipLaunchKernelGGL(loss_kernel, dim3(1), b1024, 0, st, P);
+  if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+
+  if (P.gw)
+    hipLaunchKernelGGL((transpose_kernel<DT>), dim3((unsigned)cdiv(P.H, 64), (unsigned)cdiv(L.Np, 64)), b256, 0, st,
+                       P.xs, row, P.N, P.H, P.xt, L.Np * E, (int)L.Np, P.counts, P.ga);
+  for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
+    const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
+    const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
+    Prod G = tiled<T>(F, L.Np, cp);
+    weight_piece(G, v0, cnt);
+    G.N = (int32_t)cnt;
+    G.piece = L.piece;
+    hipLaunchKernelGGL((dz_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
+    hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 256)), b256, 0, st, P, G);
+    if (P.gh) {
+      hipLaunchKernelGGL((transpose_kernel<DT>), dim3((unsigned)cdiv(P.H, 64), (unsigned)(cp / 64)), b256, 0, st,
+                         P.weight + v0 * P.w_ld, P.w_ld, (int)cnt, P.H, P.wt, L.piece * E, (int)cp,
+                         (const int32_t *)nullptr, (const float *)nullptr);
+      Prod X = tiled<T>(Prod{}, P.N, P.H);
+      X.x = P.dz;
+      X.x_ld = L.piece * E;
+      X.y = P.wt;
+      X.y_ld = L.piece * E;
+      X.nk = (int32_t)(cp * E / STEP);
+      X.split = L.split;
+      X.first = v0 == 0;
+      X.vec = P.H % 4 == 0;
+      hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt * L.split)), dim3(T::TPB), 0, st, P, X);
+    }
+    if (P.gw) {
+      Prod W = tiled<TW>(Prod{}, cnt, P.H);
+      W.v0 = v0;
+      W.x = P.dzt;
+      W.x_ld = L.Np * E;
+      W.y = P.xt;
+      W.y_ld = L.Np * E;
+      W.vec = P.H % 4 == 0 && ((uintptr_t)P.gw & 15) == 0;
+      hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
+    }
+  }
+  if (P.gh) hipLaunchKernelGGL((dx_rows_kernel<DT>), dim3(P.N), b256, 0, st, P, L.split);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const float *hidden_scale, const void *weight,
+        void *gh, void *gw, void *workspace, hipStream_t st) {
+  const Plan L = sv_head_host::plan_for(&s, kd);
+  char *ws = (char *)workspace;
+  const int he = sv_head_host::esize(s.hidden_dtype);
+  P.N = s.N;
+  P.H = s.H;
+  P.V = s.V;
+  P.T = kd ? TOP : 1;
+  P.grads = s.grads;
+  P.ignore = s.ignore_index;
+  P.inv_t = 1.f / s.temperature;
+  P.Kp = L.Kp;
+  P.Np = L.Np;
+  P.hidden = (const char *)hidden;
+  P.h_ld = (s.hidden_stride ? s.hidden_stride : s.H) * (int64_t)he;
+  P.h_scale = s.hidden_dtype == SV_I8 ? hidden_scale : nullptr;
+  P.weight = (const char *)weight;
+  P.w_ld = (s.weight_stride ? s.weight_stride : s.H) * (int64_t)L.e;
+  P.gh = (s.grads & SV_GRAD_HIDDEN) ? (char *)gh : nullptr;
+  P.gw = (s.grads & SV_GRAD_WEIGHT) ? (char *)gw : nullptr;
+  P.counts = (int32_t *)(ws + L.counts);
+  P.perm = (int32_t *)(ws + L.perm);
+  P.alpha = (float *)(ws + L.alpha);
+  P.ga = (float *)(ws + L.ga);
+  P.gb = (float *)(ws + L.gb);
+  P.lse2 = (float *)(ws + L.lse2);
+  P.w = (float *)(ws + L.w);
+  P.flags = (int32_t *)(ws + L.flags);
+  P.zt = (float *)(ws + L.zt);
+  P.pt = (float *)(ws + L.pt);
+  P.term = (double *)(ws + L.term);
+  P.part = (float2 *)(ws + L.part);
+  P.xs = ws + L.xs;
+  P.xt = ws + L.xt;
+  P.dz = ws + L.dz;
+  P.dzt = P.gw ? ws + L.dzt : nullptr;
+  P.wt = ws + L.wt;
+  P.acc = (float *)(ws + L.acc);
+  const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
+  // tiles by the number of rows: 256 rows a tile read each operand least; fewer
+  // rows than a tile would be multiplied in vain
+  if (s.dtype == SV_BF16)
+    return s.N >= 192 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
+           : s.N > 32 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
+                      : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
+  return s.N >= 192 ? enqueue<SV_F32, Big, Big>(P, L, kd, direct, st)
+         : s.N > 32 ? enqueue<SV_F32, Mid, Mid>(P, L, kd, direct, st)
+                    : enqueue<SV_F32, Few, Mid>(P, L, kd, direct, st);
+}
+
+}  // namespace
+
+extern "C" size_t sv_head_ce_workspace_bytes(const sv_head_shape_t *s) {
+  if (!s || !sv_head_host::head_shape_ok(s, false)) return 0;
+  return sv_head_host::plan_for(s, false).total;
+}
+
+extern "C" size_t sv_head_kd_workspace_bytes(const sv_head_shape_t *s) {
+  if (!s || !sv_head_host::head_shape_ok(s, true)) return 0;
+  return sv_head_host::plan_for(s, true).total;
+}
+
+extern "C" int sv_head_ce(const sv_head_shape_t *shape, const void *hidden, const float *hidden_scale,
+                          const void *weight, const int32_t *targets, const float *row_weight, float *nll, float *lse,
+                          int32_t *status, float *loss, void *grad_hidden, void *grad_weight, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  bool nothing;
+  const int rc = sv_head_host::check_head(shape, false, hidden, hidden_scale, weight, targets, nullptr, nullptr,
+                                          nullptr, nll, loss, grad_hidden, grad_weight, workspace, workspace_bytes,
+                                          &nothing);
+  if (rc != SV_OK || nothing) return rc;
+  Head P = {};
+  P.targets = targets;
+  P.row_weight = row_weight;
+  P.rows = nll;
+  P.lse = lse;
+  P.status = status;
+  P.loss = loss;
+  return run(*shape, false, P, hidden, hidden_scale, weight, grad_hidden, grad_weight, workspace, (hipStream_t)stream);
+}
+
+extern "C" int sv_head_kd(const sv_head_shape_t *shape, const void *hidden, const float *hidden_scale,
+                          const void *weight, const float *topk_val, const int32_t *topk_idx,
+                          const int32_t *row_sample, const float *rewards, float *kl, float *row_weight_out,
+                          int32_t *status, float *loss, void *grad_hidden, void *grad_weight, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  bool nothing;
+  const int rc = sv_head_host::check_head(shape, true, hidden, hidden_scale, weight, topk_val, topk_idx, row_sample,
+                                          rewards, kl, loss, grad_hidden, grad_weight, workspace, workspace_bytes,
+                                          &nothing);
+  if (rc != SV_OK || nothing) return rc;
+  Head P = {};
+  P.tval = topk_val;
+  P.tidx = topk_idx;
+  P.row_sample = row_sample;
+  P.rewards = rewards;
+  P.S = shape->S;
+  P.G = shape->group;
+  P.w_max = shape->w_max;
+  P.rows = kl;
+  P.weight_out = row_weight_out;
+  P.status = status;
+  P.loss = loss;
+  return run(*shape, true, P, hidden, hidden_scale, weight, grad_hidden, grad_weight, workspace, (hipStream_t)stream);
+}

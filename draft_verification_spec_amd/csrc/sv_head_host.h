@@ -1,0 +1,178 @@
+// sv_head_host.h -- host-side argument checks, piece sizes and workspace layouts
+// of the vocabulary-head operators, in plain C++ with no HIP (a CPU build with
+// sanitizers drives it over valid and invalid shapes).
+#pragma once
+
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+#include "sv_head.h"
+
+namespace sv_head_host {
+
+constexpr int TOP = 32;                  // stored entries per row (sv_head_kd)
+constexpr int STEP = 128;                // bytes of k per step of the tiled product
+constexpr int64_t MAX_LD = (int64_t)1 << 22;   // bytes between rows of a tiled operand: a tile's offsets fit 31 bits
+
+inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
+inline int esize(int dtype) { return dtype == SV_F32 ? 4 : dtype == SV_BF16 ? 2 : 1; }
+inline bool real_dtype(int dt) { return dt == SV_F32 || dt == SV_BF16; }
+
+// ------------------------------------------------------------------- 8-bit rows
+inline int check_act8(int N, int H, int dtype, const void *x, int64_t x_stride, const void *codes,
+                      int64_t codes_stride, const void *scale) {
+  if (!real_dtype(dtype)) return SV_ERR_DTYPE;
+  if (N < 0 || H < 1 || H > SV_HEAD_MAX_H) return SV_ERR_SHAPE;
+  if ((x_stride && x_stride < H) || (codes_stride && codes_stride < H)) return SV_ERR_SHAPE;
+  if (N && (!x || !codes || !scale)) return SV_ERR_NULL;
+  return SV_OK;
+}
+
+// ---------------------------------------------------------------- 8-bit logits
+// Copied operands (rows that are not made of whole aligned steps) have rows of Kp bytes.
+struct LogitsLayout {
+  int64_t Kp;
+  int64_t piece;                         // vocabulary entries per product where the weight is copied
+  size_t codes, scale, weight, total;
+};
+
+inline bool logits_shape_ok(const sv_logits_shape_t *s) {
+  if (s->N < 0 || s->H < 1 || s->H > SV_HEAD_MAX_H || s->V < 1 || s->V > SV_HEAD_MAX_V) return false;
+  if (s->hidden_dtype != SV_I8 && !real_dtype(s->hidden_dtype)) return false;
+  if (!real_dtype(s->out_dtype)) return false;
+  if ((s->hidden_stride && s->hidden_stride < s->H) || (s->weight_stride && s->weight_stride < s->H) ||
+      (s->out_stride && s->out_stride < s->V))
+    return false;
+  // a workgroup's index is 31 bits
+  return cdiv(s->N, 16) * cdiv(s->V, 64) < 0x7fffffffLL;
+}
+
+// Whether weight code rows can be read in 16-byte pieces where they lie.
+inline bool logits_direct(int64_t stride, uintptr_t base) { return stride % 16 == 0 && stride <= MAX_LD && base % 16 == 0; }
+
+inline LogitsLayout logits_layout(const sv_logits_shape_t *s) {
+  LogitsLayout L;
+  L.Kp = up(s->H, STEP);
+  // a copied piece of about 128 MB: it stays in the 256 MB Infinity Cache between its copy and its product
+  L.piece = up(((int64_t)128 << 20) / L.Kp, 256);
+  if (L.piece > up(s->V, 256)) L.piece = up(s->V, 256);
+  size_t o = 0;
+  L.codes = o;  o = up(o + (size_t)s->N * L.Kp, 256);
+  L.scale = o;  o = up(o + (size_t)s->N * 4, 256);
+  L.weight = o; o = up(o + (size_t)L.piece * L.Kp, 256);
+  L.total = o;
+  return L;
+}
+
+inline int check_logits(const sv_logits_shape_t *s, const void *hidden, const void *hidden_scale, const void *codes,
+                        const void *wscale, const void *logits, const void *ws, size_t wsb, bool *nothing) {
+  *nothing = false;
+  if (!s) return SV_ERR_NULL;
+  if ((s->hidden_dtype != SV_I8 && !real_dtype(s->hidden_dtype)) || !real_dtype(s->out_dtype)) return SV_ERR_DTYPE;
+  if (!logits_shape_ok(s)) return SV_ERR_SHAPE;
+  if (s->N == 0) { *nothing = true; return SV_OK; }
+  if (!hidden || !codes || !wscale || !logits || (s->hidden_dtype == SV_I8 && !hidden_scale)) return SV_ERR_NULL;
+  if (!ws || wsb < logits_layout(s).total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
+  return SV_OK;
+}
+
+// ------------------------------------------------------------------------ losses
+struct Plan {
+  int e;                                 // bytes of an element
+  int64_t Kp;                            // hidden width in whole steps, elements
+  int64_t Np;                            // rows in whole steps, elements
+  int64_t piece, pieces;                 // vocabulary entries per piece, pieces
+  int split;                             // parts of a piece's length in the hidden gradient
+  // workspace sections
+  size_t counts, perm, alpha, ga, gb, lse2, w, flags, zt, pt, term, part, xs, xt, dz, dzt, wt, acc, total;
+};
+
+inline bool head_shape_ok(const sv_head_shape_t *s, bool kd) {
+  if (s->N < 0 || s->N > SV_HEAD_MAX_N || s->H < 1 || s->H > SV_HEAD_MAX_H || s->V < 1 || s->V > SV_HEAD_MAX_V)
+    return false;
+  if (!real_dtype(s->dtype) || (s->hidden_dtype != s->dtype && s->hidden_dtype != SV_I8)) return false;
+  if (s->grads & ~(SV_GRAD_HIDDEN | SV_GRAD_WEIGHT)) return false;
+  if ((s->hidden_stride && s->hidden_stride < s->H) || (s->weight_stride && s->weight_stride < s->H)) return false;
+  if (kd) {
+    if (s->temperature != 1.f) return false;
+    if (s->N > 0 && (s->S < 1 || s->group < 1 || s->S % s->group != 0)) return false;
+    if (!(s->w_max > 0.f)) return false;
+  }
+  return true;
+}
+
+// Whether the weight's rows are whole aligned steps where they lie.
+inline bool weight_direct(const sv_head_shape_t *s, uintptr_t base) {
+  const int64_t e = esize(s->dtype), ld = (s->weight_stride ? s->weight_stride : s->H) * e;
+  return (s->H * e) % STEP == 0 && ld % 16 == 0 && ld <= MAX_LD && base % 16 == 0;
+}
+
+inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
+  Plan p;
+  const int e = p.e = esize(s->dtype), q = STEP / e;
+  const int64_t N = s->N, H = s->H, T = kd ? TOP : 1;
+  p.Kp = up(H, q);
+  p.Np = up(N, q);
+  // A piece: its dz (twice, also transposed) and its transposed weight are written
+  // and read back, so it is kept near 512 MB; a whole number of 256 entries,
+  // all pieces alike.
+  const int64_t per = (s->grads ? p.Np * e * 2 : 0) + p.Kp * e;
+  int64_t most = ((int64_t)512 << 20) / per / 256 * 256;
+  if (most < 256) most = 256;
+  const int64_t by_ld = MAX_LD / e / 2;
+  if (most > by_ld) most = by_ld;
+  p.pieces = cdiv(s->V, most);
+  p.piece = up(cdiv(s->V, p.pieces), 256);
+  p.pieces = cdiv(s->V, p.piece);
+  // the hidden gradient has N x H results and a piece's length to sum: split it
+  // until about two workgroups a CU have work, 1024 entries a part at least
+  const int64_t tiles = cdiv(N, N >= 192 ? 256 : N > 32 ? 128 : 32) * cdiv(H, N >= 192 ? 256 : 128);
+  int64_t sp = tiles > 0 ? 512 / tiles : 1;
+  if (sp > p.piece / 1024) sp = p.piece / 1024;
+  p.split = (int)(sp < 1 ? 1 : sp);
+  const bool gh = s->grads & SV_GRAD_HIDDEN, gw = s->grads & SV_GRAD_WEIGHT, g = gh || gw;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) & ~(size_t)255; return at; };
+  p.counts = take(256);
+  p.perm = take(N * 4);
+  p.alpha = take(N * 4);
+  p.ga = take(N * 4);
+  p.gb = take(N * 4);
+  p.lse2 = take(N * 4);
+  p.w = take(N * 4);
+  p.flags = take(N * 4);
+  p.zt = take(N * T * 4);
+  p.pt = take(kd ? N * T * 4 : 0);
+  p.term = take(N * 8);
+  p.part = take((size_t)cdiv(s->V, 128) * N * 8);
+  p.xs = take((size_t)N * p.Kp * e);
+  p.xt = take(gw ? (size_t)H * p.Np * e : 0);
+  p.dz = take(g ? (size_t)N * p.piece * e : 0);
+  p.dzt = take(gw ? (size_t)p.piece * p.Np * e : 0);
+  // a copied piece of the weight, and later the transposed one, in one place
+  p.wt = take((size_t)p.piece * p.Kp * e);
+  p.acc = take(gh ? (size_t)p.split * N * H * 4 : 0);
+  p.total = o;
+  return p;
+}
+
+inline int check_head(const sv_head_shape_t *s, bool kd, const void *hidden, const void *hidden_scale,
+                      const void *weight, const void *a, const void *b, const void *c, const void *d, const void *rows,
+                      const void *loss, const void *gh, const void *gw, const void *ws, size_t wsb, bool *nothing) {
+  *nothing = false;
+  if (!s) return SV_ERR_NULL;
+  if (!real_dtype(s->dtype) || (s->hidden_dtype != s->dtype && s->hidden_dtype != SV_I8)) return SV_ERR_DTYPE;
+  if (!(s->temperature > 0.f) || s->temperature == INFINITY) return SV_ERR_TEMPERATURE;
+  if (!head_shape_ok(s, kd)) return SV_ERR_SHAPE;
+  if (s->N == 0) { *nothing = true; return SV_OK; }
+  if (!hidden || !weight || !a || !rows || !loss || (s->hidden_dtype == SV_I8 && !hidden_scale)) return SV_ERR_NULL;
+  if (kd && (!b || !c || !d)) return SV_ERR_NULL;
+  if (((s->grads & SV_GRAD_HIDDEN) && !gh) || ((s->grads & SV_GRAD_WEIGHT) && !gw)) return SV_ERR_NULL;
+  if (!ws || wsb < plan_for(s, kd).total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
+  return SV_OK;
+}
+
+}  // namespace sv_head_host

@@ -1,0 +1,220 @@
+// sv_logits8.hip -- 8-bit hidden rows (sv_act8_pack, sv_act8_unpack) and the
+// vocabulary head in 8-bit integers (sv_head_logits), for gfx950 (MI355X).
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "sv_act8.h"
+#include "sv_device.h"
+#include "sv_gemm.h"
+#include "sv_head.h"
+#include "sv_head_host.h"
+
+namespace {
+
+using namespace sv_gemm;
+using sv_head_host::cdiv;
+
+// codes * scale, in fp32, rounded once to the output's type
+template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int8_t *codes, int64_t c_ld,
+                                                                       const float *scale, char *y, int H, int64_t total,
+                                                                       int vec) {
+  // one thread per four elements of a row where rows are whole fours, else per element
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  if (vec) {
+    const int per = H / 4;
+    const int64_t n = i / per;
+    const int q = (int)(i - n * per);
+    const uint32_t c = *(const uint32_t *)(codes + n * c_ld + 4 * q);
+    const float s = scale[n];
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (float)(int8_t)(c >> (8 * k)) * s;
+    if constexpr (DT == SV_F32) {
+      *(f32x4 *)(y + i * 16) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      u32x2 o;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        o[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
+      *(u32x2 *)(y + i * 8) = o;
+    }
+  } else {
+    const int64_t n = i / H;
+    const float v = (float)codes[n * c_ld + (i - n * H)] * scale[n];
+    if constexpr (DT == SV_F32) ((float *)y)[i] = v;
+    else ((__bf16 *)y)[i] = (__bf16)v;
+  }
+}
+
+// rows of bytes into rows of whole steps, zeros behind them
+__global__ __launch_bounds__(256) void copy_rows_kernel(const int8_t *src, int64_t ld, int H, int8_t *dst, int64_t Kp) {
+  const int8_t *s = src + (int64_t)blockIdx.x * ld;
+  int8_t *d = dst + (int64_t)blockIdx.x * Kp;
+  for (int i = threadIdx.x; i < (int)Kp; i += 256) d[i] = i < H ? s[i] : (int8_t)0;
+}
+
+struct LogitsP {
+  const char *x;                         // token codes, rows of whole steps
+  int64_t x_ld;
+  const float *sx;
+  const char *w;                         // weight codes
+  int64_t w_ld, w_bytes;
+  const float *sw;
+  char *out;
+  int64_t out_ld;                        // elements
+  int N, V, mt, nt, nk, band, out_vec;
+};
+
+// One tile of logits.  The int32 sums are exact; the two scales are joined first
+// and the product with them rounds once (twice with a bf16 output).
+template <class T, int OT> __global__ __launch_bounds__(T::TPB) void logits_kernel(LogitsP P) {
+  __shared__ __align__(16) char lds[T::LDS];
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x, P.mt * P.nt), P.mt, P.nt, P.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN;
+  i32x4 acc[T::FM][T::FN];
+  clear<SV_I8, T>(acc);
+  const Rows X = {P.x + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, (int64_t)P.nk * STEP};
+  const Rows Y = {P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
+  product<SV_I8, T>(acc, lds, X, Y, 0, P.nk);
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+#pragma unroll
+  for (int g = 0; g < T::FN; ++g) {
+    const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
+    float sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[i] = n + i < P.V ? P.sw[n + i] : 0.f;
+#pragma unroll
+    for (int f = 0; f < T::FM; ++f) {
+      const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+      if (m >= P.N) continue;
+      const float sx = P.sx[m];
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (float)acc[f][g][i] * (sx * sw[i]);
+      const int64_t o = (int64_t)m * P.out_ld + n;
+      if (P.out_vec && n + 4 <= P.V) {
+        if constexpr (OT == SV_F32) {
+          *(f32x4 *)(P.out + o * 4) = f32x4{v[0], v[1], v[2], v[3]};
+        } else {
+          u32x2 u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            u[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
+                   (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
+          *(u32x2 *)(P.out + o * 2) = u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < P.V) {
+            if constexpr (OT == SV_F32) ((float *)P.out)[o + i] = v[i];
+            else ((__bf16 *)P.out)[o + i] = (__bf16)v[i];
+          }
+      }
+    }
+  }
+}
+
+template <class T> void launch_logits(LogitsP P, int ot, hipStream_t st) {
+  P.mt = (int)cdiv(P.N, T::BM);
+  P.nt = (int)cdiv(P.V, T::BN);
+  P.band = 8;
+  const dim3 grid((unsigned)((int64_t)P.mt * P.nt)), block(T::TPB);
+  if (ot == SV_BF16) hipLaunchKernelGGL((logits_kernel<T, SV_BF16>), grid, block, 0, st, P);
+  else hipLaunchKernelGGL((logits_kernel<T, SV_F32>), grid, block, 0, st, P);
+}
+
+}  // namespace
+
+extern "C" int sv_act8_pack(int32_t N, int32_t H, int32_t dtype, const void *x, int64_t x_stride, int8_t *codes,
+                            int64_t codes_stride, float *scale, void *stream) {
+  const int rc = sv_head_host::check_act8(N, H, dtype, x, x_stride, codes, codes_stride, scale);
+  if (rc != SV_OK || N == 0) return rc;
+  sv_act8::Pack P = {(const char *)x, (x_stride ? x_stride : H) * (int64_t)sv_head_host::esize(dtype), codes,
+                     codes_stride ? codes_stride : H, scale, H, H, 0};
+  sv_act8::pack(dtype, N, P, (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+extern "C" int sv_act8_unpack(int32_t N, int32_t H, const int8_t *codes, int64_t codes_stride, const float *scale,
+                              int32_t y_dtype, void *y, void *stream) {
+  const int rc = sv_head_host::check_act8(N, H, y_dtype, y, 0, codes, codes_stride, scale);
+  if (rc != SV_OK || N == 0) return rc;
+  const int64_t ld = codes_stride ? codes_stride : H;
+  const int vec = H % 4 == 0 && ld % 4 == 0 && ((uintptr_t)codes & 3) == 0 && ((uintptr_t)y & 15) == 0;
+  const int64_t total = (int64_t)N * H / (vec ? 4 : 1);
+  if (cdiv(total, 256) > 0x7fffffffLL) return SV_ERR_SHAPE;
+  const dim3 grid((unsigned)cdiv(total, 256)), block(256);
+  if (y_dtype == SV_BF16)
+    hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H,
+                       total, vec);
+  else
+    hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H,
+                       total, vec);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+extern "C" size_t sv_head_logits_workspace_bytes(const sv_logits_shape_t *s) {
+  if (!s || !sv_head_host::logits_shape_ok(s)) return 0;
+  return sv_head_host::logits_layout(s).total;
+}
+
+extern "C" int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden, const float *hidden_scale,
+                              const int8_t *weight_codes, const float *weight_scale, void *logits, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  bool nothing;
+  const int rc = sv_head_host::check_logits(shape, hidden, hidden_scale, weight_codes, weight_scale, logits, workspace,
+                                            workspace_bytes, &nothing);
+  if (rc != SV_OK || nothing) return rc;
+  const sv_logits_shape_t s = *shape;
+  const hipStream_t st = (hipStream_t)stream;
+  const sv_head_host::LogitsLayout L = sv_head_host::logits_layout(&s);
+  char *ws = (char *)workspace;
+  int8_t *codes = (int8_t *)(ws + L.codes);
+  const int64_t hs = s.hidden_stride ? s.hidden_stride : s.H, wst = s.weight_stride ? s.weight_stride : s.H;
+  const int64_t os = s.out_stride ? s.out_stride : s.V;
+  const int oe = sv_head_host::esize(s.out_dtype);
+  LogitsP P = {};
+  P.x = (const char *)codes;
+  P.x_ld = L.Kp;
+  P.sx = (float *)(ws + L.scale);
+  if (s.hidden_dtype == SV_I8) {
+    hipLaunchKernelGGL(copy_rows_kernel, dim3(s.N), dim3(256), 0, st, (const int8_t *)hidden, hs, s.H, codes, L.Kp);
+    P.sx = hidden_scale;
+  } else {
+    sv_act8::Pack Q = {(const char *)hidden, hs * sv_head_host::esize(s.hidden_dtype), codes, L.Kp,
+                       (float *)(ws + L.scale), s.H, (int32_t)L.Kp, 0};
+    sv_act8::pack(s.hidden_dtype, s.N, Q, st);
+  }
+  P.N = s.N;
+  P.nk = (int)(L.Kp / STEP);
+  P.out_ld = os;
+  const bool direct = sv_head_host::logits_direct(wst, (uintptr_t)weight_codes);
+  const int64_t step = direct ? s.V : L.piece;
+  for (int64_t v0 = 0; v0 < s.V; v0 += step) {
+    P.V = (int)(s.V - v0 < step ? s.V - v0 : step);
+    if (direct) {
+      P.w = (const char *)weight_codes;
+      P.w_ld = wst;
+      // a load's range is checked by whole dwords: the last one of a row counts if
+      // any of its bytes does (aligned, so it lies in that byte's memory); the token
+      // codes are 0 past H, so what else it holds adds nothing
+      P.w_bytes = sv_head_host::up(s.H, 4);
+    } else {
+      hipLaunchKernelGGL(copy_rows_kernel, dim3(P.V), dim3(256), 0, st, weight_codes + v0 * wst, wst, s.H,
+                         (int8_t *)(ws + L.weight), L.Kp);
+      P.w = ws + L.weight;
+      P.w_ld = P.w_bytes = L.Kp;
+    }
+    P.sw = weight_scale + v0;
+    P.out = (char *)logits + v0 * oe;
+    P.out_vec = (os * oe) % (4 * oe) == 0 && ((uintptr_t)P.out & (4 * oe - 1)) == 0;
+    if (s.N > 32) launch_logits<Tile<4, 4, 2, 2>>(P, s.out_dtype, st);
+    else launch_logits<Tile<2, 2, 1, 4>>(P, s.out_dtype, st);
+  }
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
