@@ -207,10 +207,10 @@ def _own(s):
     if op == "ce":
         r = sv.head_ce(x, s["w"], s["targets"], s["row_weight"], temperature=s["temperature"], ignore_index=IGNORE,
                        grad=s["grad"])
-        out = dict(loss=r.loss, nll=r.nll, lse=r.lse)
+        out = dict(loss=r.loss[0], nll=r.nll, lse=r.lse)
     else:
         r = sv.head_kd(x, s["w"], s["topk_val"], s["topk_idx"], s["row_sample"], s["rewards"], GROUP, grad=s["grad"])
-        out = dict(loss=r.loss, kl=r.kl, weight=r.weight)
+        out = dict(loss=r.loss[0], kl=r.kl, weight=r.weight)
     if s["grad"]:
         out["grad_hidden"], out["grad_weight"] = r.grad_hidden, r.grad_weight
     return out
