@@ -1,25 +1,39 @@
 // sv_gemm.h -- the tiled matrix product behind the vocabulary-head operators,
-// for gfx950 (MI355X): C[m][n] = sum_k X[m][k] Y[n][k], both operands with k
-// contiguous ("rows against rows"), in bf16, fp32 or int8.
+// for gfx950 (MI355X): C[m][n] = sum_k X(m, k) Y(n, k) in bf16, fp32 or int8.
+// Each operand lies either with k along its rows ("rows": X[m][k]) or with k
+// down its columns ("columns": X[k][m]), so the gradients' products read dz, the
+// weight and the hidden rows as they lie and nothing is transposed in memory.
 //
 // One core for the three types: a step takes 128 bytes of k (64 bf16, 32 fp32,
-// 128 int8) of every row of both tiles, and a matrix instruction takes from
-// each lane 16 bytes of one row: lane l holds row l & 15 and 16-byte piece
-// l >> 4 of a 64-byte half step.  Which k those bytes are does not matter as
-// long as both operands agree, so the three types differ in one instruction
-// (four for fp32, whose instruction takes one element a lane) and nowhere else.
+// 128 int8) of both tiles, and a matrix instruction takes from each lane 16
+// bytes of k of one m or n: lane l holds index l & 15 and 16-byte piece l >> 4 of
+// a 64-byte half step.  Which k those bytes are does not matter as long as both
+// operands agree, so the types differ in one instruction (four for fp32, whose
+// instruction takes one element a lane) and in how columns are read.
 //
 // Tiles go from memory to LDS by direct 16-byte loads (no registers between),
-// the next step's while this step is computed, two buffers, one barrier a
-// step.  A direct load writes 64 consecutive pieces, so a row's eight pieces
-// are permuted on the memory side: piece p of row r lies at place p ^ (r & 7),
-// and the 16 rows that a fragment load touches fall on different banks.
+// into two buffers for the rows' operand and three for the columns', whose data
+// comes from farther (the weight from HBM).  A wave holds two sets of fragments:
+// while the matrix instructions work on one half step, the next half step's
+// fragments are read.  The one barrier of a step stands in its middle: by then
+// every wave has read all of the step's buffers, which later loads may overwrite,
+// and the next step's tiles have landed, one and two whole steps after they were
+// asked for.
+//
+// A direct load writes 64 consecutive 16-byte pieces, so pieces are permuted on
+// the memory side to keep LDS reads off each other's banks.  Rows: piece p of row
+// r lies at place p ^ (r & 7), and the 8 rows read together hit 8 places.
+// Columns: the 16 columns of a fragment move together, by two bits of the row
+// index that tell apart the rows read together; bf16 columns are turned into
+// pieces of k by the transposing LDS read, fp32 ones are read element by element.
 // The columns' fragment is the instruction's first operand: a lane then holds
 // four consecutive n of one m, which row-major stores want.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "sv_head.h"
 
@@ -63,83 +77,227 @@ template <int FM_, int FN_, int WM_, int WN_> struct Tile {
   static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
   static constexpr int NW = WM * WN, TPB = 64 * NW;
   static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
-  static constexpr int BUF = (BM + BN) * STEP;           // bytes of one LDS buffer
-  static constexpr int LDS = 2 * BUF;
+  static constexpr int XBUF = BM * STEP, YBUF = BN * STEP;   // bytes of one LDS buffer
+  static constexpr int LDS = 2 * XBUF + 3 * YBUF;
 };
 
-// One tile's rows of an operand: the first row, the distance of rows in bytes,
-// the rows that exist (>= 1; rows past them repeat the last one, their products
-// are not used) and the bytes of a row that exist.
-struct Rows {
+// One tile's part of an operand.
+//   rows:    base at the tile's first row; `count` rows exist (>= 1; rows past them
+//            repeat the last one, their products are not used)
+//   columns: base at the tile's first column of k = 0; `count` k exist, at least
+//            one in each step taken (later ones repeat the last: the other operand
+//            holds zeros there)
+// ld: bytes between rows (of m or of k); bytes: what exists of a row from base.
+struct Part {
   const char *base;
   int64_t ld;
-  int rows;
+  int64_t count;
   int64_t bytes;
 };
 
-// The products of one tile over steps [0, nk) from byte k0 of the rows.
-template <int DT, class T>
-__device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::FN], char *lds, const Rows &X,
-                                        const Rows &Y, int k0, int nk) {
 #ifdef __HIP_DEVICE_COMPILE__            // (the host pass knows no gfx950 builtins)
-  constexpr int NX = T::BM / 8 / T::NW, NY = T::BN / 8 / T::NW;
-  static_assert(NX >= 1 && NY >= 1 && T::BM % (8 * T::NW) == 0 && T::BN % (8 * T::NW) == 0, "tile of whole loads");
-  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wid / T::WN, wn = wid % T::WN;
-  // no load leaves the rows that exist: the resource ends with the last one
-  const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)X.base, 0, (int)((int64_t)(X.rows - 1) * X.ld + X.bytes), 0x00020000);
-  const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)Y.base, 0, (int)((int64_t)(Y.rows - 1) * Y.ld + Y.bytes), 0x00020000);
-  int xo[NX], yo[NY];
-  const int sub = lane >> 3, piece = ((lane & 7) ^ sub) * 16;
-#pragma unroll
-  for (int j = 0; j < NX; ++j) {
-    const int r = (wid + j * T::NW) * 8 + sub;
-    xo[j] = (r < X.rows ? r : X.rows - 1) * (int)X.ld + piece;
-  }
-#pragma unroll
-  for (int j = 0; j < NY; ++j) {
-    const int r = (wid + j * T::NW) * 8 + sub;
-    yo[j] = (r < Y.rows ? r : Y.rows - 1) * (int)Y.ld + piece;
-  }
-  auto issue = [&](char *buf, int ko) {
-#pragma unroll
-    for (int j = 0; j < NX; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xr, (__attribute__((address_space(3))) void *)(buf + (wid + j * T::NW) * 1024), 16, xo[j], ko, 0, 0);
-#pragma unroll
-    for (int j = 0; j < NY; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          yr, (__attribute__((address_space(3))) void *)(buf + T::BM * STEP + (wid + j * T::NW) * 1024), 16, yo[j], ko,
-          0, 0);
-  };
-  const int xf = wm * T::FM * 16 * STEP, yf = T::BM * STEP + wn * T::FN * 16 * STEP;
-  int at[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) at[h] = (lane & 15) * STEP + (((h * 4 + (lane >> 4)) ^ (lane & 7)) << 4);
+// Loads and reads of one operand's tile: R indices (m or n), COL: k down columns.
+template <int DT, int R, int NW, bool COL> struct Side {
+  static constexpr int E = Mma<DT>::E, KR = STEP / E;    // k a step
+  static constexpr int NL = R / 8 / NW;                  // 16-byte loads a thread and step
+  static_assert(NL >= 1 && NL < 16 && R % (8 * NW) == 0, "tile of whole loads");
+  static constexpr int PR = COL ? R * E / 16 : 8;        // pieces of an LDS row
+  static constexpr int GP = E;                           // pieces of 16 columns
+  static constexpr int MASK = R / 16 - 1 < 3 ? R / 16 - 1 : 3;
+  typedef __attribute__((address_space(3))) void lds_void;
 
-  if (nk > 0) issue(lds, k0);
-  for (int s = 0; s < nk; ++s) {
-    // this step's tiles have landed for every wave, and every wave is done with
-    // the buffer that the next step's loads write
-    __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0)
-    __syncthreads();
-    if (s + 1 < nk) issue(lds + ((s + 1) & 1) * T::BUF, k0 + (s + 1) * STEP);
-    const char *b = lds + (s & 1) * T::BUF;
+  __amdgpu_buffer_rsrc_t rsrc;
+  const char *base;
+  int64_t ld, left, bytes;
+  int off[NL];                                           // rows: the byte offset; columns: of the piece in its row
+  int wid;
+
+  // two bits of k's index that differ between rows read together
+  static __device__ __forceinline__ int turn(int r) { return (DT == SV_BF16 ? r : r >> 2) & MASK; }
+  static __device__ __forceinline__ int row_of(int wid, int j) { return ((wid + j * NW) * 64 + (threadIdx.x & 63)) / PR; }
+
+  int pos;                                               // rows: the next step's byte
+
+  __device__ __forceinline__ void start(const Part &p, int s0) {
+    pos = s0 * STEP;
+    wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    ld = p.ld;
+    bytes = p.bytes;
+    if constexpr (COL) {
+      base = p.base + (int64_t)s0 * KR * ld;
+      left = p.count - (int64_t)s0 * KR;
+    } else {
+      base = p.base;
+      left = p.count;
+      // no load leaves the rows that exist: the resource ends with the last one
+      rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)((left - 1) * ld + bytes), 0x00020000);
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 x[T::FM], y[T::FN];
+    for (int j = 0; j < NL; ++j) {
+      const int c = (wid + j * NW) * 64 + (threadIdx.x & 63), r = c / PR, q = c % PR;
+      if constexpr (COL) off[j] = (((q / GP) ^ turn(r)) * GP + q % GP) * 16;
+      else off[j] = (int)((r < left ? r : left - 1) * ld) + (q ^ (r & 7)) * 16;
+    }
+  }
+  // the next step's loads
+  __device__ __forceinline__ void issue(char *buf) {
+    if constexpr (COL) {
+      const int have = left < KR ? (int)left : KR;
+      rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)((have - 1) * ld + bytes), 0x00020000);
 #pragma unroll
-      for (int f = 0; f < T::FM; ++f) x[f] = *(const u32x4 *)(b + xf + at[h] + f * 16 * STEP);
+      for (int j = 0; j < NL; ++j) {
+        const int r = row_of(wid, j);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(buf + (wid + j * NW) * 1024), 16,
+                                                 (r < have ? r : have - 1) * (int)ld + off[j], 0, 0, 0);
+      }
+      base += KR * ld;
+      left -= KR;
+    } else {
 #pragma unroll
-      for (int f = 0; f < T::FN; ++f) y[f] = *(const u32x4 *)(b + yf + at[h] + f * 16 * STEP);
+      for (int j = 0; j < NL; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(buf + (wid + j * NW) * 1024), 16, off[j], pos, 0, 0);
+      pos += STEP;
+    }
+  }
+  template <int F> static constexpr int reads() { return !COL ? F : DT == SV_BF16 ? 2 * F : 4 * F; }
+  // (g0 + f) ^ t; in fours the exclusive or stays within them, and the lanes' part
+  // of it is the same for every four
+  template <int F> static __device__ __forceinline__ int place(int g0, int f, int t) {
+    if constexpr (F % 4 == 0) return g0 + (f & ~3) + ((f & 3) ^ t);
+    else return (g0 + f) ^ t;
+  }
+  // fragments g0 .. g0 + F - 1 (of 16 indices) of half step h
+  template <int F> static __device__ __forceinline__ void read(u32x4 (&v)[F], const char *buf, int g0, int h) {
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    if constexpr (!COL) {
+      const char *at = buf + g0 * 16 * STEP + i * STEP + (((h * 4 + q) ^ (lane & 7)) << 4);
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[f] = *(const u32x4 *)(at + f * 16 * STEP);
+    } else if constexpr (DT == SV_BF16) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const char *at = buf + (h * 32 + q * 8 + (i >> 2)) * (R * E) + (i & 3) * 8;
+      const int t = turn(i >> 2);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const char *p = at + place<F>(g0, f, t) * 32;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * R * E)));
+        v[f] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    } else {
+      const char *at = buf + (h * 16 + q * 4) * (R * E) + i * 4;
+      const int t = turn(q * 4);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const char *p = at + place<F>(g0, f, t) * 64;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[f][e] = *(const uint32_t *)(p + e * (R * E));
+      }
+    }
+  }
+};
+#endif
+
+#ifdef __HIP_DEVICE_COMPILE__
+// The order of a half step's instructions: MM matrix instructions with LD loads,
+// then RD LDS reads, spread evenly between them.
+template <int MM, int RD, int LD> __device__ __forceinline__ void mix() {
+  constexpr int N = RD + LD, K = MM / N > 0 ? MM / N : 1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, K, 0);
+    if (i < LD) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  if constexpr (MM > N * K) __builtin_amdgcn_sched_group_barrier(0x008, MM - N * K, 0);
+}
+#endif
+
+// The products of one tile over steps [s0, s0 + nk).  XC, YC: k down the columns.
+template <int DT, class T, bool XC = false, bool YC = false>
+__device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::FN], char *lds, const Part &X,
+                                        const Part &Y, int s0, int nk) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef Side<DT, T::BM, T::NW, XC> SX;
+  typedef Side<DT, T::BN, T::NW, YC> SY;
+  if (nk <= 0) return;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int gx = wid / T::WN * T::FM, gy = wid % T::WN * T::FN;
+  SX sx;
+  SY sy;
+  sx.start(X, s0);
+  sy.start(Y, s0);
+  char *const yl = lds + 2 * T::XBUF;
+  u32x4 x0[T::FM], y0[T::FN], x1[T::FM], y1[T::FN];
+  auto read = [&](u32x4 (&x)[T::FM], u32x4 (&y)[T::FN], int s, int yb, int h) {
+    SX::read(x, lds + (s & 1) * T::XBUF, gx, h);
+    SY::read(y, yl + yb * T::YBUF, gy, h);
+  };
+  // One barrier: this wave's LDS reads are done and its loads have landed, but for
+  // the columns' tile of the step after next.  Written out, because a fence would
+  // wait for that one too; the empty asm keeps the compiler's accesses on their side.
+  auto landed = [&](bool ahead) {
+    asm volatile("" ::: "memory");
+    if (ahead) __builtin_amdgcn_s_waitcnt(0x0070 | SY::NL);   // vmcnt(NL) lgkmcnt(0)
+    else __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  typedef typename Mma<DT>::Acc Acc;
+  auto mul = [&](Acc (&c)[T::FM][T::FN], u32x4 (&x)[T::FM], u32x4 (&y)[T::FN]) {
+#pragma unroll
+    for (int f = 0; f < T::FM; ++f)
+#pragma unroll
+      for (int g = 0; g < T::FN; ++g) Mma<DT>::mul(c[f][g], y[g], x[f]);
+  };
+  sx.issue(lds);
+  sy.issue(yl);
+  if (nk > 1) sy.issue(yl + T::YBUF);
+  landed(nk > 1);
+  if (nk > 1) sx.issue(lds + T::XBUF);
+  if (nk > 2) sy.issue(yl + 2 * T::YBUF);
+  read(x0, y0, 0, 0, 0);
+  int yb = 0;                                            // the columns' buffer of this step
+  // One step.  Loads and LDS reads are spread between the matrix instructions: a
+  // wave issues in order, and eight waves that all ask for their fragments first
+  // keep the matrix units waiting for the LDS.
+  constexpr int MM = T::FM * T::FN * (DT == SV_F32 ? 4 : 1);
+  constexpr int RD = SX::template reads<T::FM>() + SY::template reads<T::FN>(), LD = SX::NL + SY::NL;
+  auto step = [&](int s, Acc (&c)[T::FM][T::FN], auto whole) {
+    constexpr bool W = decltype(whole)::value;           // three more steps follow
+    read(x1, y1, s, yb, 1);
+    mul(c, x0, y0);
+    mix<MM, RD, 0>();
+    landed(W || s + 2 < nk);
+    if (W || s + 2 < nk) sx.issue(lds + (s & 1) * T::XBUF);
+    if (W || s + 3 < nk) sy.issue(yl + yb * T::YBUF);
+    yb = yb == 2 ? 0 : yb + 1;
+    if (W || s + 1 < nk) read(x0, y0, s + 1, yb, 0);
+    mul(c, x1, y1);
+    if constexpr (W) mix<MM, RD, LD>();
+  };
+  auto sum = [&](int s, auto whole) {
+    if constexpr (DT == SV_F32) {
+      // fp32 sums are kept in two levels, 32 terms and then the steps: the error of
+      // a long sum grows with the number of steps, not of terms
+      Acc part[T::FM][T::FN];
 #pragma unroll
       for (int f = 0; f < T::FM; ++f)
 #pragma unroll
-        for (int g = 0; g < T::FN; ++g) Mma<DT>::mul(acc[f][g], y[g], x[f]);
+        for (int g = 0; g < T::FN; ++g) part[f][g] = 0;
+      step(s, part, whole);
+#pragma unroll
+      for (int f = 0; f < T::FM; ++f)
+#pragma unroll
+        for (int g = 0; g < T::FN; ++g) acc[f][g] += part[f][g];
+    } else {
+      step(s, acc, whole);
     }
-  }
+  };
+  int s = 0;
+  for (; s + 3 < nk; ++s) sum(s, std::true_type());
+  for (; s < nk; ++s) sum(s, std::false_type());
 #endif
 }
 

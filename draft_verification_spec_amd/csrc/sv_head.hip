@@ -65,6 +65,7 @@ struct Head {
   int32_t ignore;
   float inv_t;
   int64_t Kp, Np;
+  int64_t x_ld, dz_ld;                   // bytes between rows of xs, of dz
   const char *hidden;
   int64_t h_ld;                          // bytes
   const float *h_scale;
@@ -87,16 +88,18 @@ struct Head {
   int32_t *counts;                       // rows with a gradient, rows with a loss
   int32_t *perm;                         // the row at a place
   float *alpha;                          // factor of the product: scale / T
-  float *ga, *gb;                        // factor of dz in dx and in dW (with the row's scale)
-  float *lse2;                           // base-2 normaliser, rounded; the rest of it is in ga, gb
+  float *ga;                             // factor of dz: u / T and the normaliser's part beyond fp32
+  float *lse2;                           // base-2 normaliser, rounded; the rest of it is in ga
   float *w;                              // per row: u (distillation)
   int32_t *flags;                        // per row: data-error bits (distillation)
   float *zt;                             // [.., T] logits of the targets
   float *pt;                             // [.., T] their probabilities (distillation)
   double *term;                          // loss terms
   float2 *part;                          // [column tiles][N] base-2 maximum and sum of exps
-  char *xs, *xt, *dz, *dzt, *wt;
-  float *acc;
+  char *xs;                              // rows with a loss
+  char *dz, *dzs;                        // a piece's dz, and times the rows' scales (8-bit rows; else the same)
+  char *wt;                              // a copied piece of the weight
+  float *acc;                            // sums of dx, per workgroup and tile
 };
 
 // ---------------------------------------------------------------- rows' inputs
@@ -214,7 +217,7 @@ template <int HT, int DT> __global__ __launch_bounds__(256) void stage_rows_kern
   if (at >= P.counts[1]) return;
   const int n = P.perm[at];
   const char *src = P.hidden + (int64_t)n * P.h_ld;
-  char *dst = P.xs + (int64_t)at * P.Kp * Mma<DT>::E;
+  char *dst = P.xs + (int64_t)at * P.x_ld;
   for (int k = threadIdx.x; k < (int)P.Kp; k += 256) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
   if (threadIdx.x == 0) P.alpha[at] = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
 }
@@ -230,7 +233,7 @@ template <int DT> __global__ __launch_bounds__(256) void targets_kernel(Head P) 
   float s = 0.f;
   if (id >= 0 && id < P.V) {
     constexpr int E = Mma<DT>::E, W = 16 / E;
-    const char *x = P.xs + (int64_t)at * P.Kp * E;
+    const char *x = P.xs + (int64_t)at * P.x_ld;
     const char *w = P.weight + (int64_t)id * P.w_ld;
     const bool vec = (((uintptr_t)P.weight | (uintptr_t)P.w_ld) & 15) == 0;
     const int nv = P.H / W;
@@ -261,8 +264,9 @@ struct Prod {
   int32_t M, N;                          // rows and columns of the result
   int32_t mt, nt, band, nk;
   int32_t tile0;                         // column tile of the row statistics at column 0
-  int64_t piece;                         // row length of dz
-  int32_t split, first, vec;
+  int32_t first, vec;
+  int32_t full;                          // steps of a whole piece (dx)
+  int32_t per0, groups, slots;           // dx: least steps of a workgroup, workgroups, tiles each may touch
 };
 
 // Forward tile: each row's maximum m (base 2) and sum of 2^(z log2 e - m) over
@@ -275,8 +279,8 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
   if (m0 >= M) return;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
-  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
-  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
+  const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+  const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
   product<DT, T>(acc, lds, X, Y, 0, G.nk);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   __syncthreads();                       // the tiles are done with: their LDS takes the waves' results
@@ -322,21 +326,21 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
 }
 
 // Backward tile of a piece: dz = u (2^(z log2 e - lse2)), rounded to the
-// operands' type, as rows (for dx) and transposed (for dW); zeros where the row
-// or the column does not exist, so that both can be summed in whole steps.
+// operands' type; zeros in the rows up to a whole step and in the columns up to a
+// whole tile, so that both gradients can sum whole steps.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   int im, in;
   tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
   const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[0];
-  constexpr int E = Mma<DT>::E;
-  const int Mp = (M + STEP / E - 1) / (STEP / E) * (STEP / E);
+  constexpr int Q = STEP / Mma<DT>::E;
+  const int Mp = (M + Q - 1) / Q * Q;
   if (m0 >= Mp) return;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
   if (m0 < M && n0 < G.N) {
-    const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
-    const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
+    const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+    const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
     product<DT, T>(acc, lds, X, Y, 0, G.nk);
   }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
@@ -344,22 +348,22 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   for (int f = 0; f < T::FM; ++f) {
     const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
     const bool on = m < M;
-    const float a = on ? P.alpha[m] : 0.f, l2 = on ? P.lse2[m] : 0.f;
-    const float ga = on ? P.ga[m] : 0.f, gb = on ? P.gb[m] : 0.f;
+    const float a = on ? P.alpha[m] : 0.f, l2 = on ? P.lse2[m] : 0.f, ga = on ? P.ga[m] : 0.f;
+    const float s = P.dzs != P.dz && on ? P.h_scale[P.perm[m]] : 0.f;
 #pragma unroll
     for (int g = 0; g < T::FN; ++g) {
       const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
-      float p[4], d[4];
+      float d[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2));
-        if (!(n + i < G.N) || ga == 0.f) p[i] = 0.f;
-        d[i] = p[i] * ga;
+        d[i] = __builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2)) * ga;
+        if (!(n + i < G.N) || ga == 0.f) d[i] = 0.f;
       }
-      if (on) store4<DT>(P.dz, (int64_t)m * G.piece + n, d);
-      if (P.dzt && m < Mp) {
+      if (m < Mp) store4<DT>(P.dz + m * P.dz_ld, n, d);
+      if (P.dzs != P.dz) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_real<DT>(P.dzt, (int64_t)(n + i) * P.Np + m, p[i] * gb);
+        for (int i = 0; i < 4; ++i) d[i] = ga == 0.f ? 0.f : d[i] * s;
+        if (m < Mp) store4<DT>(P.dzs + m * P.dz_ld, n, d);
       }
     }
   }
@@ -379,46 +383,105 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
   if (c < 0 || c >= G.N) return;
   if (P.T != 1 && !(P.tval[(int64_t)n * P.T + j] > NEG_INF)) return;   // padding: no target
   const float p = __builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at]));
-  // ga and gb hold the normaliser's part beyond fp32, which is p's alone
+  // ga holds the normaliser's part beyond fp32, which is p's alone
   const float u = (P.T == 1 ? (P.row_weight ? P.row_weight[n] : 1.f) : P.w[n] * P.pt[i]) * P.inv_t;
-  store_real<DT>(P.dz, (int64_t)at * G.piece + c, fmaf(p, ga, -u));
-  if (P.dzt) store_real<DT>(P.dzt, c * P.Np + at, fmaf(p, P.gb[at], -(P.h_scale ? u * P.h_scale[n] : u)));
+  store_real<DT>(P.dz + at * P.dz_ld, c, fmaf(p, ga, -u));
+  if (P.dzs != P.dz) store_real<DT>(P.dzs + at * P.dz_ld, c, fmaf(p, ga, -u) * P.h_scale[n]);
 }
 
-// dx of a piece: sums of the piece's parts, added to the earlier pieces' in fp32.
+// How a piece's dx is shared out: the steps of all tiles in one line, cut into
+// equal runs, one per workgroup, so that the chip is full whatever the number of
+// tiles.  A run touches a few tiles and adds its part of each to a sum of its own
+// (fp32, kept from piece to piece); a tile's sums are joined at the end.
+struct Share {
+  int nt, full, per;                     // column tiles, steps of a tile, steps of a run
+  __device__ __forceinline__ Share(const Prod &G, int M, int bm) {
+    nt = G.nt;
+    full = G.full;
+    const int64_t total = (int64_t)((M + bm - 1) / bm) * nt * full;
+    const int64_t p = (total + G.groups - 1) / G.groups;
+    per = (int)(p > G.per0 ? p : G.per0);
+  }
+  // the sum of run b for tile t
+  __device__ __forceinline__ int64_t slot(const Prod &G, int b, int64_t t) const {
+    return (int64_t)b * G.slots + (t - (int64_t)b * per / full);
+  }
+};
+
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
-  const int tiles = G.mt * G.nt, part = blockIdx.x / tiles;
-  int im, in;
-  tile_at(run_of_xcd(blockIdx.x - part * tiles, tiles), G.mt, G.nt, G.band, im, in);
-  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[0];
-  if (m0 >= M) return;
-  typename Mma<DT>::Acc acc[T::FM][T::FN];
-  clear<DT, T>(acc);
-  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
-  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
-  const int per = (G.nk + G.split - 1) / G.split, s0 = part * per;
-  const int ns = G.nk - s0 < per ? G.nk - s0 : per;
-  product<DT, T>(acc, lds, X, Y, s0 * STEP, ns > 0 ? ns : 0);
+  const int M = P.counts[0];
+  const Share S(G, M, T::BM);
+  const int mt = (M + T::BM - 1) / T::BM;
+  const int64_t total = (int64_t)mt * S.nt * S.full;
+  const int b = run_of_xcd(blockIdx.x, G.groups);
+  const int64_t at = (int64_t)b * S.per;
+  if (at >= total) return;
+  int left = __builtin_amdgcn_readfirstlane((int)(at + S.per < total ? S.per : total - at));
+  int t = __builtin_amdgcn_readfirstlane((int)(at / S.full)), s0 = __builtin_amdgcn_readfirstlane((int)(at % S.full));
+  float *out = P.acc + (int64_t)b * G.slots * (T::BM * T::BN) + threadIdx.x * 4;
+  for (; left > 0; ++t, s0 = 0, out += T::BM * T::BN) {
+    int ns = left < S.full - s0 ? left : S.full - s0;
+    left -= ns;
+    if (s0 + ns > G.nk) ns = G.nk - s0;  // a shorter last piece
+    if (ns <= 0) {
+      if (!G.first) continue;
+      ns = 0;                            // its sum starts at zero all the same
+    }
+    int im, in;
+    tile_at(t, mt, S.nt, G.band, im, in);
+    const int m0 = im * T::BM, n0 = in * T::BN;
+    typename Mma<DT>::Acc acc[T::FM][T::FN];
+    clear<DT, T>(acc);
+    const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
+    const Part Y = {G.y + (int64_t)n0 * Mma<DT>::E, G.y_ld, G.M, (P.Kp - n0) * Mma<DT>::E};
+    product<DT, T, false, true>(acc, lds, X, Y, s0, ns);
+#pragma unroll
+    for (int f = 0; f < T::FM; ++f)
+#pragma unroll
+      for (int g = 0; g < T::FN; ++g) {
+        f32x4 *o = (f32x4 *)(out + (f * T::FN + g) * (T::TPB * 4));
+        f32x4 v = acc[f][g];
+        if (!G.first) v += *o;
+        *o = v;
+      }
+    __syncthreads();                     // the tile's LDS is free for the next
+  }
+}
+
+// dx of every row: its tile's sums in order, rounded once; zeros for rows without a
+// gradient.  One workgroup per row tile and column tile of the product.
+template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_rows_kernel(Head P, Prod G) {
+  const int M = P.counts[0];
+  const int in = blockIdx.x % G.nt, im = blockIdx.x / G.nt, m0 = im * T::BM, n0 = in * T::BN;
+  const Share S(G, M, T::BM);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
-  float *out = P.acc + (int64_t)part * P.N * P.H;
+  int64_t t = 0;
+  int b0 = 0, b1 = -1;
+  if (m0 < M) {
+    const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
+    t = (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band);
+    b0 = (int)(t * S.full / S.per);
+    b1 = (int)(((t + 1) * S.full - 1) / S.per);
+  }
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
     const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
-    if (m >= M) continue;
+    if (m >= P.N) continue;
+    const bool on = m < M && P.ga[m] != 0.f;
+    const int64_t row = (int64_t)P.perm[m] * P.H;
 #pragma unroll
-    for (int g = 0; g < T::FN; ++g) {
-      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
-      float *o = out + (int64_t)m * P.H + n;
-      if (G.vec && n + 4 <= G.N) {
-        f32x4 v = acc[f][g];
-        if (!G.first) v += *(const f32x4 *)o;
-        *(f32x4 *)o = v;
-      } else {
-#pragma unroll
+    for (int q = 0; q < T::FN; ++q) {
+      const int n = n0 + (wn * T::FN + q) * 16 + (lane >> 4) * 4;
+      f32x4 v = 0;
+      if (on)
+        for (int b = b0; b <= b1; ++b)
+          v += *(const f32x4 *)(P.acc + S.slot(G, b, t) * (T::BM * T::BN) + (f * T::FN + q) * (T::TPB * 4) + threadIdx.x * 4);
+      const float d[4] = {v[0], v[1], v[2], v[3]};
+      if (G.vec && n + 4 <= P.H) store4<DT>(P.gh, row + n, d);
+      else
         for (int i = 0; i < 4; ++i)
-          if (n + i < G.N) o[i] = G.first ? acc[f][g][i] : o[i] + acc[f][g][i];
-      }
+          if (n + i < P.H) store_real<DT>(P.gh, row + n + i, d[i]);
     }
   }
 }
@@ -431,11 +494,11 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   const int m0 = im * T::BM, n0 = in * T::BN;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
-  constexpr int q = STEP / Mma<DT>::E;
-  const int nk = (P.counts[0] + q - 1) / q;
-  const Rows X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, G.M - m0 < T::BM ? G.M - m0 : T::BM, (int64_t)nk * STEP};
-  const Rows Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)nk * STEP};
-  product<DT, T>(acc, lds, X, Y, 0, nk);
+  constexpr int E = Mma<DT>::E, Q = STEP / E;
+  const int nk = (P.counts[0] + Q - 1) / Q;
+  const Part X = {G.x + (int64_t)m0 * E, G.x_ld, (int64_t)nk * Q, G.x_ld - (int64_t)m0 * E};
+  const Part Y = {G.y + (int64_t)n0 * E, G.y_ld, (int64_t)nk * Q, G.y_ld - (int64_t)n0 * E};
+  product<DT, T, true, true>(acc, lds, X, Y, 0, nk);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
 #pragma unroll
@@ -522,7 +585,6 @@ template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Hea
   if (P.grads) {
     const float c = F ? 0.f : u * (float)(1.0 - (l2 - (double)hi) * LN2) * P.inv_t;
     P.ga[at] = c;
-    P.gb[at] = (P.h_scale && !F) ? c * P.h_scale[n] : c;
   }
 }
 
@@ -570,58 +632,26 @@ __global__ __launch_bounds__(1024) void loss_kernel(Head P) {
   }
 }
 
-// dst[c][r] = src[r][c] for r < rows, zeros for rows .. pad-1: 64 x 64 blocks
-// through LDS.  limit: rows from counts[0] when not null, and rows whose gradient
-// factor is 0 (no gradient, or a data error: its values may be NaN) read as zeros.
-template <int DT> __global__ __launch_bounds__(256) void transpose_kernel(const char *src, int64_t s_ld, int rows,
-                                                                          int cols, char *dst, int64_t d_ld, int pad,
-                                                                          const int32_t *limit, const float *factor) {
-  typedef typename std::conditional<DT == SV_BF16, uint16_t, uint32_t>::type U;
-  __shared__ U t[64][65];
-  const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
-  if (limit) {
-    rows = *limit;
-    pad = (rows + STEP / (int)sizeof(U) - 1) / (STEP / (int)sizeof(U)) * (STEP / (int)sizeof(U));
-  }
-  if (r0 >= pad) return;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = r0 + y + i * 4, c = c0 + x;
-    U v = 0;
-    if (r < rows && c < cols && !(factor && factor[r] == 0.f)) v = *(const U *)(src + r * s_ld + (int64_t)c * sizeof(U));
-    t[y + i * 4][x] = v;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = c0 + y + i * 4, r = r0 + x;
-    if (c < cols && r < pad) *(U *)(dst + c * d_ld + (int64_t)r * sizeof(U)) = t[x][y + i * 4];
-  }
+// Rows that the sum of dW runs over without a term of their own: rows with a data
+// error (their values may be NaN) and those up to a whole step.
+template <int DT> __global__ __launch_bounds__(256) void clear_rows_kernel(Head P) {
+  constexpr int E = Mma<DT>::E, Q = STEP / E;
+  const int at = blockIdx.x, M = P.counts[0];
+  if (at >= (M + Q - 1) / Q * Q || (at < M && P.ga[at] != 0.f)) return;
+  u32x4 *x = (u32x4 *)(P.xs + (int64_t)at * P.x_ld);
+  for (int k = threadIdx.x; k < (int)(P.Kp * E / 16); k += 256) x[k] = 0;
 }
 
 // rows of the weight into rows of whole steps, zeros behind them
 template <int DT> __global__ __launch_bounds__(256) void copy_weight_kernel(const char *src, int64_t ld, int H, char *dst,
-                                                                            int64_t Kp) {
+                                                                            int64_t d_ld, int64_t Kp) {
   const char *s = src + (int64_t)blockIdx.x * ld;
-  char *d = dst + (int64_t)blockIdx.x * Kp * Mma<DT>::E;
+  char *d = dst + (int64_t)blockIdx.x * d_ld;
   for (int k = threadIdx.x; k < (int)Kp; k += 256) store_real<DT>(d, k, k < H ? load_real<DT>(s, k) : 0.f);
 }
 
-// dx of every row: its parts summed in order, rounded once; zeros without a gradient.
-template <int DT> __global__ __launch_bounds__(256) void dx_rows_kernel(Head P, int split) {
-  const int at = blockIdx.x;
-  const int64_t n = P.perm[at];
-  const bool on = at < P.counts[0] && P.ga[at] != 0.f;
-  for (int k = threadIdx.x; k < P.H; k += 256) {
-    float v = 0.f;
-    if (on)
-      for (int s = 0; s < split; ++s) v += P.acc[((int64_t)s * P.N + at) * P.H + k];
-    store_real<DT>(P.gh, n * P.H + k, v);
-  }
-}
-
 // ------------------------------------------------------------------------ host
+static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile<2, 2, 1, 4>::BM == 32, "plan_for's bm");
 typedef Tile<8, 4, 2, 4> Big;            // 256 x 256
 typedef Tile<4, 4, 2, 2> Mid;            // 128 x 128
 typedef Tile<2, 2, 1, 4> Few;            // 32 x 128
@@ -645,11 +675,10 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   else hipLaunchKernelGGL((stage_rows_kernel<DT, DT>), dim3(P.N), b256, 0, st, P);
   hipLaunchKernelGGL((targets_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 4)), b256, 0, st, P);
 
-  const int64_t row = L.Kp * E;
   Prod F = {};
   F.x = P.xs;
-  F.x_ld = row;
-  F.nk = (int32_t)(row / STEP);
+  F.x_ld = L.x_ld;
+  F.nk = (int32_t)(L.Kp * E / STEP);
   auto weight_piece = [&](Prod &G, int64_t v0, int64_t cnt) {
     G.v0 = v0;
     if (direct) {
@@ -657,9 +686,9 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
       G.y_ld = P.w_ld;
     } else {
       hipLaunchKernelGGL((copy_weight_kernel<DT>), dim3((unsigned)cnt), b256, 0, st, P.weight + v0 * P.w_ld, P.w_ld,
-                         P.H, P.wt, L.Kp);
+                         P.H, P.wt, L.x_ld, L.Kp);
       G.y = P.wt;
-      G.y_ld = row;
+      G.y_ld = L.x_ld;
     }
   };
   const int64_t fstep = direct ? P.V : L.piece;
@@ -684,45 +713,44 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   hipLaunchKernelGGL(loss_kernel, dim3(1), b1024, 0, st, P);
   if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 
-  if (P.gw)
-    hipLaunchKernelGGL((transpose_kernel<DT>), dim3((unsigned)cdiv(P.H, 64), (unsigned)cdiv(L.Np, 64)), b256, 0, st,
-                       P.xs, row, P.N, P.H, P.xt, L.Np * E, (int)L.Np, P.counts, P.ga);
+  if (P.gw) hipLaunchKernelGGL((clear_rows_kernel<DT>), dim3((unsigned)L.Np), b256, 0, st, P);
+  Prod X = tiled<T>(Prod{}, P.N, P.H);
+  X.x = P.dz;
+  X.x_ld = L.dz_ld;
+  X.full = (int32_t)(L.piece * E / STEP);
+  X.groups = L.groups;
+  X.slots = L.slots;
+  X.per0 = sv_head_host::RUN;
+  X.vec = P.H % 4 == 0 && ((uintptr_t)P.gh & 15) == 0;
   for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
     Prod G = tiled<T>(F, L.Np, cp);
     weight_piece(G, v0, cnt);
     G.N = (int32_t)cnt;
-    G.piece = L.piece;
     hipLaunchKernelGGL((dz_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
     hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 256)), b256, 0, st, P, G);
     if (P.gh) {
-      hipLaunchKernelGGL((transpose_kernel<DT>), dim3((unsigned)cdiv(P.H, 64), (unsigned)(cp / 64)), b256, 0, st,
-                         P.weight + v0 * P.w_ld, P.w_ld, (int)cnt, P.H, P.wt, L.piece * E, (int)cp,
-                         (const int32_t *)nullptr, (const float *)nullptr);
-      Prod X = tiled<T>(Prod{}, P.N, P.H);
-      X.x = P.dz;
-      X.x_ld = L.piece * E;
-      X.y = P.wt;
-      X.y_ld = L.piece * E;
-      X.nk = (int32_t)(cp * E / STEP);
-      X.split = L.split;
+      X.y = G.y;
+      X.y_ld = G.y_ld;
+      X.M = (int32_t)cnt;
+      X.nk = (int32_t)cdiv(cnt * E, STEP);
       X.first = v0 == 0;
-      X.vec = P.H % 4 == 0;
-      hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt * L.split)), dim3(T::TPB), 0, st, P, X);
+      hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)L.groups), dim3(T::TPB), 0, st, P, X);
     }
     if (P.gw) {
       Prod W = tiled<TW>(Prod{}, cnt, P.H);
       W.v0 = v0;
-      W.x = P.dzt;
-      W.x_ld = L.Np * E;
-      W.y = P.xt;
-      W.y_ld = L.Np * E;
+      W.x = P.dzs;
+      W.x_ld = L.dz_ld;
+      W.y = P.xs;
+      W.y_ld = L.x_ld;
       W.vec = P.H % 4 == 0 && ((uintptr_t)P.gw & 15) == 0;
       hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
     }
   }
-  if (P.gh) hipLaunchKernelGGL((dx_rows_kernel<DT>), dim3(P.N), b256, 0, st, P, L.split);
+  if (P.gh)
+    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt)), dim3(T::TPB), 0, st, P, X);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
@@ -739,6 +767,8 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.ignore = s.ignore_index;
   P.inv_t = 1.f / s.temperature;
   P.Kp = L.Kp;
+  P.x_ld = L.x_ld;
+  P.dz_ld = L.dz_ld;
   P.Np = L.Np;
   P.hidden = (const char *)hidden;
   P.h_ld = (s.hidden_stride ? s.hidden_stride : s.H) * (int64_t)he;
@@ -751,7 +781,6 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.perm = (int32_t *)(ws + L.perm);
   P.alpha = (float *)(ws + L.alpha);
   P.ga = (float *)(ws + L.ga);
-  P.gb = (float *)(ws + L.gb);
   P.lse2 = (float *)(ws + L.lse2);
   P.w = (float *)(ws + L.w);
   P.flags = (int32_t *)(ws + L.flags);
@@ -760,21 +789,20 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.term = (double *)(ws + L.term);
   P.part = (float2 *)(ws + L.part);
   P.xs = ws + L.xs;
-  P.xt = ws + L.xt;
   P.dz = ws + L.dz;
-  P.dzt = P.gw ? ws + L.dzt : nullptr;
+  P.dzs = P.h_scale && P.gw ? ws + L.dzs : P.dz;
   P.wt = ws + L.wt;
   P.acc = (float *)(ws + L.acc);
   const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
   // tiles by the number of rows: 256 rows a tile read each operand least; fewer
-  // rows than a tile would be multiplied in vain
+  // rows than a tile would be multiplied in vain.  fp32 holds two sets of sums,
+  // and its matrix rate leaves time to read 128-row tiles
   if (s.dtype == SV_BF16)
-    return s.N >= 192 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
-           : s.N > 32 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
-                      : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
-  return s.N >= 192 ? enqueue<SV_F32, Big, Big>(P, L, kd, direct, st)
-         : s.N > 32 ? enqueue<SV_F32, Mid, Mid>(P, L, kd, direct, st)
-                    : enqueue<SV_F32, Few, Mid>(P, L, kd, direct, st);
+    return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
+           : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
+                         : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
+  return L.bm == 128 ? enqueue<SV_F32, Mid, Mid>(P, L, kd, direct, st)
+                     : enqueue<SV_F32, Few, Mid>(P, L, kd, direct, st);
 }
 
 }  // namespace

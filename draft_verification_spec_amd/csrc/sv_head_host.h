@@ -14,9 +14,15 @@ namespace sv_head_host {
 
 constexpr int TOP = 32;                  // stored entries per row (sv_head_kd)
 constexpr int STEP = 128;                // bytes of k per step of the tiled product
+constexpr int CUS = 256;                 // compute units of the GPU
+constexpr int RUN = 8;                   // least steps of a workgroup of the hidden gradient
 constexpr int64_t MAX_LD = (int64_t)1 << 22;   // bytes between rows of a tiled operand: a tile's offsets fit 31 bits
 
+inline int64_t cdiv(int64_t x, int64_t m);
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+// bytes between rows of n bytes: an odd number of 128-byte lines, so that rows
+// spread over the L2's channels
+inline int64_t spread(int64_t n) { return (cdiv(n, 128) | 1) * 128; }
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 inline int esize(int dtype) { return dtype == SV_F32 ? 4 : dtype == SV_BF16 ? 2 : 1; }
 inline bool real_dtype(int dt) { return dt == SV_F32 || dt == SV_BF16; }
@@ -85,9 +91,11 @@ struct Plan {
   int64_t Kp;                            // hidden width in whole steps, elements
   int64_t Np;                            // rows in whole steps, elements
   int64_t piece, pieces;                 // vocabulary entries per piece, pieces
-  int split;                             // parts of a piece's length in the hidden gradient
+  int64_t x_ld, dz_ld;                   // bytes between copied rows (of hidden and weight), rows of dz
+  int bm, bn;                            // tile of the products
+  int groups, slots;                     // workgroups of the hidden gradient, tiles each may touch
   // workspace sections
-  size_t counts, perm, alpha, ga, gb, lse2, w, flags, zt, pt, term, part, xs, xt, dz, dzt, wt, acc, total;
+  size_t counts, perm, alpha, ga, lse2, w, flags, zt, pt, term, part, xs, dz, dzs, wt, acc, total;
 };
 
 inline bool head_shape_ok(const sv_head_shape_t *s, bool kd) {
@@ -116,31 +124,34 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   const int64_t N = s->N, H = s->H, T = kd ? TOP : 1;
   p.Kp = up(H, q);
   p.Np = up(N, q);
-  // A piece: its dz (twice, also transposed) and its transposed weight are written
-  // and read back, so it is kept near 512 MB; a whole number of 256 entries,
-  // all pieces alike.
-  const int64_t per = (s->grads ? p.Np * e * 2 : 0) + p.Kp * e;
-  int64_t most = ((int64_t)512 << 20) / per / 256 * 256;
+  p.bm = N <= 32 ? 32 : (N < 192 || s->dtype == SV_F32) ? 128 : 256;
+  p.bn = p.bm == 256 ? 256 : 128;
+  // A piece: its dz is written and read back twice, and a copied weight once, so
+  // both are kept near 256 MB together, the size of the Infinity Cache; a whole
+  // number of 256 entries, all pieces alike.
+  const int64_t per = (s->grads ? p.Np * e : 0) + p.Kp * e;
+  int64_t most = ((int64_t)256 << 20) / per / 256 * 256;
   if (most < 256) most = 256;
-  const int64_t by_ld = MAX_LD / e / 2;
+  const int64_t by_ld = MAX_LD / e / 2;          // (and a line more)
   if (most > by_ld) most = by_ld;
   p.pieces = cdiv(s->V, most);
   p.piece = up(cdiv(s->V, p.pieces), 256);
   p.pieces = cdiv(s->V, p.piece);
-  // the hidden gradient has N x H results and a piece's length to sum: split it
-  // until about two workgroups a CU have work, 1024 entries a part at least
-  const int64_t tiles = cdiv(N, N >= 192 ? 256 : N > 32 ? 128 : 32) * cdiv(H, N >= 192 ? 256 : 128);
-  int64_t sp = tiles > 0 ? 512 / tiles : 1;
-  if (sp > p.piece / 1024) sp = p.piece / 1024;
-  p.split = (int)(sp < 1 ? 1 : sp);
-  const bool gh = s->grads & SV_GRAD_HIDDEN, gw = s->grads & SV_GRAD_WEIGHT, g = gh || gw;
+  // the hidden gradient's workgroups: as many as run at once (LDS: one tile of
+  // 256, two of 128, four of 32 rows a CU), fewer where a run would be short
+  const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), full = p.piece * e / STEP;
+  int64_t g = CUS * (p.bm == 256 ? 1 : p.bm == 128 ? 2 : 4);
+  if (g > cdiv(tiles * full, RUN)) g = cdiv(tiles * full, RUN);
+  p.groups = (int)(g < 1 ? 1 : g);
+  const int64_t run = cdiv(tiles * full, p.groups);
+  p.slots = (int)(cdiv(run > RUN ? run : RUN, full) + 1);
+  const bool gh = s->grads & SV_GRAD_HIDDEN, gw = s->grads & SV_GRAD_WEIGHT;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) & ~(size_t)255; return at; };
   p.counts = take(256);
   p.perm = take(N * 4);
   p.alpha = take(N * 4);
   p.ga = take(N * 4);
-  p.gb = take(N * 4);
   p.lse2 = take(N * 4);
   p.w = take(N * 4);
   p.flags = take(N * 4);
@@ -148,13 +159,13 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.pt = take(kd ? N * T * 4 : 0);
   p.term = take(N * 8);
   p.part = take((size_t)cdiv(s->V, 128) * N * 8);
-  p.xs = take((size_t)N * p.Kp * e);
-  p.xt = take(gw ? (size_t)H * p.Np * e : 0);
-  p.dz = take(g ? (size_t)N * p.piece * e : 0);
-  p.dzt = take(gw ? (size_t)p.piece * p.Np * e : 0);
-  // a copied piece of the weight, and later the transposed one, in one place
-  p.wt = take((size_t)p.piece * p.Kp * e);
-  p.acc = take(gh ? (size_t)p.split * N * H * 4 : 0);
+  p.x_ld = spread(p.Kp * e);
+  p.dz_ld = spread(p.piece * e);
+  p.xs = take((size_t)p.Np * p.x_ld);
+  p.dz = take(gh || gw ? (size_t)p.Np * p.dz_ld : 0);
+  p.dzs = take(gw && s->hidden_dtype == SV_I8 ? (size_t)p.Np * p.dz_ld : 0);
+  p.wt = take((size_t)p.piece * p.x_ld);
+  p.acc = take(gh ? (size_t)p.groups * p.slots * p.bm * p.bn * 4 : 0);
   p.total = o;
   return p;
 }

@@ -77,8 +77,8 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void logits_kern
   const int m0 = im * T::BM, n0 = in * T::BN;
   i32x4 acc[T::FM][T::FN];
   clear<SV_I8, T>(acc);
-  const Rows X = {P.x + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, (int64_t)P.nk * STEP};
-  const Rows Y = {P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
+  const Part X = {P.x + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, (int64_t)P.nk * STEP};
+  const Part Y = {P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
   product<SV_I8, T>(acc, lds, X, Y, 0, P.nk);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
 #pragma unroll
