@@ -23,11 +23,14 @@
 // A direct load writes 64 consecutive 16-byte pieces, so pieces are permuted on
 // the memory side to keep LDS reads off each other's banks.  Rows: piece p of row
 // r lies at place p ^ (r & 7), and the 8 rows read together hit 8 places.
-// Columns: the 16 columns of a fragment move together, by two bits of the row
-// index that tell apart the rows read together; bf16 columns are turned into
-// pieces of k by the transposing LDS read, fp32 ones are read element by element.
+// Columns: a lane reads, for each of its k, the neighbouring columns that its F
+// fragments hold (fragment f's index i is column i F + f), and bf16 pairs of k are
+// put together by byte permutes; the parts of k read together are turned against
+// each other.  (The LDS read that transposes by itself does not serve: the compiler
+// lets it wait for every load into LDS, those for later steps among them; dW ran
+// at 1.0 PFLOP/s with it, measured at 2048 x 4096 x 65536.)
 // The columns' fragment is the instruction's first operand: a lane then holds
-// four consecutive n of one m, which row-major stores want.
+// four n of one m; index_of tells which.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -96,25 +99,32 @@ struct Part {
 };
 
 #ifdef __HIP_DEVICE_COMPILE__            // (the host pass knows no gfx950 builtins)
-// Loads and reads of one operand's tile: R indices (m or n), COL: k down columns.
-template <int DT, int R, int NW, bool COL> struct Side {
+// Loads and reads of one operand's tile: R indices (m or n), F fragments a wave,
+// COL: k down columns.
+template <int DT, int R, int F, int NW, bool COL> struct Side {
   static constexpr int E = Mma<DT>::E, KR = STEP / E;    // k a step
   static constexpr int NL = R / 8 / NW;                  // 16-byte loads a thread and step
   static_assert(NL >= 1 && NL < 16 && R % (8 * NW) == 0, "tile of whole loads");
   static constexpr int PR = COL ? R * E / 16 : 8;        // pieces of an LDS row
-  static constexpr int GP = E;                           // pieces of 16 columns
-  static constexpr int MASK = R / 16 - 1 < 3 ? R / 16 - 1 : 3;
+  // columns: k of a lane's 16 bytes, bytes that 16 lanes read of one k, and how
+  // many such parts are read together
+  static constexpr int KL = 16 / E, SPAN = 16 * F * E, PARTS = SPAN >= 256 ? 1 : 256 / SPAN;
+  static_assert(!COL || (E > 1 && (F == 2 || F == 4 || F == 8)), "whole reads of columns");
   typedef __attribute__((address_space(3))) void lds_void;
 
   __amdgpu_buffer_rsrc_t rsrc;
   const char *base;
   int64_t ld, left, bytes;
-  int off[NL];                                           // rows: the byte offset; columns: of the piece in its row
+  int off[NL];                                           // a load's byte offset from its step
   int wid;
 
-  // two bits of k's index that differ between rows read together
-  static __device__ __forceinline__ int turn(int r) { return (DT == SV_BF16 ? r : r >> 2) & MASK; }
-  static __device__ __forceinline__ int row_of(int wid, int j) { return ((wid + j * NW) * 64 + (threadIdx.x & 63)) / PR; }
+  // the byte in its row that LDS piece q of k r holds
+  static __device__ __forceinline__ int piece(int q, int r) { return q * 16 ^ (r / KL & (PARTS - 1)) * SPAN; }
+  // steps from s0 whose k all exist
+  __device__ __forceinline__ int whole(int nk) const {
+    if constexpr (COL) return left / KR < nk ? (int)(left / KR) : nk;
+    else return nk;
+  }
 
   int pos;                                               // rows: the next step's byte
 
@@ -135,20 +145,25 @@ template <int DT, int R, int NW, bool COL> struct Side {
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
       const int c = (wid + j * NW) * 64 + (threadIdx.x & 63), r = c / PR, q = c % PR;
-      if constexpr (COL) off[j] = (((q / GP) ^ turn(r)) * GP + q % GP) * 16;
+      if constexpr (COL) off[j] = r * (int)ld + piece(q, r);
       else off[j] = (int)((r < left ? r : left - 1) * ld) + (q ^ (r & 7)) * 16;
     }
   }
-  // the next step's loads
-  __device__ __forceinline__ void issue(char *buf) {
+  // the next step's loads; all: every k of it exists
+  __device__ __forceinline__ void issue(char *buf, bool all) {
     if constexpr (COL) {
-      const int have = left < KR ? (int)left : KR;
+      const int have = all || left >= KR ? KR : (int)left;
       rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)((have - 1) * ld + bytes), 0x00020000);
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const int r = row_of(wid, j);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(buf + (wid + j * NW) * 1024), 16,
-                                                 (r < have ? r : have - 1) * (int)ld + off[j], 0, 0, 0);
+        int o = off[j];
+        if (!all) {
+          int c = (wid + j * NW) * 64 + (threadIdx.x & 63);
+          asm volatile("" : "+v"(c));    // (formed again in the few steps that need it, not held)
+          const int r = c / PR;
+          if (r >= have) o -= (r - (have - 1)) * (int)ld;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(buf + (wid + j * NW) * 1024), 16, o, 0, 0, 0);
       }
       base += KR * ld;
       left -= KR;
@@ -159,41 +174,53 @@ template <int DT, int R, int NW, bool COL> struct Side {
       pos += STEP;
     }
   }
-  template <int F> static constexpr int reads() { return !COL ? F : DT == SV_BF16 ? 2 * F : 4 * F; }
-  // (g0 + f) ^ t; in fours the exclusive or stays within them, and the lanes' part
-  // of it is the same for every four
-  template <int F> static __device__ __forceinline__ int place(int g0, int f, int t) {
-    if constexpr (F % 4 == 0) return g0 + (f & ~3) + ((f & 3) ^ t);
-    else return (g0 + f) ^ t;
-  }
-  // fragments g0 .. g0 + F - 1 (of 16 indices) of half step h
-  template <int F> static __device__ __forceinline__ void read(u32x4 (&v)[F], const char *buf, int g0, int h) {
+  static constexpr int READS = COL ? KL : F;
+  // what the wave's fragments g0 .. g0 + F - 1 (of 16 indices) of half step h hold,
+  // for columns in the order of k
+  static __device__ __forceinline__ void read(u32x4 (&v)[F], const char *buf, int g0, int h) {
     const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
     if constexpr (!COL) {
       const char *at = buf + g0 * 16 * STEP + i * STEP + (((h * 4 + q) ^ (lane & 7)) << 4);
 #pragma unroll
       for (int f = 0; f < F; ++f) v[f] = *(const u32x4 *)(at + f * 16 * STEP);
-    } else if constexpr (DT == SV_BF16) {
-      typedef short s16x4 __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const char *at = buf + (h * 32 + q * 8 + (i >> 2)) * (R * E) + (i & 3) * 8;
-      const int t = turn(i >> 2);
-#pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const char *p = at + place<F>(g0, f, t) * 32;
-        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
-        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * R * E)));
-        v[f] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-      }
     } else {
-      const char *at = buf + (h * 16 + q * 4) * (R * E) + i * 4;
-      const int t = turn(q * 4);
+      constexpr int B = F * E;                           // bytes a lane reads of one k
+      const char *at = buf + (h * 4 + q) * KL * (R * E) + ((g0 * 16 * E + i * B) ^ (q & (PARTS - 1)) * SPAN);
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const char *p = at + place<F>(g0, f, t) * 64;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[f][e] = *(const uint32_t *)(p + e * (R * E));
+      for (int e = 0; e < KL; ++e) {
+        const char *p = at + e * (R * E);
+        if constexpr (B == 16) {
+          v[e] = *(const u32x4 *)p;
+        } else if constexpr (B == 8) {
+          const u32x2 w = *(const u32x2 *)p;
+          v[e / 2][e % 2 * 2] = w[0];
+          v[e / 2][e % 2 * 2 + 1] = w[1];
+        } else {
+          v[e / 4][e % 4] = *(const uint32_t *)p;
+        }
       }
+    }
+  }
+  // fragments from what was read
+  static __device__ __forceinline__ void finish(u32x4 (&v)[F]) {
+    if constexpr (COL) {
+      constexpr int WORDS = F * E / 4;                   // words read of one k
+      u32x4 o[F];
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if constexpr (DT == SV_BF16) {
+            const uint32_t a = v[(2 * d * WORDS + w) >> 2][(2 * d * WORDS + w) & 3];
+            const uint32_t b = v[((2 * d + 1) * WORDS + w) >> 2][((2 * d + 1) * WORDS + w) & 3];
+            o[2 * w][d] = __builtin_amdgcn_perm(b, a, 0x05040100);
+            o[2 * w + 1][d] = __builtin_amdgcn_perm(b, a, 0x07060302);
+          } else {
+            o[w][d] = v[(d * WORDS + w) >> 2][(d * WORDS + w) & 3];
+          }
+        }
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[f] = o[f];
     }
   }
 };
@@ -219,8 +246,8 @@ template <int DT, class T, bool XC = false, bool YC = false>
 __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::FN], char *lds, const Part &X,
                                         const Part &Y, int s0, int nk) {
 #ifdef __HIP_DEVICE_COMPILE__
-  typedef Side<DT, T::BM, T::NW, XC> SX;
-  typedef Side<DT, T::BN, T::NW, YC> SY;
+  typedef Side<DT, T::BM, T::FM, T::NW, XC> SX;
+  typedef Side<DT, T::BN, T::FN, T::NW, YC> SY;
   if (nk <= 0) return;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int gx = wid / T::WN * T::FM, gy = wid % T::WN * T::FN;
@@ -246,32 +273,35 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
   };
   typedef typename Mma<DT>::Acc Acc;
   auto mul = [&](Acc (&c)[T::FM][T::FN], u32x4 (&x)[T::FM], u32x4 (&y)[T::FN]) {
+    SX::finish(x);
+    SY::finish(y);
 #pragma unroll
     for (int f = 0; f < T::FM; ++f)
 #pragma unroll
       for (int g = 0; g < T::FN; ++g) Mma<DT>::mul(c[f][g], y[g], x[f]);
   };
-  sx.issue(lds);
-  sy.issue(yl);
-  if (nk > 1) sy.issue(yl + T::YBUF);
+  const int wx = sx.whole(nk), wy = sy.whole(nk), full = wx < wy ? wx : wy;
+  sx.issue(lds, false);
+  sy.issue(yl, false);
+  if (nk > 1) sy.issue(yl + T::YBUF, false);
   landed(nk > 1);
-  if (nk > 1) sx.issue(lds + T::XBUF);
-  if (nk > 2) sy.issue(yl + 2 * T::YBUF);
+  if (nk > 1) sx.issue(lds + T::XBUF, false);
+  if (nk > 2) sy.issue(yl + 2 * T::YBUF, false);
   read(x0, y0, 0, 0, 0);
   int yb = 0;                                            // the columns' buffer of this step
   // One step.  Loads and LDS reads are spread between the matrix instructions: a
   // wave issues in order, and eight waves that all ask for their fragments first
   // keep the matrix units waiting for the LDS.
   constexpr int MM = T::FM * T::FN * (DT == SV_F32 ? 4 : 1);
-  constexpr int RD = SX::template reads<T::FM>() + SY::template reads<T::FN>(), LD = SX::NL + SY::NL;
+  constexpr int RD = SX::READS + SY::READS, LD = SX::NL + SY::NL;
   auto step = [&](int s, Acc (&c)[T::FM][T::FN], auto whole) {
-    constexpr bool W = decltype(whole)::value;           // three more steps follow
+    constexpr bool W = decltype(whole)::value;           // three more whole steps follow
     read(x1, y1, s, yb, 1);
     mul(c, x0, y0);
     mix<MM, RD, 0>();
     landed(W || s + 2 < nk);
-    if (W || s + 2 < nk) sx.issue(lds + (s & 1) * T::XBUF);
-    if (W || s + 3 < nk) sy.issue(yl + yb * T::YBUF);
+    if (W || s + 2 < nk) sx.issue(lds + (s & 1) * T::XBUF, W);
+    if (W || s + 3 < nk) sy.issue(yl + yb * T::YBUF, W);
     yb = yb == 2 ? 0 : yb + 1;
     if (W || s + 1 < nk) read(x0, y0, s + 1, yb, 0);
     mul(c, x1, y1);
@@ -296,9 +326,14 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
     }
   };
   int s = 0;
-  for (; s + 3 < nk; ++s) sum(s, std::true_type());
+  for (; s + 3 < full; ++s) sum(s, std::true_type());
   for (; s < nk; ++s) sum(s, std::false_type());
 #endif
+}
+
+// The index in its tile of a fragment's index i (0 .. 15) of wave w.
+template <int F, bool COL> __device__ __forceinline__ int index_of(int w, int f, int i) {
+  return COL ? (w * 16 + i) * F + f : (w * F + f) * 16 + i;
 }
 
 template <int DT, class T>

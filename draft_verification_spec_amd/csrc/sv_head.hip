@@ -58,6 +58,24 @@ template <int DT> __device__ __forceinline__ void store4(char *p, int64_t i, con
   else *(f32x4 *)(p + i * 4) = f32x4{v[0], v[1], v[2], v[3]};
 }
 
+// A lane's results of a row where the columns' operand lies k down its columns: F
+// fragments hold 4 F neighbouring columns from n (index_of), v[g][i] column n + i F + g.
+template <int DT, int F>
+__device__ __forceinline__ void store_columns(char *p, int64_t row, int n, int N, bool vec, const f32x4 (&v)[F]) {
+#pragma unroll
+  for (int q = 0; q < F; ++q) {
+    float d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = v[(4 * q + i) % F][(4 * q + i) / F];
+    const int c = n + 4 * q;
+    if (vec && c + 4 <= N) store4<DT>(p, row + c, d);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < N) store_real<DT>(p, row + c + i, d[i]);
+  }
+}
+
 // What the kernels share: the call's arrays and the workspace.
 struct Head {
   int32_t N, H, V, T;                    // T: targets per row
@@ -466,23 +484,20 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_rows_ker
   }
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
-    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    const int m = m0 + index_of<T::FM, false>(wm, f, lane & 15);
     if (m >= P.N) continue;
     const bool on = m < M && P.ga[m] != 0.f;
     const int64_t row = (int64_t)P.perm[m] * P.H;
+    f32x4 v[T::FN];
 #pragma unroll
-    for (int q = 0; q < T::FN; ++q) {
-      const int n = n0 + (wn * T::FN + q) * 16 + (lane >> 4) * 4;
-      f32x4 v = 0;
-      if (on)
-        for (int b = b0; b <= b1; ++b)
-          v += *(const f32x4 *)(P.acc + S.slot(G, b, t) * (T::BM * T::BN) + (f * T::FN + q) * (T::TPB * 4) + threadIdx.x * 4);
-      const float d[4] = {v[0], v[1], v[2], v[3]};
-      if (G.vec && n + 4 <= P.H) store4<DT>(P.gh, row + n, d);
-      else
-        for (int i = 0; i < 4; ++i)
-          if (n + i < P.H) store_real<DT>(P.gh, row + n + i, d[i]);
-    }
+    for (int q = 0; q < T::FN; ++q) v[q] = 0;
+    if (on)
+      for (int b = b0; b <= b1; ++b) {
+        const float *s = P.acc + S.slot(G, b, t) * (T::BM * T::BN) + threadIdx.x * 4;
+#pragma unroll
+        for (int q = 0; q < T::FN; ++q) v[q] += *(const f32x4 *)(s + (f * T::FN + q) * (T::TPB * 4));
+      }
+    store_columns<DT, T::FN>(P.gh, row, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec, v);
   }
 }
 
@@ -503,23 +518,12 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
-    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    const int m = m0 + index_of<T::FM, true>(wm, f, lane & 15);
     if (m >= G.M) continue;
+    f32x4 v[T::FN];
 #pragma unroll
-    for (int g = 0; g < T::FN; ++g) {
-      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
-      const int64_t o = (int64_t)m * P.H + n;
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = acc[f][g][i];
-      if (G.vec && n + 4 <= G.N) {
-        store4<DT>(out, o, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < G.N) store_real<DT>(out, o + i, v[i]);
-      }
-    }
+    for (int g = 0; g < T::FN; ++g) v[g] = acc[f][g];
+    store_columns<DT, T::FN>(out, (int64_t)m * P.H, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec, v);
   }
 }
 
