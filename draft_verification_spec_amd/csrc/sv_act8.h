@@ -57,9 +57,53 @@ struct Pack {
   int32_t vec;                           // 16-byte aligned x rows, codes rows aligned for their stores
 };
 
-// One workgroup per row: the largest magnitude (its bit pattern, as an integer
-// maximum, keeps NaN and infinity above every number), then the codes.  HBM
-// bound: the row is read twice, the second time from the caches.
+// The largest magnitude (its bit pattern, as an integer maximum, keeps NaN and
+// infinity above every number), then the codes.  HBM bound.  A wave takes a row and
+// holds it in registers, REGS 16-byte vectors a lane, so it is read once; rows too
+// long for that, or not aligned, take a workgroup and a second read from the caches.
+template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_kernel(Pack P, int N) {
+  constexpr int E = In<DT>::E, W = 16 / E;
+  const int lane = threadIdx.x & 63;
+  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (n >= N) return;
+  const char *x = P.x + n * P.x_ld;
+  int8_t *c = P.codes + n * P.c_ld;
+  const int nv = P.H / W;                // (a whole number of vectors)
+  u32x4 v[REGS];
+  uint32_t top = 0;
+#pragma unroll
+  for (int r = 0; r < REGS; ++r) {
+    v[r] = 0;
+    if (r * 64 + lane < nv) v[r] = __builtin_nontemporal_load((const u32x4 *)x + r * 64 + lane);
+  }
+#pragma unroll
+  for (int r = 0; r < REGS; ++r)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t u = __float_as_uint(In<DT>::of(v[r], i)) & 0x7fffffffu;
+      top = u > top ? u : top;
+    }
+  const float s = scale_of((uint32_t)sv_dev::wave_max_i((int)top));
+  if (lane == 0) P.scale[n] = s;
+  const bool none = !(s > 0.f);          // a row of zeros, of magnitudes whose scale rounds to 0, or NaN
+#pragma unroll
+  for (int r = 0; r < REGS; ++r) {
+    const int q = r * 64 + lane;
+    if (q >= nv) continue;
+    uint32_t o[W / 4];
+#pragma unroll
+    for (int w = 0; w < W / 4; ++w) {
+      o[w] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!none) o[w] |= (uint32_t)(code_of(In<DT>::of(v[r], 4 * w + i), s) & 0xff) << (8 * i);
+    }
+    if constexpr (W == 8) *(uint64_t *)(c + (int64_t)q * 8) = ((uint64_t)o[1] << 32) | o[0];
+    else *(uint32_t *)(c + (int64_t)q * 4) = o[0];
+  }
+  for (int i = P.H + lane; i < P.Hp; i += 64) c[i] = 0;
+}
+
 template <int DT> __global__ __launch_bounds__(256) void pack_kernel(Pack P) {
   constexpr int E = In<DT>::E, W = 16 / E;
   __shared__ uint32_t top_of[4];
@@ -112,11 +156,20 @@ inline bool pack_vec(int E, const void *x, int64_t x_ld, const void *c, int64_t 
   return ((uintptr_t)x & 15) == 0 && (x_ld & 15) == 0 && ((uintptr_t)c & (st - 1)) == 0 && (c_ld & (st - 1)) == 0;
 }
 
-inline void pack(int dtype, int N, Pack P, hipStream_t st) {
-  const int E = dtype == SV_BF16 ? 2 : 4;
+template <int DT> void pack_as(int N, Pack P, hipStream_t st) {
+  constexpr int E = In<DT>::E, W = 16 / E;
   P.vec = pack_vec(E, P.x, P.x_ld, P.codes, P.c_ld) ? 1 : 0;
-  if (dtype == SV_BF16) hipLaunchKernelGGL((pack_kernel<SV_BF16>), dim3(N), dim3(256), 0, st, P);
-  else hipLaunchKernelGGL((pack_kernel<SV_F32>), dim3(N), dim3(256), 0, st, P);
+  const dim3 rows((unsigned)((N + 3) / 4)), block(256);
+  const int regs = P.H / W / 64 + (P.H % (W * 64) != 0);
+  if (P.vec && P.H % W == 0 && regs <= 4) hipLaunchKernelGGL((pack_rows_kernel<DT, 4>), rows, block, 0, st, P, N);
+  else if (P.vec && P.H % W == 0 && regs <= 16)
+    hipLaunchKernelGGL((pack_rows_kernel<DT, 16>), rows, block, 0, st, P, N);
+  else hipLaunchKernelGGL((pack_kernel<DT>), dim3(N), block, 0, st, P);
+}
+
+inline void pack(int dtype, int N, const Pack &P, hipStream_t st) {
+  if (dtype == SV_BF16) pack_as<SV_BF16>(N, P, st);
+  else pack_as<SV_F32>(N, P, st);
 }
 
 }  // namespace sv_act8

@@ -240,14 +240,14 @@ template <int HT, int DT> __global__ __launch_bounds__(256) void stage_rows_kern
   if (threadIdx.x == 0) P.alpha[at] = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
 }
 
-// z of the targets: one wave per (row, target), fp32 sums.
+// z of the stored entries: one wave per (row, entry), fp32 sums.
 template <int DT> __global__ __launch_bounds__(256) void targets_kernel(Head P) {
   const int lane = threadIdx.x & 63;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int at = (int)(i / P.T), j = (int)(i - (int64_t)at * P.T);
   if (at >= P.counts[1]) return;
   const int n = P.perm[at];
-  const int id = P.T == 1 ? P.targets[n] : P.tidx[(int64_t)n * P.T + j];
+  const int id = P.tidx[(int64_t)n * P.T + j];
   float s = 0.f;
   if (id >= 0 && id < P.V) {
     constexpr int E = Mma<DT>::E, W = 16 / E;
@@ -291,10 +291,11 @@ struct Prod {
 // the tile's columns.  A NaN makes both NaN, +inf alone only the sum.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
-  int im, in;
-  tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
-  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[1];
-  if (m0 >= M) return;
+  const int M = P.counts[1], mt = (M + T::BM - 1) / T::BM;
+  if ((int)blockIdx.x >= mt * G.nt) return;
+  int im, in;                            // (over the rows there are: each XCD gets its share of them)
+  tile_at(run_of_xcd(blockIdx.x, mt * G.nt), mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
   const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
@@ -307,6 +308,8 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
   for (int f = 0; f < T::FM; ++f) {
     const int r = (wm * T::FM + f) * 16 + (lane & 15);
     const float a = m0 + r < M ? P.alpha[m0 + r] : 0.f;
+    // cross entropy: the target's own z, where it lies in this tile
+    const int64_t t = P.T == 1 && m0 + r < M ? P.targets[P.perm[m0 + r]] - G.v0 : -1;
     float m = NEG_INF;
 #pragma unroll
     for (int g = 0; g < T::FN; ++g)
@@ -315,6 +318,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
         const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4 + i;
         const float z = n < G.N ? acc[f][g][i] * a : NEG_INF;
         acc[f][g][i] = z;
+        if (n == t) P.zt[m0 + r] = z;
         m = sv_dev::fmax_nan(m, z);
       }
     m = sv_dev::fmax_nan(m, __shfl_xor(m, 16));
@@ -348,12 +352,12 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
 // whole tile, so that both gradients can sum whole steps.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
-  int im, in;
-  tile_at(run_of_xcd(blockIdx.x, G.mt * G.nt), G.mt, G.nt, G.band, im, in);
-  const int m0 = im * T::BM, n0 = in * T::BN, M = P.counts[0];
   constexpr int Q = STEP / Mma<DT>::E;
-  const int Mp = (M + Q - 1) / Q * Q;
-  if (m0 >= Mp) return;
+  const int M = P.counts[0], Mp = (M + Q - 1) / Q * Q, mt = (Mp + T::BM - 1) / T::BM;
+  if ((int)blockIdx.x >= mt * G.nt) return;
+  int im, in;
+  tile_at(run_of_xcd(blockIdx.x, mt * G.nt), mt, G.nt, G.band, im, in);
+  const int m0 = im * T::BM, n0 = in * T::BN;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
   if (m0 < M && n0 < G.N) {
@@ -367,14 +371,18 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
     const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
     const bool on = m < M;
     const float a = on ? P.alpha[m] : 0.f, l2 = on ? P.lse2[m] : 0.f, ga = on ? P.ga[m] : 0.f;
-    const float s = P.dzs != P.dz && on ? P.h_scale[P.perm[m]] : 0.f;
+    const int row = on ? P.perm[m] : 0;
+    const float s = P.dzs != P.dz && on ? P.h_scale[row] : 0.f;
+    // cross entropy: the target and u / T, which its dz has less
+    const int64_t t = P.T == 1 && on ? P.targets[row] - G.v0 : -1;
+    const float u = P.T == 1 && on ? (P.row_weight ? P.row_weight[row] : 1.f) * P.inv_t : 0.f;
 #pragma unroll
     for (int g = 0; g < T::FN; ++g) {
       const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
       float d[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        d[i] = __builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2)) * ga;
+        d[i] = fmaf(__builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2)), ga, n + i == t ? -u : 0.f);
         if (!(n + i < G.N) || ga == 0.f) d[i] = 0.f;
       }
       if (m < Mp) store4<DT>(P.dz + m * P.dz_ld, n, d);
@@ -387,24 +395,20 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   }
 }
 
-// dz at the targets of a piece: u (p - pt), from the targets' own logits, over
-// what the tiles stored there.
+// Distillation: dz at the stored entries of a piece, u (q - pt), from the entries' own
+// logits, over what the tiles stored there.
 template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod G) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int at = (int)(i / P.T), j = (int)(i - (int64_t)at * P.T);
+  const int at = (int)(i / TOP), j = (int)(i - (int64_t)at * TOP);
   if (at >= P.counts[0]) return;
   const float ga = P.ga[at];
   if (ga == 0.f) return;
-  const int n = P.perm[at];
-  const int id = P.T == 1 ? P.targets[n] : P.tidx[(int64_t)n * P.T + j];
-  const int64_t c = id - G.v0;
-  if (c < 0 || c >= G.N) return;
-  if (P.T != 1 && !(P.tval[(int64_t)n * P.T + j] > NEG_INF)) return;   // padding: no target
-  const float p = __builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at]));
-  // ga holds the normaliser's part beyond fp32, which is p's alone
-  const float u = (P.T == 1 ? (P.row_weight ? P.row_weight[n] : 1.f) : P.w[n] * P.pt[i]) * P.inv_t;
-  store_real<DT>(P.dz + at * P.dz_ld, c, fmaf(p, ga, -u));
-  if (P.dzs != P.dz) store_real<DT>(P.dzs + at * P.dz_ld, c, fmaf(p, ga, -u) * P.h_scale[n]);
+  const int64_t n = P.perm[at], c = P.tidx[n * TOP + j] - G.v0;
+  if (c < 0 || c >= G.N || !(P.tval[n * TOP + j] > NEG_INF)) return;   // another piece, or padding
+  // ga holds the normaliser's part beyond fp32, which is q's alone
+  const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -P.w[n] * P.pt[i]);
+  store_real<DT>(P.dz + at * P.dz_ld, c, d);
+  if (P.dzs != P.dz) store_real<DT>(P.dzs + at * P.dz_ld, c, d * P.h_scale[n]);
 }
 
 // How a piece's dx is shared out: the steps of all tiles in one line, cut into
@@ -468,37 +472,43 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
 }
 
 // dx of every row: its tile's sums in order, rounded once; zeros for rows without a
-// gradient.  One workgroup per row tile and column tile of the product.
-template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_rows_kernel(Head P, Prod G) {
-  const int M = P.counts[0];
-  const int in = blockIdx.x % G.nt, im = blockIdx.x / G.nt, m0 = im * T::BM, n0 = in * T::BN;
-  const Share S(G, M, T::BM);
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
-  int64_t t = 0;
-  int b0 = 0, b1 = -1;
-  if (m0 < M) {
-    const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
-    t = (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band);
-    b0 = (int)(t * S.full / S.per);
-    b1 = (int)(((t + 1) * S.full - 1) / S.per);
-  }
+// gradient.  One wave per fragment row of a tile's wave; the loads of eight sums go
+// out together.
+template <int DT, class T> __global__ __launch_bounds__(64) void dx_rows_kernel(Head P, Prod G) {
+  const int M = P.counts[0], lane = threadIdx.x;
+  constexpr int PER = T::NW * T::FM;
+  const int tile = blockIdx.x / PER, f = blockIdx.x % PER / T::NW, wid = blockIdx.x % T::NW;
+  const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
+  const int wm = wid / T::WN, wn = wid % T::WN;
+  const int m = m0 + index_of<T::FM, false>(wm, f, lane & 15);
+  f32x4 v[T::FN];
 #pragma unroll
-  for (int f = 0; f < T::FM; ++f) {
-    const int m = m0 + index_of<T::FM, false>(wm, f, lane & 15);
-    if (m >= P.N) continue;
-    const bool on = m < M && P.ga[m] != 0.f;
-    const int64_t row = (int64_t)P.perm[m] * P.H;
-    f32x4 v[T::FN];
+  for (int q = 0; q < T::FN; ++q) v[q] = 0;
+  if (m0 < M) {
+    const Share S(G, M, T::BM);
+    const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
+    const int64_t t = (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band);
+    const int b0 = (int)(t * S.full / S.per), b1 = (int)(((t + 1) * S.full - 1) / S.per);
+    const float *s = P.acc + f * T::FN * (T::TPB * 4) + (wid * 64 + lane) * 4;
+    for (int b = b0; b <= b1; b += 8) {
+      f32x4 o[8][T::FN];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int q = 0; q < T::FN; ++q)
+          o[e][q] = b + e <= b1 ? *(const f32x4 *)(s + S.slot(G, b + e, t) * (T::BM * T::BN) + q * (T::TPB * 4)) : f32x4(0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int q = 0; q < T::FN; ++q) v[q] += o[e][q];
+    }
+  }
+  if (m >= P.N) return;
+  if (m >= M || P.ga[m] == 0.f)
 #pragma unroll
     for (int q = 0; q < T::FN; ++q) v[q] = 0;
-    if (on)
-      for (int b = b0; b <= b1; ++b) {
-        const float *s = P.acc + S.slot(G, b, t) * (T::BM * T::BN) + threadIdx.x * 4;
-#pragma unroll
-        for (int q = 0; q < T::FN; ++q) v[q] += *(const f32x4 *)(s + (f * T::FN + q) * (T::TPB * 4));
-      }
-    store_columns<DT, T::FN>(P.gh, row, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec, v);
-  }
+  store_columns<DT, T::FN>(P.gh, (int64_t)P.perm[m] * P.H, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec,
+                           v);
 }
 
 // dW of a piece: complete, in the weight's type.
@@ -620,30 +630,26 @@ __global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
   }
 }
 
-// The loss terms, in order: a fixed run per thread, then the waves.
-__global__ __launch_bounds__(1024) void loss_kernel(Head P) {
-  __shared__ double red[16];
-  const int M = P.counts[1], per = (M + 1023) / 1024;
+// Workgroup 0: the loss terms, in order (a fixed run per thread, then the waves).
+// The others clear a row each that the sum of dW runs over without a term of its
+// own: those with a data error (their values may be NaN) and those up to a whole step.
+template <int DT> __global__ __launch_bounds__(256) void loss_kernel(Head P) {
+  if (blockIdx.x > 0) {
+    constexpr int E = Mma<DT>::E, Q = STEP / E;
+    const int at = blockIdx.x - 1, M = P.counts[0];
+    if (at >= (M + Q - 1) / Q * Q || (at < M && P.ga[at] != 0.f)) return;
+    u32x4 *x = (u32x4 *)(P.xs + (int64_t)at * P.x_ld);
+    for (int k = threadIdx.x; k < (int)(P.Kp * E / 16); k += 256) x[k] = 0;
+    return;
+  }
+  __shared__ double red[4];
+  const int M = P.counts[1], per = (M + 255) / 256;
   double s = 0.0;
   for (int i = threadIdx.x * per; i < M && i < (int)(threadIdx.x + 1) * per; ++i) s += P.term[i];
   s = wave_sum_d(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double t = 0.0;
-    for (int w = 0; w < 16; ++w) t += red[w];
-    P.loss[0] = (float)t;
-  }
-}
-
-// Rows that the sum of dW runs over without a term of their own: rows with a data
-// error (their values may be NaN) and those up to a whole step.
-template <int DT> __global__ __launch_bounds__(256) void clear_rows_kernel(Head P) {
-  constexpr int E = Mma<DT>::E, Q = STEP / E;
-  const int at = blockIdx.x, M = P.counts[0];
-  if (at >= (M + Q - 1) / Q * Q || (at < M && P.ga[at] != 0.f)) return;
-  u32x4 *x = (u32x4 *)(P.xs + (int64_t)at * P.x_ld);
-  for (int k = threadIdx.x; k < (int)(P.Kp * E / 16); k += 256) x[k] = 0;
+  if (threadIdx.x == 0) P.loss[0] = (float)(((red[0] + red[1]) + red[2]) + red[3]);
 }
 
 // rows of the weight into rows of whole steps, zeros behind them
@@ -677,7 +683,7 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   else hipLaunchKernelGGL((order_kernel<false>), dim3(1), b1024, 0, st, P);
   if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT>), dim3(P.N), b256, 0, st, P);
   else hipLaunchKernelGGL((stage_rows_kernel<DT, DT>), dim3(P.N), b256, 0, st, P);
-  hipLaunchKernelGGL((targets_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 4)), b256, 0, st, P);
+  if (kd) hipLaunchKernelGGL((targets_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 4)), b256, 0, st, P);
 
   Prod F = {};
   F.x = P.xs;
@@ -714,10 +720,9 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   } else {
     hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
   }
-  hipLaunchKernelGGL(loss_kernel, dim3(1), b1024, 0, st, P);
+  hipLaunchKernelGGL((loss_kernel<DT>), dim3((unsigned)(P.gw ? L.Np + 1 : 1)), b256, 0, st, P);
   if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 
-  if (P.gw) hipLaunchKernelGGL((clear_rows_kernel<DT>), dim3((unsigned)L.Np), b256, 0, st, P);
   Prod X = tiled<T>(Prod{}, P.N, P.H);
   X.x = P.dz;
   X.x_ld = L.dz_ld;
@@ -733,7 +738,7 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
     weight_piece(G, v0, cnt);
     G.N = (int32_t)cnt;
     hipLaunchKernelGGL((dz_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
-    hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * P.T, 256)), b256, 0, st, P, G);
+    if (kd) hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 256)), b256, 0, st, P, G);
     if (P.gh) {
       X.y = G.y;
       X.y_ld = G.y_ld;
@@ -754,7 +759,7 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
     }
   }
   if (P.gh)
-    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt)), dim3(T::TPB), 0, st, P, X);
+    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt * T::NW * T::FM)), dim3(64), 0, st, P, X);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

@@ -15,37 +15,40 @@ namespace {
 using namespace sv_gemm;
 using sv_head_host::cdiv;
 
-// codes * scale, in fp32, rounded once to the output's type
+// codes * scale, in fp32, rounded once to the output's type: a wave takes a row,
+// each lane 8 codes at a time where rows are made of aligned eights.  HBM bound.
 template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int8_t *codes, int64_t c_ld,
-                                                                       const float *scale, char *y, int H, int64_t total,
-                                                                       int vec) {
-  // one thread per four elements of a row where rows are whole fours, else per element
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
+                                                                       const float *scale, char *y, int H, int N, int vec) {
+  const int lane = threadIdx.x & 63;
+  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (n >= N) return;
+  const int8_t *c = codes + n * c_ld;
+  const float s = scale[n];
   if (vec) {
-    const int per = H / 4;
-    const int64_t n = i / per;
-    const int q = (int)(i - n * per);
-    const uint32_t c = *(const uint32_t *)(codes + n * c_ld + 4 * q);
-    const float s = scale[n];
-    float v[4];
+    char *o = y + n * H * (DT == SV_F32 ? 4 : 2);
+    for (int q = lane; q < H / 8; q += 64) {
+      const u32x2 w = __builtin_nontemporal_load((const u32x2 *)c + q);
+      float v[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = (float)(int8_t)(c >> (8 * k)) * s;
-    if constexpr (DT == SV_F32) {
-      *(f32x4 *)(y + i * 16) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-      u32x2 o;
+      for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)(w[k >> 2] >> (8 * (k & 3))) * s;
+      if constexpr (DT == SV_F32) {
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4 *)o + 2 * q);
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4 *)o + 2 * q + 1);
+      } else {
+        u32x4 u;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        o[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
-               (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
-      *(u32x2 *)(y + i * 8) = o;
+        for (int k = 0; k < 4; ++k)
+          u[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
+                 (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
+        __builtin_nontemporal_store(u, (u32x4 *)o + q);
+      }
     }
   } else {
-    const int64_t n = i / H;
-    const float v = (float)codes[n * c_ld + (i - n * H)] * scale[n];
-    if constexpr (DT == SV_F32) ((float *)y)[i] = v;
-    else ((__bf16 *)y)[i] = (__bf16)v;
+    for (int k = lane; k < H; k += 64) {
+      const float v = (float)c[k] * s;
+      if constexpr (DT == SV_F32) ((float *)y)[n * H + k] = v;
+      else ((__bf16 *)y)[n * H + k] = (__bf16)v;
+    }
   }
 }
 
@@ -145,16 +148,14 @@ extern "C" int sv_act8_unpack(int32_t N, int32_t H, const int8_t *codes, int64_t
   const int rc = sv_head_host::check_act8(N, H, y_dtype, y, 0, codes, codes_stride, scale);
   if (rc != SV_OK || N == 0) return rc;
   const int64_t ld = codes_stride ? codes_stride : H;
-  const int vec = H % 4 == 0 && ld % 4 == 0 && ((uintptr_t)codes & 3) == 0 && ((uintptr_t)y & 15) == 0;
-  const int64_t total = (int64_t)N * H / (vec ? 4 : 1);
-  if (cdiv(total, 256) > 0x7fffffffLL) return SV_ERR_SHAPE;
-  const dim3 grid((unsigned)cdiv(total, 256)), block(256);
+  const int vec = H % 8 == 0 && ld % 8 == 0 && ((uintptr_t)codes & 7) == 0 && ((uintptr_t)y & 15) == 0;
+  const dim3 grid((unsigned)cdiv(N, 4)), block(256);
   if (y_dtype == SV_BF16)
-    hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H,
-                       total, vec);
+    hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H, N,
+                       vec);
   else
-    hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H,
-                       total, vec);
+    hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H, N,
+                       vec);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
@@ -213,7 +214,8 @@ extern "C" int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden
     P.sw = weight_scale + v0;
     P.out = (char *)logits + v0 * oe;
     P.out_vec = (os * oe) % (4 * oe) == 0 && ((uintptr_t)P.out & (4 * oe - 1)) == 0;
-    if (s.N > 32) launch_logits<Tile<4, 4, 2, 2>>(P, s.out_dtype, st);
+    if (s.N >= 192) launch_logits<Tile<8, 4, 2, 4>>(P, s.out_dtype, st);
+    else if (s.N > 32) launch_logits<Tile<4, 4, 2, 2>>(P, s.out_dtype, st);
     else launch_logits<Tile<2, 2, 1, 4>>(P, s.out_dtype, st);
   }
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;

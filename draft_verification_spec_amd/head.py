@@ -55,9 +55,15 @@ def bind(lib):
         f.argtypes, f.restype = args, res
 
 
+_library = None
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    global _library
+    if _library is None:
+        from . import load_library
+        _library = load_library()
+    return _library
 
 
 def _check(rc):
@@ -68,30 +74,30 @@ def _check(rc):
 
 def _code(dtype, what):
     import torch
-    if dtype == torch.float32:
-        return 0
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return 1
+    if dtype is torch.float32:
+        return 0
     raise TypeError(f"{what} must be float32 or bfloat16")
 
 
-@contextlib.contextmanager
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev, stream):
-    """The tensors' device and the call's stream made current (conversions and
-    allocations of the call belong to that stream); yields the stream's handle."""
+    """(context, stream handle): in the context the tensors' device and the call's
+    stream are the current ones (conversions and allocations of the call belong to
+    that stream)."""
     import torch
     if dev.type != "cuda":
         raise ValueError("tensors must live on the GPU")
-    cur = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device() and (stream is None or stream == cur.cuda_stream):
-        yield cur.cuda_stream
-        return
-    with torch.cuda.device(dev):
-        if stream is None or stream == cur.cuda_stream:
-            yield cur.cuda_stream
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-                yield stream
+    cur = torch.cuda.current_stream(dev).cuda_stream
+    if stream is None or stream == cur:
+        return (_HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)), cur
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(dev))
+    both.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)))
+    return both, stream
 
 
 def _rows(t, H, what):
@@ -99,20 +105,19 @@ def _rows(t, H, what):
     if t.dim() < 1 or t.shape[-1] != H:
         raise ValueError(f"{what} must be [..., {H}]")
     t = t.reshape(-1, H) if t.dim() != 2 else t
-    if H > 1 and t.stride(1) != 1:
-        t = t.contiguous()
-    if t.shape[0] < 2:
-        return t, H
-    if t.stride(0) < H:
-        t = t.contiguous()
-    return t, t.stride(0)
+    ld, one = t.stride()
+    if H > 1 and one != 1 or ld < H and t.shape[0] > 1:
+        t, ld = t.contiguous(), H
+    return t, ld if t.shape[0] > 1 else H
 
 
 def _scales(s, shape, dev, what):
     import torch
     if s.device != dev or tuple(s.shape) != tuple(shape):
         raise ValueError(f"{what} must be one scale per row on the rows' device")
-    return s.to(dtype=torch.float32).contiguous().reshape(-1)
+    if s.dtype is torch.float32 and s.is_contiguous():
+        return s
+    return s.to(dtype=torch.float32).contiguous()
 
 
 def _scratch(workspace, nbytes, dev):
@@ -129,14 +134,15 @@ def act8_pack(x, *, stream=None) -> Act8:
     dt = _code(x.dtype, "rows")
     if x.dim() < 1 or not 1 <= x.shape[-1] <= MAX_H:
         raise ValueError(f"rows must be [..., H] with H of 1 .. {MAX_H}")
-    lead, H, dev = tuple(x.shape[:-1]), x.shape[-1], x.device
-    with _on(dev, stream) as st:
+    lead, H, dev = x.shape[:-1], x.shape[-1], x.device
+    here, st = _on(dev, stream)
+    with here:
         r, ld = _rows(x, H, "rows")
         N, Hp = r.shape[0], -(-H // 128) * 128
-        codes = torch.empty(N, Hp, dtype=torch.int8, device=dev)
-        scale = torch.empty(N, dtype=torch.float32, device=dev)
+        codes = torch.empty((*lead, Hp), dtype=torch.int8, device=dev)
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
         _check(_lib().sv_act8_pack(N, H, dt, r.data_ptr(), ld, codes.data_ptr(), Hp, scale.data_ptr(), st))
-    return Act8(codes[:, :H] if len(lead) == 1 else codes.view(*lead, Hp)[..., :H], scale.view(lead))
+    return Act8(codes if H == Hp else codes[..., :H], scale)
 
 
 def act8_unpack(a: Act8, dtype=None, *, stream=None):
@@ -149,7 +155,8 @@ def act8_unpack(a: Act8, dtype=None, *, stream=None):
     if codes.dtype != torch.int8 or codes.dim() < 1 or not 1 <= codes.shape[-1] <= MAX_H:
         raise TypeError("codes must be int8 [..., H]")
     H = codes.shape[-1]
-    with _on(dev, stream) as st:
+    here, st = _on(dev, stream)
+    with here:
         scale = _scales(a.scale, codes.shape[:-1], dev, "scale")
         r, ld = _rows(codes, H, "codes")
         y = torch.empty(codes.shape, dtype=dtype, device=dev)
@@ -184,7 +191,8 @@ def head_logits(hidden, weight: Act8, *, out_dtype=None, workspace=None, stream=
     hc = SV_I8 if xs is not None else _code(x.dtype, "hidden rows")
     if weight.codes.device != dev:
         raise ValueError("hidden and weight must be on one device")
-    with _on(dev, stream) as st:
+    here, st = _on(dev, stream)
+    with here:
         r, ld = _rows(x, H, "hidden")
         w, wld = _rows(weight.codes, H, "weight codes")
         ws = _scales(weight.scale, (V,), dev, "weight scale")
@@ -233,7 +241,8 @@ def _loss(fn, result, hidden, weight, grad, temperature, workspace, stream, inpu
     if grads is None:
         raise ValueError('grad must be True, False, "hidden" or "weight"')
     N = x.shape[0]
-    with _on(dev, stream) as st:
+    here, st = _on(dev, stream)
+    with here:
         r, ld = _rows(x, H, "hidden")
         w, wld = _rows(weight, H, "weight")
         if xs is not None:
