@@ -1,8 +1,9 @@
 // sv_gemm.h -- the tiled matrix product behind the vocabulary-head operators,
 // for gfx950 (MI355X): C[m][n] = sum_k X(m, k) Y(n, k) in bf16, fp32 or int8.
-// Each operand lies either with k along its rows ("rows": X[m][k]) or with k
-// down its columns ("columns": X[k][m]), so the gradients' products read dz, the
-// weight and the hidden rows as they lie and nothing is transposed in memory.
+// Each operand lies with k along its rows ("rows": X[m][k]), with k down its columns
+// ("columns": X[k][m]), or in 16-byte blocks of k of one m ("blocks": X[k / 8][m][8]
+// in bf16, X[k / 4][m][4] in fp32), so the gradients' products read the weight as it
+// lies and nothing is transposed in memory.
 //
 // One core for the three types: a step takes 128 bytes of k (64 bf16, 32 fp32,
 // 128 int8) of both tiles, and a matrix instruction takes from each lane 16
@@ -26,7 +27,7 @@
 // Columns: a lane reads, for each of its k, the neighbouring columns that its F
 // fragments hold (fragment f's index i is column i F + f), and bf16 pairs of k are
 // put together by byte permutes; the parts of k read together are turned against
-// each other.  (The LDS read that transposes by itself does not serve: the compiler
+// each other.  Blocks: a piece is a lane's, as with rows.  (The LDS read that transposes by itself does not serve: the compiler
 // lets it wait for every load into LDS, those for later steps among them; dW ran
 // at 1.0 PFLOP/s with it, measured at 2048 x 4096 x 65536.)
 // The columns' fragment is the instruction's first operand: a lane then holds
@@ -98,18 +99,22 @@ struct Part {
   int64_t bytes;
 };
 
+// How an operand lies in memory.  For blocks a row is one of blocks: ld and bytes are
+// its, count counts blocks of k.
+enum Lie { ROWS, COLS, BLOCKS };
+
 #ifdef __HIP_DEVICE_COMPILE__            // (the host pass knows no gfx950 builtins)
-// Loads and reads of one operand's tile: R indices (m or n), F fragments a wave,
-// COL: k down columns.
-template <int DT, int R, int F, int NW, bool COL> struct Side {
-  static constexpr int E = Mma<DT>::E, KR = STEP / E;    // k a step
+// Loads and reads of one operand's tile: R indices (m or n), F fragments a wave.
+template <int DT, int R, int F, int NW, Lie LIE> struct Side {
+  static constexpr bool COL = LIE != ROWS;               // k down the memory's rows
+  static constexpr int E = LIE == BLOCKS ? 16 : Mma<DT>::E, KR = STEP / E;   // bytes of an entry, entries of k a step
   static constexpr int NL = R / 8 / NW;                  // 16-byte loads a thread and step
   static_assert(NL >= 1 && NL < 16 && R % (8 * NW) == 0, "tile of whole loads");
   static constexpr int PR = COL ? R * E / 16 : 8;        // pieces of an LDS row
   // columns: k of a lane's 16 bytes, bytes that 16 lanes read of one k, and how
   // many such parts are read together
   static constexpr int KL = 16 / E, SPAN = 16 * F * E, PARTS = SPAN >= 256 ? 1 : 256 / SPAN;
-  static_assert(!COL || (E > 1 && (F == 2 || F == 4 || F == 8)), "whole reads of columns");
+  static_assert(LIE != COLS || (E > 1 && (F == 2 || F == 4 || F == 8)), "whole reads of columns");
   typedef __attribute__((address_space(3))) void lds_void;
 
   __amdgpu_buffer_rsrc_t rsrc;
@@ -174,7 +179,7 @@ template <int DT, int R, int F, int NW, bool COL> struct Side {
       pos += STEP;
     }
   }
-  static constexpr int READS = COL ? KL : F;
+  static constexpr int READS = LIE == COLS ? KL : F;
   // what the wave's fragments g0 .. g0 + F - 1 (of 16 indices) of half step h hold,
   // for columns in the order of k
   static __device__ __forceinline__ void read(u32x4 (&v)[F], const char *buf, int g0, int h) {
@@ -183,6 +188,10 @@ template <int DT, int R, int F, int NW, bool COL> struct Side {
       const char *at = buf + g0 * 16 * STEP + i * STEP + (((h * 4 + q) ^ (lane & 7)) << 4);
 #pragma unroll
       for (int f = 0; f < F; ++f) v[f] = *(const u32x4 *)(at + f * 16 * STEP);
+    } else if constexpr (LIE == BLOCKS) {
+      const char *at = buf + (h * 4 + q) * (R * 16) + (g0 * 16 + i) * 16;
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[f] = *(const u32x4 *)(at + f * 256);
     } else {
       constexpr int B = F * E;                           // bytes a lane reads of one k
       const char *at = buf + (h * 4 + q) * KL * (R * E) + ((g0 * 16 * E + i * B) ^ (q & (PARTS - 1)) * SPAN);
@@ -203,7 +212,7 @@ template <int DT, int R, int F, int NW, bool COL> struct Side {
   }
   // fragments from what was read
   static __device__ __forceinline__ void finish(u32x4 (&v)[F]) {
-    if constexpr (COL) {
+    if constexpr (LIE == COLS) {
       constexpr int WORDS = F * E / 4;                   // words read of one k
       u32x4 o[F];
 #pragma unroll
@@ -241,8 +250,8 @@ template <int MM, int RD, int LD> __device__ __forceinline__ void mix() {
 }
 #endif
 
-// The products of one tile over steps [s0, s0 + nk).  XC, YC: k down the columns.
-template <int DT, class T, bool XC = false, bool YC = false>
+// The products of one tile over steps [s0, s0 + nk).
+template <int DT, class T, Lie XC = ROWS, Lie YC = ROWS>
 __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::FN], char *lds, const Part &X,
                                         const Part &Y, int s0, int nk) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -331,9 +340,9 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
 #endif
 }
 
-// The index in its tile of a fragment's index i (0 .. 15) of wave w.
-template <int F, bool COL> __device__ __forceinline__ int index_of(int w, int f, int i) {
-  return COL ? (w * 16 + i) * F + f : (w * F + f) * 16 + i;
+// The index in its tile of index i (0 .. 15) of fragment f of wave w.
+template <int F, Lie LIE> __device__ __forceinline__ int index_of(int w, int f, int i) {
+  return LIE == COLS ? (w * 16 + i) * F + f : (w * F + f) * 16 + i;
 }
 
 template <int DT, class T>

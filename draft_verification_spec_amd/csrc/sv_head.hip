@@ -84,6 +84,7 @@ struct Head {
   float inv_t;
   int64_t Kp, Np;
   int64_t x_ld, dz_ld;                   // bytes between rows of xs, of dz
+  int64_t xw_ld, dzw_ld;                 // bytes between rows of blocks
   const char *hidden;
   int64_t h_ld;                          // bytes
   const float *h_scale;
@@ -115,7 +116,9 @@ struct Head {
   double *term;                          // loss terms
   float2 *part;                          // [column tiles][N] base-2 maximum and sum of exps
   char *xs;                              // rows with a loss
-  char *dz, *dzs;                        // a piece's dz, and times the rows' scales (8-bit rows; else the same)
+  char *dz;                              // a piece's dz, rows for dx
+  char *dzw;                             // the same, times the rows' scales (8-bit rows), in blocks for dW
+  char *xw;                              // rows with a gradient in blocks for dW
   char *wt;                              // a copied piece of the weight
   float *acc;                            // sums of dx, per workgroup and tile
 };
@@ -347,6 +350,54 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
   }
 }
 
+// A fragment turned into blocks: a lane starts with four columns n .. n + 3 of its row
+// m and ends with rows of one column.  Lanes whose rows differ in one bit swap what
+// the other one keeps: rows 2j and 2j + 1, then rows two apart (fp32: 16 bytes now),
+// and for bf16 then rows of the other half of eight, between two fragments.  That
+// last swap mirrors the eight lanes, so lanes of the upper half keep their columns
+// in mirrored order.
+__device__ __forceinline__ uint32_t pick(bool b, uint32_t x, uint32_t y) { return b ? x : y; }
+template <int CTRL> __device__ __forceinline__ uint32_t swap_lanes(uint32_t v) { return sv_dev::dpp<CTRL, 0xf, 0xf>(0u, v); }
+constexpr int LANE_1 = 0xb1, LANE_2 = 0x4e, LANE_7 = 0x141;   // DPP: lane ^ 1, lane ^ 2, lane ^ 7
+
+struct Turn {                            // the lane's bits, and the bits of the column it keeps
+  bool b0, b1, b2, k0, k1;
+  __device__ __forceinline__ Turn() {
+    b0 = threadIdx.x & 1;
+    b1 = threadIdx.x & 2;
+    b2 = threadIdx.x & 4;
+    k0 = b0 != b2;
+    k1 = b1 != b2;
+  }
+  // bf16: rows (m & ~3) .. + 3 of column n + 2 k0 + k1
+  __device__ __forceinline__ u32x2 four(uint32_t lo, uint32_t hi) const {
+    const uint32_t mine = pick(k0, hi, lo), o = swap_lanes<LANE_1>(pick(k0, lo, hi));
+    const uint32_t x = pick(b0, o, mine), y = pick(b0, mine, o);   // of the even row, of the odd one
+    const uint32_t p = __builtin_amdgcn_perm(y, x, 0x05040100), q = __builtin_amdgcn_perm(y, x, 0x07060302);
+    const uint32_t own = pick(k1, q, p), r = swap_lanes<LANE_2>(pick(k1, p, q));
+    return u32x2{pick(b1, r, own), pick(b1, own, r)};
+  }
+  // bf16: rows (m & ~7) .. + 7 of that column of fragment g, in the upper half of g + 1
+  __device__ __forceinline__ u32x4 eight(u32x2 g, u32x2 h) const {
+    const uint32_t o0 = pick(b2, h[0], g[0]), o1 = pick(b2, h[1], g[1]);
+    const uint32_t r0 = swap_lanes<LANE_7>(pick(b2, g[0], h[0])), r1 = swap_lanes<LANE_7>(pick(b2, g[1], h[1]));
+    return u32x4{pick(b2, r0, o0), pick(b2, r1, o1), pick(b2, o0, r0), pick(b2, o1, r1)};
+  }
+  // fp32: rows (m & ~3) .. + 3 of column n + b0 + 2 b1
+  __device__ __forceinline__ u32x4 four(const float (&d)[4]) const {
+    uint32_t x[2], y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __float_as_uint(d[2 * i]), b = __float_as_uint(d[2 * i + 1]);
+      const uint32_t mine = pick(b0, b, a), o = swap_lanes<LANE_1>(pick(b0, a, b));
+      x[i] = pick(b0, o, mine);
+      y[i] = pick(b0, mine, o);
+    }
+    const uint32_t r = swap_lanes<LANE_2>(pick(b1, x[0], x[1])), s = swap_lanes<LANE_2>(pick(b1, y[0], y[1]));
+    return u32x4{pick(b1, r, x[0]), pick(b1, s, y[0]), pick(b1, x[1], r), pick(b1, y[1], s)};
+  }
+};
+
 // Backward tile of a piece: dz = u (2^(z log2 e - lse2)), rounded to the
 // operands' type; zeros in the rows up to a whole step and in the columns up to a
 // whole tile, so that both gradients can sum whole steps.
@@ -366,30 +417,52 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
     product<DT, T>(acc, lds, X, Y, 0, G.nk);
   }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+  const Turn turn;
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
     const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
     const bool on = m < M;
     const float a = on ? P.alpha[m] : 0.f, l2 = on ? P.lse2[m] : 0.f, ga = on ? P.ga[m] : 0.f;
     const int row = on ? P.perm[m] : 0;
-    const float s = P.dzs != P.dz && on ? P.h_scale[row] : 0.f;
+    const float s = P.h_scale && on && ga != 0.f ? P.h_scale[row] : 1.f;
     // cross entropy: the target and u / T, which its dz has less
     const int64_t t = P.T == 1 && on ? P.targets[row] - G.v0 : -1;
     const float u = P.T == 1 && on ? (P.row_weight ? P.row_weight[row] : 1.f) * P.inv_t : 0.f;
+    float d[T::FN][4];
 #pragma unroll
-    for (int g = 0; g < T::FN; ++g) {
-      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
-      float d[4];
+    for (int g = 0; g < T::FN; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        d[i] = fmaf(__builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2)), ga, n + i == t ? -u : 0.f);
-        if (!(n + i < G.N) || ga == 0.f) d[i] = 0.f;
+        const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4 + i;
+        const float v = fmaf(__builtin_amdgcn_exp2f(fmaf(acc[f][g][i] * a, LOG2E, -l2)), ga, n == t ? -u : 0.f);
+        d[g][i] = n < G.N && ga != 0.f ? v : 0.f;
       }
-      if (m < Mp) store4<DT>(P.dz + m * P.dz_ld, n, d);
-      if (P.dzs != P.dz) {
+    const int n = n0 + wn * T::FN * 16 + (lane >> 4) * 4;
+    if (P.gh && m < Mp) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = ga == 0.f ? 0.f : d[i] * s;
-        if (m < Mp) store4<DT>(P.dzs + m * P.dz_ld, n, d);
+      for (int g = 0; g < T::FN; ++g) store4<DT>(P.dz + m * P.dz_ld, n + g * 16, d[g]);
+    }
+    if (P.gw) {
+      char *at = P.dzw + m / (16 / Mma<DT>::E) * P.dzw_ld;
+      u32x4 o[T::FN];                    // bf16: every second one
+#pragma unroll
+      for (int g = 0; g < T::FN; ++g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[g][i] *= s;
+        if constexpr (DT == SV_F32) o[g] = turn.four(d[g]);
+      }
+      if constexpr (DT == SV_BF16) {
+#pragma unroll
+        for (int g = 0; g < T::FN; g += 2)
+          o[g] = turn.eight(turn.four(pack2(d[g][0], d[g][1]), pack2(d[g][2], d[g][3])),
+                            turn.four(pack2(d[g + 1][0], d[g + 1][1]), pack2(d[g + 1][2], d[g + 1][3])));
+        at += (n + 2 * turn.k0 + turn.k1 + 16 * turn.b2) * 16;
+      } else {
+        at += (n + turn.b0 + 2 * turn.b1) * 16;
+      }
+      if (m < Mp) {
+#pragma unroll
+        for (int g = 0; g < T::FN; g += DT == SV_BF16 ? 2 : 1) *(u32x4 *)(at + g * 256) = o[g];
       }
     }
   }
@@ -407,8 +480,9 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
   if (c < 0 || c >= G.N || !(P.tval[n * TOP + j] > NEG_INF)) return;   // another piece, or padding
   // ga holds the normaliser's part beyond fp32, which is q's alone
   const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -P.w[n] * P.pt[i]);
-  store_real<DT>(P.dz + at * P.dz_ld, c, d);
-  if (P.dzs != P.dz) store_real<DT>(P.dzs + at * P.dz_ld, c, d * P.h_scale[n]);
+  constexpr int B = 16 / Mma<DT>::E;
+  if (P.gh) store_real<DT>(P.dz + at * P.dz_ld, c, d);
+  if (P.gw) store_real<DT>(P.dzw + at / B * P.dzw_ld, c * B + at % B, P.h_scale ? d * P.h_scale[n] : d);
 }
 
 // How a piece's dx is shared out: the steps of all tiles in one line, cut into
@@ -457,7 +531,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
     clear<DT, T>(acc);
     const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
     const Part Y = {G.y + (int64_t)n0 * Mma<DT>::E, G.y_ld, G.M, (P.Kp - n0) * Mma<DT>::E};
-    product<DT, T, false, true>(acc, lds, X, Y, s0, ns);
+    product<DT, T, ROWS, COLS>(acc, lds, X, Y, s0, ns);
 #pragma unroll
     for (int f = 0; f < T::FM; ++f)
 #pragma unroll
@@ -480,7 +554,7 @@ template <int DT, class T> __global__ __launch_bounds__(64) void dx_rows_kernel(
   const int tile = blockIdx.x / PER, f = blockIdx.x % PER / T::NW, wid = blockIdx.x % T::NW;
   const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
   const int wm = wid / T::WN, wn = wid % T::WN;
-  const int m = m0 + index_of<T::FM, false>(wm, f, lane & 15);
+  const int m = m0 + index_of<T::FM, ROWS>(wm, f, lane & 15);
   f32x4 v[T::FN];
 #pragma unroll
   for (int q = 0; q < T::FN; ++q) v[q] = 0;
@@ -507,7 +581,7 @@ template <int DT, class T> __global__ __launch_bounds__(64) void dx_rows_kernel(
   if (m >= M || P.ga[m] == 0.f)
 #pragma unroll
     for (int q = 0; q < T::FN; ++q) v[q] = 0;
-  store_columns<DT, T::FN>(P.gh, (int64_t)P.perm[m] * P.H, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec,
+  store_columns<DT, T::FN>(P.gh, (int64_t)P.perm[m] * P.H, n0 + index_of<T::FN, COLS>(wn, 0, (lane >> 4) * 4), P.H, G.vec,
                            v);
 }
 
@@ -519,21 +593,30 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   const int m0 = im * T::BM, n0 = in * T::BN;
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
-  constexpr int E = Mma<DT>::E, Q = STEP / E;
+  constexpr int Q = STEP / Mma<DT>::E;
   const int nk = (P.counts[0] + Q - 1) / Q;
-  const Part X = {G.x + (int64_t)m0 * E, G.x_ld, (int64_t)nk * Q, G.x_ld - (int64_t)m0 * E};
-  const Part Y = {G.y + (int64_t)n0 * E, G.y_ld, (int64_t)nk * Q, G.y_ld - (int64_t)n0 * E};
-  product<DT, T, true, true>(acc, lds, X, Y, 0, nk);
+  const Part X = {G.x + (int64_t)m0 * 16, G.x_ld, (int64_t)nk * (STEP / 16), G.x_ld - (int64_t)m0 * 16};
+  const Part Y = {G.y + (int64_t)n0 * 16, G.y_ld, (int64_t)nk * (STEP / 16), G.y_ld - (int64_t)n0 * 16};
+  product<DT, T, BLOCKS, BLOCKS>(acc, lds, X, Y, 0, nk);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
-    const int m = m0 + index_of<T::FM, true>(wm, f, lane & 15);
+    const int m = m0 + index_of<T::FM, BLOCKS>(wm, f, lane & 15);
     if (m >= G.M) continue;
-    f32x4 v[T::FN];
 #pragma unroll
-    for (int g = 0; g < T::FN; ++g) v[g] = acc[f][g];
-    store_columns<DT, T::FN>(out, (int64_t)m * P.H, n0 + index_of<T::FN, true>(wn, 0, (lane >> 4) * 4), P.H, G.vec, v);
+    for (int g = 0; g < T::FN; ++g) {
+      const int n = n0 + index_of<T::FN, BLOCKS>(wn, g, (lane >> 4) * 4);
+      const int64_t o = (int64_t)m * P.H + n;
+      const float v[4] = {acc[f][g][0], acc[f][g][1], acc[f][g][2], acc[f][g][3]};
+      if (G.vec && n + 4 <= G.N) {
+        store4<DT>(out, o, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < G.N) store_real<DT>(out, o + i, v[i]);
+      }
+    }
   }
 }
 
@@ -631,15 +714,34 @@ __global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
 }
 
 // Workgroup 0: the loss terms, in order (a fixed run per thread, then the waves).
-// The others clear a row each that the sum of dW runs over without a term of its
-// own: those with a data error (their values may be NaN) and those up to a whole step.
+// The others put the rows that the sum of dW runs over into blocks, with zeros for
+// rows without a term of their own: those with a data error (their values may be NaN)
+// and those up to a whole step.
 template <int DT> __global__ __launch_bounds__(256) void loss_kernel(Head P) {
   if (blockIdx.x > 0) {
-    constexpr int E = Mma<DT>::E, Q = STEP / E;
-    const int at = blockIdx.x - 1, M = P.counts[0];
-    if (at >= (M + Q - 1) / Q * Q || (at < M && P.ga[at] != 0.f)) return;
-    u32x4 *x = (u32x4 *)(P.xs + (int64_t)at * P.x_ld);
-    for (int k = threadIdx.x; k < (int)(P.Kp * E / 16); k += 256) x[k] = 0;
+    constexpr int E = Mma<DT>::E, Q = STEP / E, B = 16 / E;
+    const int at = B * (blockIdx.x - 1), M = P.counts[0];
+    if (at >= (M + Q - 1) / Q * Q) return;
+    bool on[B];
+#pragma unroll
+    for (int r = 0; r < B; ++r) on[r] = at + r < M && P.ga[at + r] != 0.f;
+    const char *x = P.xs + at * P.x_ld;
+    u32x4 *o = (u32x4 *)(P.xw + at / B * P.xw_ld);
+    for (int k = threadIdx.x; k < (int)P.Kp; k += 256) {
+      u32x4 v;
+      if constexpr (DT == SV_BF16) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t a = on[2 * r] ? ((const uint16_t *)(x + 2 * r * P.x_ld))[k] : 0u;
+          const uint32_t b = on[2 * r + 1] ? ((const uint16_t *)(x + (2 * r + 1) * P.x_ld))[k] : 0u;
+          v[r] = a | b << 16;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = on[r] ? ((const uint32_t *)(x + r * P.x_ld))[k] : 0u;
+      }
+      o[k] = v;
+    }
     return;
   }
   __shared__ double red[4];
@@ -720,7 +822,7 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   } else {
     hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
   }
-  hipLaunchKernelGGL((loss_kernel<DT>), dim3((unsigned)(P.gw ? L.Np + 1 : 1)), b256, 0, st, P);
+  hipLaunchKernelGGL((loss_kernel<DT>), dim3((unsigned)(P.gw ? L.Np * E / 16 + 1 : 1)), b256, 0, st, P);
   if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 
   Prod X = tiled<T>(Prod{}, P.N, P.H);
@@ -750,10 +852,10 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
     if (P.gw) {
       Prod W = tiled<TW>(Prod{}, cnt, P.H);
       W.v0 = v0;
-      W.x = P.dzs;
-      W.x_ld = L.dz_ld;
-      W.y = P.xs;
-      W.y_ld = L.x_ld;
+      W.x = P.dzw;
+      W.x_ld = L.dzw_ld;
+      W.y = P.xw;
+      W.y_ld = L.xw_ld;
       W.vec = P.H % 4 == 0 && ((uintptr_t)P.gw & 15) == 0;
       hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
     }
@@ -799,7 +901,10 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.part = (float2 *)(ws + L.part);
   P.xs = ws + L.xs;
   P.dz = ws + L.dz;
-  P.dzs = P.h_scale && P.gw ? ws + L.dzs : P.dz;
+  P.dzw = ws + L.dzw;
+  P.xw = ws + L.xw;
+  P.xw_ld = L.xw_ld;
+  P.dzw_ld = L.dzw_ld;
   P.wt = ws + L.wt;
   P.acc = (float *)(ws + L.acc);
   const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);

@@ -15,6 +15,7 @@ namespace sv_head_host {
 constexpr int TOP = 32;                  // stored entries per row (sv_head_kd)
 constexpr int STEP = 128;                // bytes of k per step of the tiled product
 constexpr int CUS = 256;                 // compute units of the GPU
+constexpr int64_t PIECE = (int64_t)512 << 20;   // bytes of a piece's dz and weight
 constexpr int RUN = 8;                   // least steps of a workgroup of the hidden gradient
 constexpr int64_t MAX_LD = (int64_t)1 << 22;   // bytes between rows of a tiled operand: a tile's offsets fit 31 bits
 
@@ -92,10 +93,11 @@ struct Plan {
   int64_t Np;                            // rows in whole steps, elements
   int64_t piece, pieces;                 // vocabulary entries per piece, pieces
   int64_t x_ld, dz_ld;                   // bytes between copied rows (of hidden and weight), rows of dz
+  int64_t xw_ld, dzw_ld;                 // the same for dW's operands, rows of 16-byte blocks
   int bm, bn;                            // tile of the products
   int groups, slots;                     // workgroups of the hidden gradient, tiles each may touch
   // workspace sections
-  size_t counts, perm, alpha, ga, lse2, w, flags, zt, pt, term, part, xs, dz, dzs, wt, acc, total;
+  size_t counts, perm, alpha, ga, lse2, w, flags, zt, pt, term, part, xs, xw, dz, dzw, wt, acc, total;
 };
 
 inline bool head_shape_ok(const sv_head_shape_t *s, bool kd) {
@@ -126,13 +128,14 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.Np = up(N, q);
   p.bm = N <= 32 ? 32 : (N < 192 || s->dtype == SV_F32) ? 128 : 256;
   p.bn = p.bm == 256 ? 256 : 128;
-  // A piece: its dz is written and read back twice, and a copied weight once, so
-  // both are kept near 256 MB together, the size of the Infinity Cache; a whole
-  // number of 256 entries, all pieces alike.
-  const int64_t per = (s->grads ? p.Np * e : 0) + p.Kp * e;
-  int64_t most = ((int64_t)256 << 20) / per / 256 * 256;
+  // A piece: its dz, for dx and for dW, and a copied weight take PIECE bytes together;
+  // a whole number of 256 entries, all pieces alike.  More pays a little (4096 rows,
+  // 4096 x 151936 in bf16: 13.2 ms with 256 MB, 12.8 with 640, 12.6 with 1280, for
+  // fewer passes over the sums of dx), but the logits in fp32 would be 2.5 GB.
+  const int64_t per = (s->grads ? 2 * p.Np * e : 0) + p.Kp * e;
+  int64_t most = PIECE / per / 256 * 256;
   if (most < 256) most = 256;
-  const int64_t by_ld = MAX_LD / e / 2;          // (and a line more)
+  const int64_t by_ld = MAX_LD / 16 - 8;           // rows of blocks (and a line more)
   if (most > by_ld) most = by_ld;
   p.pieces = cdiv(s->V, most);
   p.piece = up(cdiv(s->V, p.pieces), 256);
@@ -162,8 +165,11 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.x_ld = spread(p.Kp * e);
   p.dz_ld = spread(p.piece * e);
   p.xs = take((size_t)p.Np * p.x_ld);
-  p.dz = take(gh || gw ? (size_t)p.Np * p.dz_ld : 0);
-  p.dzs = take(gw && s->hidden_dtype == SV_I8 ? (size_t)p.Np * p.dz_ld : 0);
+  p.xw_ld = spread(p.Kp * 16);
+  p.dzw_ld = spread(p.piece * 16);
+  p.xw = take(gw ? (size_t)(p.Np * e / 16) * p.xw_ld : 0);
+  p.dz = take(gh ? (size_t)p.Np * p.dz_ld : 0);
+  p.dzw = take(gw ? (size_t)(p.Np * e / 16) * p.dzw_ld : 0);
   p.wt = take((size_t)p.piece * p.x_ld);
   p.acc = take(gh ? (size_t)p.groups * p.slots * p.bm * p.bn * 4 : 0);
   p.total = o;
