@@ -177,8 +177,16 @@ template <bool KD> __device__ __forceinline__ int class_of(const Head &P, int n,
   }
 }
 
+// The results of a row that is left out.
+__device__ __forceinline__ void left_out(const Head &P, int n, int bits) {
+  const float r = bits ? __builtin_nanf("") : 0.f;
+  P.rows[n] = r;
+  if (P.lse) P.lse[n] = r;
+  if (P.status) P.status[n] = bits;
+}
+
 // The order of rows: by class, by index within a class.  One workgroup; two
-// passes over N small entries (a few microseconds at the largest batches).
+// passes over N small entries (12 us at 4096 rows).
 template <bool KD> __global__ __launch_bounds__(1024) void order_kernel(Head P) {
   __shared__ int cnt[3][16];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
@@ -222,57 +230,82 @@ template <bool KD> __global__ __launch_bounds__(1024) void order_kernel(Head P) 
       if (k == q) P.perm[base[q] + before + at] = n;
       base[q] += all;
     }
-    if (k == 2) {                        // left out: its results are known
-      const float r = bits ? __builtin_nanf("") : 0.f;
-      P.rows[n] = r;
-      if (P.lse) P.lse[n] = r;
-      if (P.status) P.status[n] = bits;
-    }
+    if (k == 2) left_out(P, n, bits);
   }
 }
 
-// Rows with a loss, in order, in the operands' type, zeros up to whole steps.
-// 8-bit codes are exact in bf16 and fp32; their scale goes into alpha.
-template <int HT, int DT> __global__ __launch_bounds__(256) void stage_rows_kernel(Head P) {
-  const int at = blockIdx.x;
-  if (at >= P.counts[1]) return;
-  const int n = P.perm[at];
+// Rows with a loss, in order, in the operands' type, zeros up to whole steps; for the
+// distillation also z of the stored entries (fp32 sums, an entry a wave).  8-bit codes
+// are exact in bf16 and fp32; their scale goes into alpha.  FIND: a workgroup per row
+// that finds its place itself, for batches of at most FIND_ROWS rows (each looks at
+// all of them), which saves the order's launch.
+constexpr int FIND_ROWS = 1024;
+
+template <int HT, int DT, bool KD, bool FIND> __global__ __launch_bounds__(256) void stage_rows_kernel(Head P) {
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  int at = blockIdx.x, n = at;
+  if constexpr (FIND) {
+    __shared__ int cnt[4][3];
+    int bits, c[3] = {0, 0, 0};          // rows before this one, rows of class 0, of class 1
+    const int k = class_of<KD>(P, n, bits);
+    for (int i = tid; i < P.N; i += 256) {
+      int other;
+      const int q = class_of<KD>(P, i, other);
+      c[0] += q < k || (q == k && i < n);
+      c[1] += q == 0;
+      c[2] += q == 1;
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      c[q] = sv_dev::wave_sum_i(c[q]);
+      if (lane == 0) cnt[wid][q] = c[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) c[q] = cnt[0][q] + cnt[1][q] + cnt[2][q] + cnt[3][q];
+    at = c[0];
+    if (tid == 0) {
+      P.perm[at] = n;
+      if (n == 0) { P.counts[0] = c[1]; P.counts[1] = c[1] + c[2]; }
+      if (k == 2) left_out(P, n, bits);
+    }
+    if (k == 2) return;
+  } else {
+    if (at >= P.counts[1]) return;
+    n = P.perm[at];
+  }
   const char *src = P.hidden + (int64_t)n * P.h_ld;
   char *dst = P.xs + (int64_t)at * P.x_ld;
-  for (int k = threadIdx.x; k < (int)P.Kp; k += 256) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
-  if (threadIdx.x == 0) P.alpha[at] = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
-}
-
-// z of the stored entries: one wave per (row, entry), fp32 sums.
-template <int DT> __global__ __launch_bounds__(256) void targets_kernel(Head P) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int at = (int)(i / P.T), j = (int)(i - (int64_t)at * P.T);
-  if (at >= P.counts[1]) return;
-  const int n = P.perm[at];
-  const int id = P.tidx[(int64_t)n * P.T + j];
-  float s = 0.f;
-  if (id >= 0 && id < P.V) {
+  for (int k = tid; k < (int)P.Kp; k += 256) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
+  const float alpha = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
+  if (tid == 0) P.alpha[at] = alpha;
+  if constexpr (KD) {
+    __syncthreads();                     // the row as stored, for every wave
     constexpr int E = Mma<DT>::E, W = 16 / E;
-    const char *x = P.xs + (int64_t)at * P.x_ld;
-    const char *w = P.weight + (int64_t)id * P.w_ld;
     const bool vec = (((uintptr_t)P.weight | (uintptr_t)P.w_ld) & 15) == 0;
     const int nv = P.H / W;
-    for (int q = lane; q < nv; q += 64) {  // (the same order of terms whatever the alignment)
-      const u32x4 a = *(const u32x4 *)(x + (int64_t)q * 16);
-      if (vec) {
-        const u32x4 b = *(const u32x4 *)(w + (int64_t)q * 16);
+    for (int j = wid; j < TOP; j += 4) {
+      const int id = P.tidx[(int64_t)n * TOP + j];
+      float s = 0.f;
+      if (id >= 0 && id < P.V) {
+        const char *w = P.weight + (int64_t)id * P.w_ld;
+        for (int q = lane; q < nv; q += 64) {  // (the same order of terms whatever the alignment)
+          const u32x4 a = *(const u32x4 *)(dst + (int64_t)q * 16);
+          if (vec) {
+            const u32x4 b = *(const u32x4 *)(w + (int64_t)q * 16);
 #pragma unroll
-        for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), sv_dev::unpack<DT>(b, e), s);
-      } else {
+            for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), sv_dev::unpack<DT>(b, e), s);
+          } else {
 #pragma unroll
-        for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), load_real<DT>(w, q * W + e), s);
+            for (int e = 0; e < W; ++e) s = fmaf(sv_dev::unpack<DT>(a, e), load_real<DT>(w, q * W + e), s);
+          }
+        }
+        for (int k = nv * W + lane; k < P.H; k += 64) s = fmaf(load_real<DT>(dst, k), load_real<DT>(w, k), s);
+        s = wave_sum_f(s);
       }
+      if (lane == 0) P.zt[(int64_t)at * TOP + j] = s * alpha;
     }
-    for (int k = nv * W + lane; k < P.H; k += 64) s = fmaf(load_real<DT>(x, k), load_real<DT>(w, k), s);
-    s = wave_sum_f(s);
   }
-  if (lane == 0) P.zt[i] = s * P.alpha[at];
 }
 
 // -------------------------------------------------------------------- products
@@ -545,11 +578,14 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
   }
 }
 
-// dx of every row: its tile's sums in order, rounded once; zeros for rows without a
-// gradient.  One wave per fragment row of a tile's wave; the loads of eight sums go
-// out together.
-template <int DT, class T> __global__ __launch_bounds__(64) void dx_rows_kernel(Head P, Prod G) {
-  const int M = P.counts[0], lane = threadIdx.x;
+// dx of every row: its tile's sums in a fixed order, rounded once; zeros for rows
+// without a gradient.  A workgroup per fragment row of a tile's wave: each of its WS
+// waves adds a run of the tile's sums, four loads under way at a time, and the first
+// joins the runs.  (Few rows have many sums of a few steps each: 79 at 24 rows of 512
+// in fp32, which one wave took 21 us for.)
+template <int DT, class T, int WS> __global__ __launch_bounds__(64 * WS) void dx_rows_kernel(Head P, Prod G) {
+  __shared__ f32x4 red[WS > 1 ? WS - 1 : 1][T::FN][64];
+  const int M = P.counts[0], lane = threadIdx.x & 63, ws = threadIdx.x >> 6;
   constexpr int PER = T::NW * T::FM;
   const int tile = blockIdx.x / PER, f = blockIdx.x % PER / T::NW, wid = blockIdx.x % T::NW;
   const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
@@ -563,19 +599,33 @@ template <int DT, class T> __global__ __launch_bounds__(64) void dx_rows_kernel(
     const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
     const int64_t t = (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band);
     const int b0 = (int)(t * S.full / S.per), b1 = (int)(((t + 1) * S.full - 1) / S.per);
+    const int run = (b1 - b0 + WS) / WS, first = b0 + ws * run, last = first + run - 1 < b1 ? first + run - 1 : b1;
     const float *s = P.acc + f * T::FN * (T::TPB * 4) + (wid * 64 + lane) * 4;
-    for (int b = b0; b <= b1; b += 8) {
-      f32x4 o[8][T::FN];
+    for (int b = first; b <= last; b += 4) {
+      f32x4 o[4][T::FN];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int q = 0; q < T::FN; ++q)
-          o[e][q] = b + e <= b1 ? *(const f32x4 *)(s + S.slot(G, b + e, t) * (T::BM * T::BN) + q * (T::TPB * 4)) : f32x4(0.f);
+        for (int q = 0; q < T::FN; ++q) {
+          o[e][q] = 0;
+          if (b + e <= last) o[e][q] = *(const f32x4 *)(s + S.slot(G, b + e, t) * (T::BM * T::BN) + q * (T::TPB * 4));
+        }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int q = 0; q < T::FN; ++q) v[q] += o[e][q];
     }
+  }
+  if constexpr (WS > 1) {
+    if (ws > 0) {
+#pragma unroll
+      for (int q = 0; q < T::FN; ++q) red[ws - 1][q][lane] = v[q];
+    }
+    __syncthreads();
+    if (ws > 0) return;
+    for (int w = 0; w < WS - 1; ++w)
+#pragma unroll
+      for (int q = 0; q < T::FN; ++q) v[q] += red[w][q][lane];
   }
   if (m >= P.N) return;
   if (m >= M || P.ga[m] == 0.f)
@@ -621,77 +671,18 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
 }
 
 // -------------------------------------------------------------- rows' results
-// The normaliser of each row from its tiles, in a fixed order: lanes take
-// (row, part of the tiles), waves take parts too; then one thread per row.
-template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Head P, int tiles, int per) {
-  __shared__ double ms[1024], ss[1024];
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int M = P.counts[1], r0 = blockIdx.x * per;
-  if (r0 >= M) return;
-  const int r = lane & (per - 1), parts = 16 * (64 / per), q = wid * (64 / per) + lane / per;
-  const int at = r0 + r;
-  double m = -__builtin_inf(), s = 0.0;
-  if (at < M)
-    for (int t = q; t < tiles; t += parts) {
-      const float2 v = P.part[(int64_t)t * P.N + at];
-      if (!(v.x == v.x)) m = s = __builtin_nan("");
-      else if (v.x > (float)m) {
-        s = s * (double)__builtin_amdgcn_exp2f((float)m - v.x) + (double)v.y;
-        m = v.x;
-      } else if (v.x != NEG_INF) {
-        s += (double)v.y * (double)__builtin_amdgcn_exp2f(v.x - (float)m);
-      }
-    }
-  ms[q * per + r] = m;
-  ss[q * per + r] = s;
-  __syncthreads();
-  if (threadIdx.x >= (unsigned)per || at >= M) return;
-  m = -__builtin_inf();
-  bool nan = false;
-  for (int t = 0; t < parts; ++t) {
-    const double v = ms[t * per + r];
-    nan |= !(v == v);
-    m = v > m ? v : m;
-  }
-  s = 0.0;
-  for (int t = 0; t < parts; ++t) {
-    const double v = ms[t * per + r];
-    if (v > -__builtin_inf()) s += ss[t * per + r] * (double)__builtin_amdgcn_exp2f((float)(v - m));
-  }
-  int F = nan ? SV_HEAD_NAN : m == __builtin_inf() ? SV_HEAD_POSINF : m == -__builtin_inf() ? SV_HEAD_EMPTY : 0;
-  static_assert(SV_HEAD_NAN == SV_KD_NAN && SV_HEAD_POSINF == SV_KD_POSINF && SV_HEAD_EMPTY == SV_KD_EMPTY, "one set");
-  const double l2 = F ? 0.0 : m + log2(s);
-  const int n = P.perm[at];
-  const float hi = (float)l2;
-  P.lse2[at] = hi;
-  float u;
-  if constexpr (KD) {
-    // the part of the normaliser beyond fp32, for the distillation's rows kernel
-    P.term[at] = l2;
-    P.flags[n] |= F;
-    u = P.w[n];
-  } else {
-    u = P.row_weight ? P.row_weight[n] : 1.f;
-    const double lse = l2 * LN2;
-    const float nll = F ? __builtin_nanf("") : (float)(lse - (double)P.zt[at]);
-    P.rows[n] = nll;
-    if (P.lse) P.lse[n] = F ? __builtin_nanf("") : (float)lse;
-    if (P.status) P.status[n] = F;
-    P.term[at] = (!F && u != 0.f) ? (double)u * (double)nll : 0.0;
-  }
-  if (P.grads) {
-    const float c = F ? 0.f : u * (float)(1.0 - (l2 - (double)hi) * LN2) * P.inv_t;
-    P.ga[at] = c;
-  }
+// (m, s) of two parts of a row: the maximum in base 2 and the sum of 2^(. - m).  A NaN
+// maximum stays; one of -infinity has no terms.
+__device__ __forceinline__ void join(float &m, double &s, float om, double os) {
+  const float t = sv_dev::fmax_nan(m, om), ref = fabsf(t) == __builtin_inff() ? 0.f : t;
+  const float a = m == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m - ref), b = om == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(om - ref);
+  s = s * (double)a + os * (double)b;
+  m = t;
 }
 
-// KL of a row over its stored entries: one wave per row.
-__global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
+// KL of a row over its stored entries, by a wave; l2: its normaliser.
+__device__ __forceinline__ void kd_row(const Head &P, int at, int n, int F, double l2) {
   const int lane = threadIdx.x & 63;
-  const int at = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= P.counts[1]) return;
-  const int n = P.perm[at];
-  const int F = P.flags[n];
   const float v = lane < TOP ? P.tval[(int64_t)n * TOP + lane] : NEG_INF;
   const int x = lane < TOP ? P.tidx[(int64_t)n * TOP + lane] : -1;
   const bool use = !F && v != NEG_INF && x != -1;
@@ -700,7 +691,6 @@ __global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
   const double e = use ? exp(a) : 0.0;
   const double sv = wave_sum_d(e);
   const double pt = use ? e / sv : 0.0;
-  const double l2 = P.term[at];
   double t = 0.0;
   if (use && pt > 0.0) t = pt * (a - log(sv) - ((double)P.zt[(int64_t)at * TOP + lane] - l2 * LN2));
   const double kl = wave_sum_d(t);
@@ -710,6 +700,62 @@ __global__ __launch_bounds__(256) void kd_loss_kernel(Head P) {
     P.rows[n] = F ? __builtin_nanf("") : (float)kl;
     if (P.status) P.status[n] = F;
     P.term[at] = (!F && w > 0.f) ? (double)w * kl : 0.0;
+  }
+}
+
+// The normaliser of each row from its tiles and the row's results.  Lanes take (row,
+// part of the tiles), waves take parts too, all joined in a fixed order; then one
+// thread per row, and for the distillation one wave per row.
+template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Head P, int tiles, int per) {
+  __shared__ float ms[16][64];
+  __shared__ double ss[16][64], l2s[64];
+  __shared__ int fs[64];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int M = P.counts[1], r0 = blockIdx.x * per;
+  if (r0 >= M) return;
+  const int r = lane & (per - 1), parts = 16 * (64 / per), q = wid * (64 / per) + lane / per;
+  const int at = r0 + r;
+  float m = NEG_INF;
+  double s = 0.0;
+  if (at < M)
+#pragma unroll 4
+    for (int t = q; t < tiles; t += parts) {
+      const float2 v = P.part[(int64_t)t * P.N + at];
+      join(m, s, v.x, (double)v.y);
+    }
+  for (int o = per; o < 64; o *= 2) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o));
+  if (lane < per) { ms[wid][r] = m; ss[wid][r] = s; }
+  __syncthreads();
+  if (threadIdx.x < (unsigned)per && at < M) {
+    m = ms[0][r];
+    s = ss[0][r];
+    for (int w = 1; w < 16; ++w) join(m, s, ms[w][r], ss[w][r]);
+    static_assert(SV_HEAD_NAN == SV_KD_NAN && SV_HEAD_POSINF == SV_KD_POSINF && SV_HEAD_EMPTY == SV_KD_EMPTY, "one set");
+    int F = !(m == m) ? SV_HEAD_NAN : m == __builtin_inff() ? SV_HEAD_POSINF : m == NEG_INF ? SV_HEAD_EMPTY : 0;
+    const double l2 = F ? 0.0 : (double)m + log2(s);
+    const int n = P.perm[at];
+    const float hi = (float)l2;
+    P.lse2[at] = hi;
+    float u;
+    if constexpr (KD) {
+      F |= P.flags[n];
+      l2s[r] = l2;
+      fs[r] = F;
+      u = P.w[n];
+    } else {
+      u = P.row_weight ? P.row_weight[n] : 1.f;
+      const double lse = l2 * LN2;
+      const float nll = F ? __builtin_nanf("") : (float)(lse - (double)P.zt[at]);
+      P.rows[n] = nll;
+      if (P.lse) P.lse[n] = F ? __builtin_nanf("") : (float)lse;
+      if (P.status) P.status[n] = F;
+      P.term[at] = (!F && u != 0.f) ? (double)u * (double)nll : 0.0;
+    }
+    if (P.grads) P.ga[at] = F ? 0.f : u * (float)(1.0 - (l2 - (double)hi) * LN2) * P.inv_t;
+  }
+  if constexpr (KD) {
+    __syncthreads();
+    for (int k = wid; k < per && r0 + k < M; k += 16) kd_row(P, r0 + k, P.perm[r0 + k], fs[k], l2s[k]);
   }
 }
 
@@ -781,11 +827,18 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   constexpr int E = Mma<DT>::E;
   const dim3 b256(256), b1024(1024);
   if (kd) hipLaunchKernelGGL(kd_rows_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
-  if (kd) hipLaunchKernelGGL((order_kernel<true>), dim3(1), b1024, 0, st, P);
-  else hipLaunchKernelGGL((order_kernel<false>), dim3(1), b1024, 0, st, P);
-  if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT>), dim3(P.N), b256, 0, st, P);
-  else hipLaunchKernelGGL((stage_rows_kernel<DT, DT>), dim3(P.N), b256, 0, st, P);
-  if (kd) hipLaunchKernelGGL((targets_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 4)), b256, 0, st, P);
+  const bool find = P.N <= FIND_ROWS;
+  auto stage = [&](auto KD) {
+    constexpr bool kd = decltype(KD)::value;
+    const dim3 rows(P.N);
+    if (!find) hipLaunchKernelGGL((order_kernel<kd>), dim3(1), b1024, 0, st, P);
+    if (P.h_scale && find) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, true>), rows, b256, 0, st, P);
+    else if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, false>), rows, b256, 0, st, P);
+    else if (find) hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, true>), rows, b256, 0, st, P);
+    else hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, false>), rows, b256, 0, st, P);
+  };
+  if (kd) stage(std::true_type());
+  else stage(std::false_type());
 
   Prod F = {};
   F.x = P.xs;
@@ -816,12 +869,8 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   int per = 1;                           // rows of a normaliser workgroup: 64, fewer when there are fewer
   while (per < 64 && per < P.N) per *= 2;
   const dim3 ng((unsigned)cdiv(P.N, per));
-  if (kd) {
-    hipLaunchKernelGGL((normaliser_kernel<true>), ng, b1024, 0, st, P, tiles, per);
-    hipLaunchKernelGGL(kd_loss_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
-  } else {
-    hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
-  }
+  if (kd) hipLaunchKernelGGL((normaliser_kernel<true>), ng, b1024, 0, st, P, tiles, per);
+  else hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
   hipLaunchKernelGGL((loss_kernel<DT>), dim3((unsigned)(P.gw ? L.Np * E / 16 + 1 : 1)), b256, 0, st, P);
   if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 
@@ -860,8 +909,10 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
       hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
     }
   }
+  constexpr int WS = T::BM == 256 ? 1 : 8;   // waves that share a row's sums: few with as many tiles as workgroups
   if (P.gh)
-    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)(X.mt * X.nt * T::NW * T::FM)), dim3(64), 0, st, P, X);
+    hipLaunchKernelGGL((dx_rows_kernel<DT, T, WS>), dim3((unsigned)(X.mt * X.nt * T::NW * T::FM)), dim3(64 * WS), 0, st,
+                       P, X);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

@@ -16,7 +16,7 @@ using namespace sv_gemm;
 using sv_head_host::cdiv;
 
 // codes * scale, in fp32, rounded once to the output's type: a wave takes a row,
-// each lane 8 codes at a time where rows are made of aligned eights.  HBM bound.
+// each lane the codes of a 16-byte store at a time where rows are aligned.  HBM bound.
 template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int8_t *codes, int64_t c_ld,
                                                                        const float *scale, char *y, int H, int N, int vec) {
   const int lane = threadIdx.x & 63;
@@ -25,23 +25,29 @@ template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int
   const int8_t *c = codes + n * c_ld;
   const float s = scale[n];
   if (vec) {
-    char *o = y + n * H * (DT == SV_F32 ? 4 : 2);
-    for (int q = lane; q < H / 8; q += 64) {
-      const u32x2 w = __builtin_nontemporal_load((const u32x2 *)c + q);
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)(w[k >> 2] >> (8 * (k & 3))) * s;
-      if constexpr (DT == SV_F32) {
-        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4 *)o + 2 * q);
-        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4 *)o + 2 * q + 1);
+    constexpr int W = DT == SV_F32 ? 4 : 8;              // codes of a 16-byte store
+    u32x4 *o = (u32x4 *)(y + n * H * (16 / W));
+    for (int q = lane; q < H / W; q += 64) {
+      uint32_t w[2];
+      if constexpr (W == 8) {
+        const u32x2 u = __builtin_nontemporal_load((const u32x2 *)c + q);
+        w[0] = u[0];
+        w[1] = u[1];
       } else {
-        u32x4 u;
+        w[0] = __builtin_nontemporal_load((const uint32_t *)c + q);
+      }
+      float v[W];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < W; ++k) v[k] = (float)(int8_t)(w[k >> 2] >> (8 * (k & 3))) * s;
+      u32x4 u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (W == 4) u[k] = __float_as_uint(v[k]);
+        else
           u[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
                  (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
-        __builtin_nontemporal_store(u, (u32x4 *)o + q);
       }
+      __builtin_nontemporal_store(u, o + q);
     }
   } else {
     for (int k = lane; k < H; k += 64) {

@@ -91,7 +91,8 @@ def _on(dev, stream):
     import torch
     if dev.type != "cuda":
         raise ValueError("tensors must live on the GPU")
-    cur = torch.cuda.current_stream(dev).cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # (a tenth of current_stream's time)
+    cur = raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
     if stream is None or stream == cur:
         return (_HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)), cur
     both = contextlib.ExitStack()
