@@ -12,6 +12,9 @@ namespace sv_act8 {
 
 using sv_dev::u32x4;
 
+// 16 bytes of a row, wherever it begins (the GPU takes 16-byte accesses at any address)
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
 template <int DT> struct In;
 template <> struct In<SV_BF16> {
   static constexpr int E = 2;
@@ -41,20 +44,23 @@ __device__ __forceinline__ int code_of(float x, float s) {
   return (int)fminf(fmaxf(r, -127.f), 127.f);
 }
 
-// Four codes of a row in one word, the usual way: x / s as a product with 1 / s that
-// is rounded to a whole number by adding 3 * 2^22, whose low byte is the code.  It may
-// be off by one next to a border: the remainder x - r s is exact in fp32 (a multiple of
-// half the scale's last place, and no larger than the scale), and `edge` is set where it
-// reaches half the scale; the caller then takes code_of.  (The division for every
-// element kept the row pass at 2.5 TB/s, bound by its arithmetic.)
+// Four codes of a row in one word: x / s as a product with 1 / s that is rounded to a
+// whole number by adding 3 * 2^22, whose low byte is the code.  It may be off by one
+// next to a border: the remainder x - r s is exact in fp32 (a multiple of half the
+// scale's last place, and no larger than the scale), and where it reaches half the
+// scale the code moves on, at half to the even one; FIX does that, and without it
+// `edge` tells whether it is needed.  (A division per element kept the row pass at
+// 2.5 TB/s, bound by its arithmetic; now 5.1.)
+template <bool FIX>
 __device__ __forceinline__ uint32_t four_codes(const float (&x)[4], float s, float inv, float half, bool &edge) {
   constexpr float MAGIC = 12582912.f;
   uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y = fmaf(x[i], inv, MAGIC);
-    edge |= fabsf(fmaf(-(y - MAGIC), s, x[i])) >= half;
+    const float y = fmaf(x[i], inv, MAGIC), e = fmaf(-(y - MAGIC), s, x[i]);
     q[i] = __float_as_uint(y);
+    if constexpr (FIX) q[i] += (e > half || (e == half && (q[i] & 1))) - (e < -half || (e == -half && (q[i] & 1)));
+    else edge |= fabsf(e) >= half;
   }
   const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(q[3], q[2], 0x0c0c0400);
   return lo | hi << 16;
@@ -78,8 +84,9 @@ struct Pack {
 
 // The largest magnitude (its bit pattern, as an integer maximum, keeps NaN and
 // infinity above every number), then the codes.  HBM bound.  A wave takes a row and
-// holds it in registers, REGS 16-byte vectors a lane, so it is read once; rows too
-// long for that, or not aligned, take a workgroup and a second read from the caches.
+// holds it in registers, REGS 16-byte vectors a lane (the last one may be short), so
+// it is read once; rows too long for that, or codes that four-byte stores do not fit,
+// take a workgroup and a second read from the caches.
 template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_kernel(Pack P, int N) {
   constexpr int E = In<DT>::E, W = 16 / E;
   const int lane = threadIdx.x & 63;
@@ -87,14 +94,16 @@ template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_ker
   if (n >= N) return;
   const char *x = P.x + n * P.x_ld;
   int8_t *c = P.codes + n * P.c_ld;
-  const int nv = P.H / W;                // (a whole number of vectors)
+  const int nv = P.H / W;                // whole vectors; up to W - 1 elements behind them, a lane each
   u32x4 v[REGS];
-  uint32_t top = 0;
 #pragma unroll
   for (int r = 0; r < REGS; ++r) {
     v[r] = 0;
-    if (r * 64 + lane < nv) v[r] = __builtin_nontemporal_load((const u32x4 *)x + r * 64 + lane);
+    if (r * 64 + lane < nv) v[r] = __builtin_nontemporal_load((const u32x4_any *)x + r * 64 + lane);
   }
+  const int k = nv * W + lane;
+  const float rest = k < P.H ? In<DT>::one(x + (int64_t)k * E) : 0.f;
+  uint32_t top = __float_as_uint(rest) & 0x7fffffffu;
 #pragma unroll
   for (int r = 0; r < REGS; ++r)
 #pragma unroll
@@ -105,34 +114,38 @@ template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_ker
   const float s = scale_of((uint32_t)sv_dev::wave_max_i((int)top));
   if (lane == 0) P.scale[n] = s;
   const bool none = !(s > 0.f);          // a row of zeros, of magnitudes whose scale rounds to 0, or NaN
-  const bool plain = s > 1e-30f;         // 1 / s and s / 2 are ordinary numbers
-  const float inv = plain ? 1.f / s : 0.f, half = 0.5f * s;
+  if (!(s > 1e-30f)) {                   // or one whose 1 / s or s / 2 is no ordinary number
+    for (int i = lane; i < P.Hp; i += 64)
+      c[i] = i < P.H && !none ? (int8_t)code_of(In<DT>::one(x + (int64_t)i * E), s) : (int8_t)0;
+    return;
+  }
+  const float inv = 1.f / s, half = 0.5f * s;
 #pragma unroll
   for (int r = 0; r < REGS; ++r) {
     const int q = r * 64 + lane;
     if (q >= nv) continue;
     uint32_t o[W / 4];
-    bool edge = !plain;
+    bool edge = false;
 #pragma unroll
     for (int w = 0; w < W / 4; ++w) {
-      float x[4];
+      float f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = In<DT>::of(v[r], 4 * w + i);
-      o[w] = four_codes(x, s, inv, half, edge);
+      for (int i = 0; i < 4; ++i) f[i] = In<DT>::of(v[r], 4 * w + i);
+      o[w] = four_codes<false>(f, s, inv, half, edge);
     }
     if (edge) {
 #pragma unroll
       for (int w = 0; w < W / 4; ++w) {
-        o[w] = 0;
+        float f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!none) o[w] |= (uint32_t)(code_of(In<DT>::of(v[r], 4 * w + i), s) & 0xff) << (8 * i);
+        for (int i = 0; i < 4; ++i) f[i] = In<DT>::of(v[r], 4 * w + i);
+        o[w] = four_codes<true>(f, s, inv, half, edge);
       }
     }
     if constexpr (W == 8) *(uint64_t *)(c + (int64_t)q * 8) = ((uint64_t)o[1] << 32) | o[0];
     else *(uint32_t *)(c + (int64_t)q * 4) = o[0];
   }
-  for (int i = P.H + lane; i < P.Hp; i += 64) c[i] = 0;
+  for (int i = k; i < P.Hp; i += 64) c[i] = i < P.H ? (int8_t)code_of(rest, s) : (int8_t)0;
 }
 
 template <int DT> __global__ __launch_bounds__(256) void pack_kernel(Pack P) {
@@ -182,19 +195,15 @@ template <int DT> __global__ __launch_bounds__(256) void pack_kernel(Pack P) {
     c[i] = (i < P.H && !none) ? (int8_t)code_of(In<DT>::one(x + (int64_t)i * E), s) : (int8_t)0;
 }
 
-inline bool pack_vec(int E, const void *x, int64_t x_ld, const void *c, int64_t c_ld) {
-  const int st = 16 / E;                 // bytes of codes of one vector
-  return ((uintptr_t)x & 15) == 0 && (x_ld & 15) == 0 && ((uintptr_t)c & (st - 1)) == 0 && (c_ld & (st - 1)) == 0;
-}
-
 template <int DT> void pack_as(int N, Pack P, hipStream_t st) {
   constexpr int E = In<DT>::E, W = 16 / E;
-  P.vec = pack_vec(E, P.x, P.x_ld, P.codes, P.c_ld) ? 1 : 0;
+  const bool codes = ((uintptr_t)P.codes & (W - 1)) == 0 && (P.c_ld & (W - 1)) == 0;
+  P.vec = codes && ((uintptr_t)P.x & 15) == 0 && (P.x_ld & 15) == 0 ? 1 : 0;
   const dim3 rows((unsigned)((N + 3) / 4)), block(256);
-  const int regs = P.H / W / 64 + (P.H % (W * 64) != 0);
-  if (P.vec && P.H % W == 0 && regs <= 4) hipLaunchKernelGGL((pack_rows_kernel<DT, 4>), rows, block, 0, st, P, N);
-  else if (P.vec && P.H % W == 0 && regs <= 16)
-    hipLaunchKernelGGL((pack_rows_kernel<DT, 16>), rows, block, 0, st, P, N);
+  if (codes && P.H <= 4 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 4>), rows, block, 0, st, P, N);
+  else if (DT == SV_BF16 && codes && P.H <= 8 * W * 64)
+    hipLaunchKernelGGL((pack_rows_kernel<DT, 8>), rows, block, 0, st, P, N);
+  else if (codes && P.H <= 16 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 16>), rows, block, 0, st, P, N);
   else hipLaunchKernelGGL((pack_kernel<DT>), dim3(N), block, 0, st, P);
 }
 

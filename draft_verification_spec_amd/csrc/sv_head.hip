@@ -241,14 +241,16 @@ template <bool KD> __global__ __launch_bounds__(1024) void order_kernel(Head P) 
 // all of them), which saves the order's launch.
 constexpr int FIND_ROWS = 1024;
 
-template <int HT, int DT, bool KD, bool FIND> __global__ __launch_bounds__(256) void stage_rows_kernel(Head P) {
+template <int HT, int DT, bool KD, bool FIND>
+__global__ __launch_bounds__(KD ? 1024 : 256) void stage_rows_kernel(Head P) {
+  constexpr int TPB = KD ? 1024 : 256, NW = TPB / 64;
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   int at = blockIdx.x, n = at;
   if constexpr (FIND) {
-    __shared__ int cnt[4][3];
+    __shared__ int cnt[NW][3];
     int bits, c[3] = {0, 0, 0};          // rows before this one, rows of class 0, of class 1
     const int k = class_of<KD>(P, n, bits);
-    for (int i = tid; i < P.N; i += 256) {
+    for (int i = tid; i < P.N; i += TPB) {
       int other;
       const int q = class_of<KD>(P, i, other);
       c[0] += q < k || (q == k && i < n);
@@ -262,7 +264,10 @@ template <int HT, int DT, bool KD, bool FIND> __global__ __launch_bounds__(256) 
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 3; ++q) c[q] = cnt[0][q] + cnt[1][q] + cnt[2][q] + cnt[3][q];
+    for (int q = 0; q < 3; ++q) {
+      c[q] = 0;
+      for (int w = 0; w < NW; ++w) c[q] += cnt[w][q];
+    }
     at = c[0];
     if (tid == 0) {
       P.perm[at] = n;
@@ -276,7 +281,7 @@ template <int HT, int DT, bool KD, bool FIND> __global__ __launch_bounds__(256) 
   }
   const char *src = P.hidden + (int64_t)n * P.h_ld;
   char *dst = P.xs + (int64_t)at * P.x_ld;
-  for (int k = tid; k < (int)P.Kp; k += 256) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
+  for (int k = tid; k < (int)P.Kp; k += TPB) store_real<DT>(dst, k, k < P.H ? load_real<HT>(src, k) : 0.f);
   const float alpha = HT == SV_I8 ? P.h_scale[n] * P.inv_t : P.inv_t;
   if (tid == 0) P.alpha[at] = alpha;
   if constexpr (KD) {
@@ -284,7 +289,7 @@ template <int HT, int DT, bool KD, bool FIND> __global__ __launch_bounds__(256) 
     constexpr int E = Mma<DT>::E, W = 16 / E;
     const bool vec = (((uintptr_t)P.weight | (uintptr_t)P.w_ld) & 15) == 0;
     const int nv = P.H / W;
-    for (int j = wid; j < TOP; j += 4) {
+    for (int j = wid; j < TOP; j += NW) {
       const int id = P.tidx[(int64_t)n * TOP + j];
       float s = 0.f;
       if (id >= 0 && id < P.V) {
@@ -670,6 +675,80 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   }
 }
 
+// dW where all rows fit one step (64 in bf16, 32 in fp32): bound by writing it.  A
+// wave keeps its 64 entries' dz in registers and runs along the hidden width, 64
+// columns at a time; blocks come straight from memory, each lane's 16 bytes being a
+// fragment's, so no LDS and no barrier stand between the stores (20000 x 1024 in
+// bf16: 18 us through the tiled product).
+template <int DT> __global__ __launch_bounds__(256) void dw_few_kernel(Head P, Prod G, int span) {
+  typedef typename Mma<DT>::Acc Acc;
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int nm = (G.M + 255) / 256, m0 = (blockIdx.x % nm) * 256 + (threadIdx.x >> 6) * 64;
+  const int c0 = blockIdx.x / nm * span, c1 = c0 + span < G.N ? c0 + span : G.N;
+  constexpr int Q = STEP / Mma<DT>::E;
+  const int halves = P.counts[0] > Q / 2 ? 2 : P.counts[0] > 0 ? 1 : 0;   // 64-byte half steps with rows in them
+  if (m0 >= G.M) return;
+  u32x4 x[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      x[h][f] = 0;                       // (dz has whole tiles of 256 entries)
+      if (h < halves) x[h][f] = *(const u32x4 *)(G.x + (h * 4 + q) * G.x_ld + (int64_t)(m0 + f * 16 + i) * 16);
+    }
+  // the column of index j of fragment g: four lanes' 16-byte stores make 64 bytes of a row
+  auto column = [](int g, int j) { return DT == SV_F32 ? g * 16 + j : g / 2 * 32 + j / 4 * 8 + g % 2 * 4 + j % 4; };
+  char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
+  for (int c = c0; c < c1; c += 64) {
+    Acc acc[4][4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) acc[f][g] = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h >= halves) break;
+      u32x4 y[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = c + column(g, i);
+        y[g] = *(const u32x4 *)(G.y + (h * 4 + q) * G.y_ld + (int64_t)(n < G.N ? n : G.N - 1) * 16);
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) Mma<DT>::mul(acc[f][g], y[g], x[h][f]);
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int m = m0 + f * 16 + i;
+      if (m >= G.M) continue;
+      const int64_t row = (int64_t)m * P.H;
+      if (G.vec && c + 64 <= G.N) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 a = acc[f][g];
+          if constexpr (DT == SV_F32) {
+            *(f32x4 *)(out + (row + c + column(g, 4 * q)) * 4) = a;
+          } else if (g % 2 == 0) {
+            const f32x4 b = acc[f][g + 1];
+            *(u32x4 *)(out + (row + c + column(g, 4 * q)) * 2) =
+                u32x4{pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
+          }
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int n = c + column(g, 4 * q + r);
+            if (n < G.N) store_real<DT>(out, row + n, acc[f][g][r]);
+          }
+      }
+    }
+  }
+}
+
 // -------------------------------------------------------------- rows' results
 // (m, s) of two parts of a row: the maximum in base 2 and the sum of 2^(. - m).  A NaN
 // maximum stays; one of -infinity has no terms.
@@ -813,6 +892,7 @@ static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile
 typedef Tile<8, 4, 2, 4> Big;            // 256 x 256
 typedef Tile<4, 4, 2, 2> Mid;            // 128 x 128
 typedef Tile<2, 2, 1, 4> Few;            // 32 x 128
+typedef Tile<1, 2, 2, 2> Narrow;         // 32 x 64
 
 template <class T> Prod tiled(Prod G, int64_t M, int64_t N) {
   G.M = (int32_t)M;
@@ -823,19 +903,19 @@ template <class T> Prod tiled(Prod G, int64_t M, int64_t N) {
   return G;
 }
 
-template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, bool kd, bool direct, hipStream_t st) {
+template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, const Plan &L, bool kd, bool direct, hipStream_t st) {
   constexpr int E = Mma<DT>::E;
   const dim3 b256(256), b1024(1024);
   if (kd) hipLaunchKernelGGL(kd_rows_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
   const bool find = P.N <= FIND_ROWS;
   auto stage = [&](auto KD) {
     constexpr bool kd = decltype(KD)::value;
-    const dim3 rows(P.N);
+    const dim3 rows(P.N), block(kd ? 1024 : 256);
     if (!find) hipLaunchKernelGGL((order_kernel<kd>), dim3(1), b1024, 0, st, P);
-    if (P.h_scale && find) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, true>), rows, b256, 0, st, P);
-    else if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, false>), rows, b256, 0, st, P);
-    else if (find) hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, true>), rows, b256, 0, st, P);
-    else hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, false>), rows, b256, 0, st, P);
+    if (P.h_scale && find) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, true>), rows, block, 0, st, P);
+    else if (P.h_scale) hipLaunchKernelGGL((stage_rows_kernel<SV_I8, DT, kd, false>), rows, block, 0, st, P);
+    else if (find) hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, true>), rows, block, 0, st, P);
+    else hipLaunchKernelGGL((stage_rows_kernel<DT, DT, kd, false>), rows, block, 0, st, P);
   };
   if (kd) stage(std::true_type());
   else stage(std::false_type());
@@ -860,10 +940,10 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   int tiles = 0;
   for (int64_t v0 = 0; v0 < P.V; v0 += fstep) {
     const int64_t cnt = P.V - v0 < fstep ? P.V - v0 : fstep;
-    Prod G = tiled<T>(F, P.N, cnt);
+    Prod G = tiled<TS>(F, P.N, cnt);
     weight_piece(G, v0, cnt);
     G.tile0 = tiles;
-    hipLaunchKernelGGL((stats_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
+    hipLaunchKernelGGL((stats_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
     tiles += G.nt;
   }
   int per = 1;                           // rows of a normaliser workgroup: 64, fewer when there are fewer
@@ -885,10 +965,10 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
   for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
-    Prod G = tiled<T>(F, L.Np, cp);
+    Prod G = tiled<TS>(F, L.Np, cp);
     weight_piece(G, v0, cnt);
     G.N = (int32_t)cnt;
-    hipLaunchKernelGGL((dz_kernel<DT, T>), dim3((unsigned)(G.mt * G.nt)), dim3(T::TPB), 0, st, P, G);
+    hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
     if (kd) hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 256)), b256, 0, st, P, G);
     if (P.gh) {
       X.y = G.y;
@@ -906,7 +986,14 @@ template <int DT, class T, class TW> int enqueue(const Head &P, const Plan &L, b
       W.y = P.xw;
       W.y_ld = L.xw_ld;
       W.vec = P.H % 4 == 0 && ((uintptr_t)P.gw & 15) == 0;
-      hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
+      if (L.Np * E == STEP) {            // (columns in parts that give every CU a few workgroups)
+        W.vec = P.H * E % 16 == 0 && ((uintptr_t)P.gw & 15) == 0;
+        const int64_t parts = cdiv(1024, cdiv(cnt, 256)), span = sv_head_host::up(cdiv(P.H, parts), 64);
+        hipLaunchKernelGGL((dw_few_kernel<DT>), dim3((unsigned)(cdiv(cnt, 256) * cdiv(P.H, span))), b256, 0, st, P, W,
+                           (int)span);
+      } else {
+        hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
+      }
     }
   }
   constexpr int WS = T::BM == 256 ? 1 : 8;   // waves that share a row's sums: few with as many tiles as workgroups
@@ -960,13 +1047,16 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.acc = (float *)(ws + L.acc);
   const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
   // tiles by the number of rows: 256 rows a tile read each operand least; fewer
-  // rows than a tile would be multiplied in vain.  fp32 holds two sets of sums,
+  // rows than a tile would be multiplied in vain, and where 128 columns a tile leave
+  // CUs without one, 64 do (24 x 1024 x 20000: 10.2 to 7 us).  fp32 holds two sets of sums,
   // and its matrix rate leaves time to read 128-row tiles
   if (s.dtype == SV_BF16)
     return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
            : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
+           : L.narrow    ? enqueue<SV_BF16, Few, Mid, Narrow>(P, L, kd, direct, st)
                          : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
   return L.bm == 128 ? enqueue<SV_F32, Mid, Mid>(P, L, kd, direct, st)
+         : L.narrow  ? enqueue<SV_F32, Few, Mid, Narrow>(P, L, kd, direct, st)
                      : enqueue<SV_F32, Few, Mid>(P, L, kd, direct, st);
 }
 

@@ -95,6 +95,7 @@ struct Plan {
   int64_t x_ld, dz_ld;                   // bytes between copied rows (of hidden and weight), rows of dz
   int64_t xw_ld, dzw_ld;                 // the same for dW's operands, rows of 16-byte blocks
   int bm, bn;                            // tile of the products
+  bool narrow;                           // tiles of 64 columns against the weight's rows
   int groups, slots;                     // workgroups of the hidden gradient, tiles each may touch
   // workspace sections
   size_t counts, perm, alpha, ga, lse2, w, flags, zt, pt, term, part, xs, xw, dz, dzw, wt, acc, total;
@@ -128,6 +129,7 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.Np = up(N, q);
   p.bm = N <= 32 ? 32 : (N < 192 || s->dtype == SV_F32) ? 128 : 256;
   p.bn = p.bm == 256 ? 256 : 128;
+  p.narrow = p.bm == 32 && s->V < 2 * CUS * 128;
   // A piece: its dz, for dx and for dW, and a copied weight take PIECE bytes together;
   // a whole number of 256 entries, all pieces alike.  More pays a little (4096 rows,
   // 4096 x 151936 in bf16: 13.2 ms with 256 MB, 12.8 with 640, 12.6 with 1280, for
@@ -161,7 +163,7 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.zt = take(N * T * 4);
   p.pt = take(kd ? N * T * 4 : 0);
   p.term = take(N * 8);
-  p.part = take((size_t)cdiv(s->V, 128) * N * 8);
+  p.part = take((size_t)cdiv(s->V, p.narrow ? 64 : 128) * N * 8);
   p.x_ld = spread(p.Kp * e);
   p.dz_ld = spread(p.piece * e);
   p.xs = take((size_t)p.Np * p.x_ld);

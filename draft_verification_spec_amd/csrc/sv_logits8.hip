@@ -26,7 +26,7 @@ template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int
   const float s = scale[n];
   if (vec) {
     constexpr int W = DT == SV_F32 ? 4 : 8;              // codes of a 16-byte store
-    u32x4 *o = (u32x4 *)(y + n * H * (16 / W));
+    sv_act8::u32x4_any *o = (sv_act8::u32x4_any *)(y + n * H * (16 / W));
     for (int q = lane; q < H / W; q += 64) {
       uint32_t w[2];
       if constexpr (W == 8) {
@@ -48,6 +48,11 @@ template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int
                  (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
       }
       __builtin_nontemporal_store(u, o + q);
+    }
+    for (int k = H / W * W + lane; k < H; k += 64) {
+      const float v = (float)c[k] * s;
+      if constexpr (DT == SV_F32) ((float *)y)[n * H + k] = v;
+      else ((__bf16 *)y)[n * H + k] = (__bf16)v;
     }
   } else {
     for (int k = lane; k < H; k += 64) {
@@ -154,7 +159,7 @@ extern "C" int sv_act8_unpack(int32_t N, int32_t H, const int8_t *codes, int64_t
   const int rc = sv_head_host::check_act8(N, H, y_dtype, y, 0, codes, codes_stride, scale);
   if (rc != SV_OK || N == 0) return rc;
   const int64_t ld = codes_stride ? codes_stride : H;
-  const int vec = H % 8 == 0 && ld % 8 == 0 && ((uintptr_t)codes & 7) == 0 && ((uintptr_t)y & 15) == 0;
+  const int vec = ld % 8 == 0 && ((uintptr_t)codes & 7) == 0;
   const dim3 grid((unsigned)cdiv(N, 4)), block(256);
   if (y_dtype == SV_BF16)
     hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H, N,
