@@ -85,6 +85,7 @@ struct Head {
   int64_t Kp, Np;
   int64_t x_ld, dz_ld;                   // bytes between rows of xs, of dz
   int64_t xw_ld, dzw_ld;                 // bytes between rows of blocks
+  int32_t keep;                          // the forward product leaves its logits in dz (fp32, one piece)
   const char *hidden;
   int64_t h_ld;                          // bytes
   const float *h_scale;
@@ -364,6 +365,12 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
       }
     m = sv_dev::fmax_nan(m, __shfl_xor(m, 16));
     m = sv_dev::fmax_nan(m, __shfl_xor(m, 32));
+    if constexpr (DT == SV_F32) {
+      if (P.keep && m0 + r < M)
+#pragma unroll
+        for (int g = 0; g < T::FN; ++g)
+          *(f32x4 *)(P.dz + (m0 + r) * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4) * 4) = acc[f][g];
+    }
     const float hi = m == NEG_INF ? NEG_INF : m * LOG2E, ref = hi == NEG_INF ? 0.f : hi;
     float s = 0.f;
 #pragma unroll
@@ -504,6 +511,40 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
       }
     }
   }
+}
+
+// The same from logits that the forward product kept: fp32 products are slow enough
+// (154 TFLOP/s) that a piece's logits are worth their memory where the piece is all of
+// the vocabulary.  A thread takes 4 rows x 4 columns.
+__global__ __launch_bounds__(256) void dz_kept_kernel(Head P, Prod G) {
+  const int M = P.counts[0], Mp = (M + 31) / 32 * 32;
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 4, r0 = blockIdx.x * 4;
+  if (r0 >= Mp || c >= G.M) return;      // (G.M: columns in whole tiles)
+  f32x4 w[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int m = r0 + r;
+    const bool on = m < M;
+    const float l2 = on ? P.lse2[m] : 0.f, ga = on ? P.ga[m] : 0.f;
+    const int row = on ? P.perm[m] : 0;
+    const float s = P.h_scale && on && ga != 0.f ? P.h_scale[row] : 1.f;
+    const int64_t t = P.T == 1 && on ? P.targets[row] : -1;
+    const float u = P.T == 1 && on ? (P.row_weight ? P.row_weight[row] : 1.f) * P.inv_t : 0.f;
+    f32x4 *z = (f32x4 *)(P.dz + m * P.dz_ld + (int64_t)c * 4);
+    f32x4 v = 0;
+    if (ga != 0.f) v = *z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(v[i], LOG2E, -l2)), ga, c + i == t ? -u : 0.f);
+      v[i] = c + i < G.N && ga != 0.f ? d : 0.f;
+    }
+    *z = v;
+    w[r] = v * s;
+  }
+  if (P.gw)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *(f32x4 *)(P.dzw + (r0 >> 2) * P.dzw_ld + (int64_t)(c + i) * 16) = f32x4{w[0][i], w[1][i], w[2][i], w[3][i]};
 }
 
 // Distillation: dz at the stored entries of a piece, u (q - pt), from the entries' own
@@ -888,9 +929,12 @@ template <int DT> __global__ __launch_bounds__(256) void copy_weight_kernel(cons
 }
 
 // ------------------------------------------------------------------------ host
-static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile<2, 2, 1, 4>::BM == 32, "plan_for's bm");
+static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile<2, 2, 2, 2>::BM == 64 &&
+                  Tile<2, 2, 1, 4>::BM == 32,
+              "plan_for's bm");
 typedef Tile<8, 4, 2, 4> Big;            // 256 x 256
 typedef Tile<4, 4, 2, 2> Mid;            // 128 x 128
+typedef Tile<2, 2, 2, 2> Square;         // 64 x 64
 typedef Tile<2, 2, 1, 4> Few;            // 32 x 128
 typedef Tile<1, 2, 2, 2> Narrow;         // 32 x 64
 
@@ -966,9 +1010,14 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
     Prod G = tiled<TS>(F, L.Np, cp);
-    weight_piece(G, v0, cnt);
+    if (!P.keep || P.gh) weight_piece(G, v0, cnt);
     G.N = (int32_t)cnt;
-    hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
+    if (P.keep) {
+      G.M = (int32_t)cp;
+      hipLaunchKernelGGL(dz_kept_kernel, dim3((unsigned)(L.Np / 4), (unsigned)cdiv(cp, 1024)), b256, 0, st, P, G);
+    } else {
+      hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
+    }
     if (kd) hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 256)), b256, 0, st, P, G);
     if (P.gh) {
       X.y = G.y;
@@ -1018,6 +1067,7 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.Kp = L.Kp;
   P.x_ld = L.x_ld;
   P.dz_ld = L.dz_ld;
+  P.keep = L.keep;
   P.Np = L.Np;
   P.hidden = (const char *)hidden;
   P.h_ld = (s.hidden_stride ? s.hidden_stride : s.H) * (int64_t)he;
@@ -1048,16 +1098,16 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
   // tiles by the number of rows: 256 rows a tile read each operand least; fewer
   // rows than a tile would be multiplied in vain, and where 128 columns a tile leave
-  // CUs without one, 64 do (24 x 1024 x 20000: 10.2 to 7 us).  fp32 holds two sets of sums,
-  // and its matrix rate leaves time to read 128-row tiles
+  // CUs without one, 64 do (24 x 1024 x 20000: dz 12.3 to 10.8 us).  The fp32 matrix
+  // rate leaves time to read 64 x 64 tiles, which fill the chip sooner.
   if (s.dtype == SV_BF16)
     return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
            : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
            : L.narrow    ? enqueue<SV_BF16, Few, Mid, Narrow>(P, L, kd, direct, st)
                          : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
-  return L.bm == 128 ? enqueue<SV_F32, Mid, Mid>(P, L, kd, direct, st)
-         : L.narrow  ? enqueue<SV_F32, Few, Mid, Narrow>(P, L, kd, direct, st)
-                     : enqueue<SV_F32, Few, Mid>(P, L, kd, direct, st);
+  return L.bm == 64 ? enqueue<SV_F32, Square, Square>(P, L, kd, direct, st)
+         : L.narrow ? enqueue<SV_F32, Few, Square, Narrow>(P, L, kd, direct, st)
+                    : enqueue<SV_F32, Few, Square>(P, L, kd, direct, st);
 }
 
 }  // namespace

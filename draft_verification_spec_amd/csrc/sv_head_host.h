@@ -95,6 +95,7 @@ struct Plan {
   int64_t x_ld, dz_ld;                   // bytes between copied rows (of hidden and weight), rows of dz
   int64_t xw_ld, dzw_ld;                 // the same for dW's operands, rows of 16-byte blocks
   int bm, bn;                            // tile of the products
+  bool keep;                             // the forward product's logits stay in dz (fp32, one piece)
   bool narrow;                           // tiles of 64 columns against the weight's rows
   int groups, slots;                     // workgroups of the hidden gradient, tiles each may touch
   // workspace sections
@@ -127,8 +128,8 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   const int64_t N = s->N, H = s->H, T = kd ? TOP : 1;
   p.Kp = up(H, q);
   p.Np = up(N, q);
-  p.bm = N <= 32 ? 32 : (N < 192 || s->dtype == SV_F32) ? 128 : 256;
-  p.bn = p.bm == 256 ? 256 : 128;
+  p.bm = N <= 32 ? 32 : s->dtype == SV_F32 ? 64 : N < 192 ? 128 : 256;
+  p.bn = p.bm == 32 ? 128 : p.bm;
   p.narrow = p.bm == 32 && s->V < 2 * CUS * 128;
   // A piece: its dz, for dx and for dW, and a copied weight take PIECE bytes together;
   // a whole number of 256 entries, all pieces alike.  More pays a little (4096 rows,
@@ -142,10 +143,11 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.pieces = cdiv(s->V, most);
   p.piece = up(cdiv(s->V, p.pieces), 256);
   p.pieces = cdiv(s->V, p.piece);
+  p.keep = s->grads && s->dtype == SV_F32 && p.pieces == 1;
   // the hidden gradient's workgroups: as many as run at once (LDS: one tile of
-  // 256, two of 128, four of 32 rows a CU), fewer where a run would be short
+  // 256, two of 128 or 32, four of 64 rows a CU), fewer where a run would be short
   const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), full = p.piece * e / STEP;
-  int64_t g = CUS * (p.bm == 256 ? 1 : p.bm == 128 ? 2 : 4);
+  int64_t g = CUS * (p.bm == 256 ? 1 : p.bm == 64 ? 4 : 2);
   if (g > cdiv(tiles * full, RUN)) g = cdiv(tiles * full, RUN);
   p.groups = (int)(g < 1 ? 1 : g);
   const int64_t run = cdiv(tiles * full, p.groups);
@@ -163,14 +165,14 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.zt = take(N * T * 4);
   p.pt = take(kd ? N * T * 4 : 0);
   p.term = take(N * 8);
-  p.part = take((size_t)cdiv(s->V, p.narrow ? 64 : 128) * N * 8);
+  p.part = take((size_t)cdiv(s->V, p.narrow || p.bm == 64 ? 64 : 128) * N * 8);
   p.x_ld = spread(p.Kp * e);
   p.dz_ld = spread(p.piece * e);
   p.xs = take((size_t)p.Np * p.x_ld);
   p.xw_ld = spread(p.Kp * 16);
   p.dzw_ld = spread(p.piece * 16);
   p.xw = take(gw ? (size_t)(p.Np * e / 16) * p.xw_ld : 0);
-  p.dz = take(gh ? (size_t)p.Np * p.dz_ld : 0);
+  p.dz = take(gh || p.keep ? (size_t)p.Np * p.dz_ld : 0);
   p.dzw = take(gw ? (size_t)(p.Np * e / 16) * p.dzw_ld : 0);
   p.wt = take((size_t)p.piece * p.x_ld);
   p.acc = take(gh ? (size_t)p.groups * p.slots * p.bm * p.bn * 4 : 0);

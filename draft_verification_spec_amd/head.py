@@ -123,7 +123,11 @@ def _scales(s, shape, dev, what):
 
 def _scratch(workspace, nbytes, dev):
     import torch
-    return workspace if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 memory on the tensors' device")
+    return workspace
 
 
 def act8_pack(x, *, stream=None) -> Act8:

@@ -429,6 +429,74 @@ def test_kd_agrees_with_logits_form(sv):
     within(b.grad_hidden, want, 1e-4, "grad_hidden")
 
 
+def test_stored_row_that_was_not_finite(sv):
+    """A row packed with a NaN in it has scale NaN: the losses report that row and
+    leave it out of both gradients."""
+    g = gen(71)
+    x = torch.randn(40, 96, generator=g, device="cuda")
+    x[7, 3] = float("nan")
+    w = torch.randn(300, 96, generator=g, device="cuda").to(BF)
+    t = torch.randint(0, 300, (40,), generator=g, device="cuda")
+    r = sv.head_ce(sv.act8_pack(x), w, t)
+    keep = torch.arange(40, device="cuda") != 7
+    assert r.status.tolist() == [sv.HEAD_NAN if i == 7 else 0 for i in range(40)]
+    assert torch.isnan(r.nll[7]) and torch.isfinite(r.loss).all()
+    s = sv.head_ce(sv.act8_pack(x[keep]), w, t[keep])
+    assert torch.equal(s.nll, r.nll[keep]) and not r.grad_hidden[7].any()
+    within(r.grad_weight, s.grad_weight.double(), 4 * HALF[BF] * s.grad_weight.double().abs().amax(), "grad_weight")
+
+
+def test_head_beyond_32_bits(sv):
+    """A head of more than 2^32 bytes, and int8 codes of as many: offsets of its last
+    rows, checked piece by piece."""
+    h, v = 4096, 560000                               # 4.6 GB in bf16
+    g = gen(81)
+    w = torch.empty(v, h, dtype=BF, device="cuda")
+    for i in range(0, v, 70000):
+        w[i:i + 70000] = (torch.randn(70000, h, generator=g, device="cuda") * 0.04).to(BF)
+    x = torch.randn(3, h, generator=g, device="cuda").to(BF)
+    t = torch.tensor([v - 1, 5, v - 70000], device="cuda")
+    log("head_ce over a 4.6 GB head")
+    r = sv.head_ce(x, w, t)
+    z = torch.cat([(x.float() @ w[i:i + 70000].float().T).double() for i in range(0, v, 70000)], 1)
+    lse = torch.logsumexp(z, 1)
+    at = z.gather(1, t[:, None])[:, 0]
+    # fp32 sums of 4096 terms on both sides: 2 * 4096 * 2^-24 of their magnitudes (about 4096 * 0.8 * 0.032)
+    e = 2 * h * 2.0 ** -24 * 4096 * 0.8 * 0.032 + 1e-5
+    within(r.nll, lse - at, e, "nll")
+    d = torch.exp(z - lse[:, None])
+    d[torch.arange(3), t] -= 1
+    for i in (0, v - 70000):
+        want = d[:, i:i + 70000].T @ x.double()
+        tol = (2 * e + 2 * HALF[BF]) * (d[:, i:i + 70000].abs().T @ x.double().abs()) + 1e-12
+        within(r.grad_weight[i:i + 70000], want, tol, "grad_weight")
+    want = sum(d[:, i:i + 70000] @ w[i:i + 70000].double() for i in range(0, v, 70000))
+    size = sum(d[:, i:i + 70000].abs() @ w[i:i + 70000].double().abs() for i in range(0, v, 70000))
+    within(r.grad_hidden, want, (2 * e + 2 * HALF[BF]) * size, "grad_hidden")
+    del r, d, z, w
+    v = 1100000                                       # 4.5 GB of codes
+    codes = torch.randint(-127, 128, (v, h), generator=g, device="cuda", dtype=torch.int8)
+    scale = torch.rand(v, generator=g, device="cuda")
+    log("head_logits over 4.5 GB of codes")
+    a = sv.act8_pack(x)
+    y = sv.head_logits(a, sv.Act8(codes, scale), out_dtype=F)
+    for i in (0, v - 50000):
+        want = (a.codes.double() @ codes[i:i + 50000].double().T) * a.scale.double()[:, None] * scale[i:i + 50000].double()
+        within(y[:, i:i + 50000], want, want.abs() * 4 * HALF[F], "logits")
+
+
+@pytest.mark.parametrize("n", [32, 33, 64, 65, 191, 192, 256, 1024, 1025])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_ce_at_the_borders_of_the_rules(sv, n, dtype):
+    """The row counts where tiles, the order of rows and dW change their form, with
+    most rows left out: a front part that ends anywhere in a tile."""
+    log(f"head_ce border n={n} {dtype}")
+    hidden, x, w, t, u = ce_case(sv, n, 136, 777, dtype, "same", 1.0, n)
+    t[n // 7::3] = -1
+    t[n // 3::2] = -1
+    check_ce(sv, hidden, x, w, t, u, 1.0, dtype)
+
+
 # ------------------------------------------------- as a program uses them together
 def test_deterministic_and_streams(sv):
     """The same bits again, on another stream, and beside another call that runs
@@ -459,6 +527,8 @@ def test_own_workspace(sv):
     assert (buf[need:] == 0xff).all()
     with pytest.raises(sv.SpecVerifyError):
         sv.head_ce(hidden, w, t, u, workspace=buf[:need - 256])
+    with pytest.raises(ValueError):
+        sv.head_ce(hidden, w, t, u, workspace=torch.empty(need, dtype=torch.uint8))
 
 
 def test_rollout_step_together(sv):
@@ -540,3 +610,25 @@ def test_graph_replays(sv, op):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b), (op, seed)
+
+
+def test_two_graphs_take_turns(sv):
+    """Two captured calls of different shapes, replayed in turn and with eager calls
+    between: neither disturbs the other's scratch or results."""
+    a, b = (ce_case(sv, n, 128, v, BF, "same", 1.0, n) for n, v in ((40, 900), (300, 1500)))
+    call = lambda c: list(sv.head_ce(c[0], c[2], c[3], c[4]))  # noqa: E731
+    want = [call(a), call(b)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in (a, b):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(c))
+        graphs.append(graph)
+    for turn in range(3):
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        call(b)
+        torch.cuda.synchronize()
+        for out, ref in zip(outs, want):
+            assert all(torch.equal(p, q) for p, q in zip(out, ref)), turn
