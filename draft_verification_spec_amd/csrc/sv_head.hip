@@ -1054,7 +1054,8 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
 
 int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const float *hidden_scale, const void *weight,
         void *gh, void *gw, void *workspace, hipStream_t st) {
-  const Plan L = sv_head_host::plan_for(&s, kd);
+  const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
+  const Plan L = sv_head_host::plan_for(&s, kd, direct);
   char *ws = (char *)workspace;
   const int he = sv_head_host::esize(s.hidden_dtype);
   P.N = s.N;
@@ -1095,7 +1096,6 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.dzw_ld = L.dzw_ld;
   P.wt = ws + L.wt;
   P.acc = (float *)(ws + L.acc);
-  const bool direct = sv_head_host::weight_direct(&s, (uintptr_t)weight);
   // tiles by the number of rows: 256 rows a tile read each operand least; fewer
   // rows than a tile would be multiplied in vain, and where 128 columns a tile leave
   // CUs without one, 64 do (24 x 1024 x 20000: dz 12.3 to 10.8 us).  The fp32 matrix
@@ -1114,12 +1114,12 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
 
 extern "C" size_t sv_head_ce_workspace_bytes(const sv_head_shape_t *s) {
   if (!s || !sv_head_host::head_shape_ok(s, false)) return 0;
-  return sv_head_host::plan_for(s, false).total;
+  return sv_head_host::head_bytes(s, false);
 }
 
 extern "C" size_t sv_head_kd_workspace_bytes(const sv_head_shape_t *s) {
   if (!s || !sv_head_host::head_shape_ok(s, true)) return 0;
-  return sv_head_host::plan_for(s, true).total;
+  return sv_head_host::head_bytes(s, true);
 }
 
 extern "C" int sv_head_ce(const sv_head_shape_t *shape, const void *hidden, const float *hidden_scale,

@@ -122,7 +122,8 @@ inline bool weight_direct(const sv_head_shape_t *s, uintptr_t base) {
   return (s->H * e) % STEP == 0 && ld % 16 == 0 && ld <= MAX_LD && base % 16 == 0;
 }
 
-inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
+// direct: the weight is read where it lies, else copied a piece at a time.
+inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   Plan p;
   const int e = p.e = esize(s->dtype), q = STEP / e;
   const int64_t N = s->N, H = s->H, T = kd ? TOP : 1;
@@ -133,9 +134,11 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.narrow = p.bm == 32 && s->V < 2 * CUS * 128;
   // A piece: its dz, for dx and for dW, and a copied weight take PIECE bytes together;
   // a whole number of 256 entries, all pieces alike.  More pays a little (4096 rows,
-  // 4096 x 151936 in bf16: 13.2 ms with 256 MB, 12.8 with 640, 12.6 with 1280, for
-  // fewer passes over the sums of dx), but the logits in fp32 would be 2.5 GB.
-  const int64_t per = (s->grads ? 2 * p.Np * e : 0) + p.Kp * e;
+  // 4096 x 151936 in bf16, with the weight counted too: 13.2 ms with 256 MB, 12.8 with
+  // 640, 12.6 with 1280, for fewer passes over the sums of dx and fewer last rounds of
+  // tiles), but the logits in fp32 would be 2.5 GB.
+  int64_t per = (s->grads ? 2 * p.Np * e : 0) + (direct ? 0 : p.Kp * e);
+  if (per < 16) per = 16;
   int64_t most = PIECE / per / 256 * 256;
   if (most < 256) most = 256;
   const int64_t by_ld = MAX_LD / 16 - 8;           // rows of blocks (and a line more)
@@ -174,10 +177,18 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd) {
   p.xw = take(gw ? (size_t)(p.Np * e / 16) * p.xw_ld : 0);
   p.dz = take(gh || p.keep ? (size_t)p.Np * p.dz_ld : 0);
   p.dzw = take(gw ? (size_t)(p.Np * e / 16) * p.dzw_ld : 0);
-  p.wt = take((size_t)p.piece * p.x_ld);
+  p.wt = take(direct ? 0 : (size_t)p.piece * p.x_ld);
   p.acc = take(gh ? (size_t)p.groups * p.slots * p.bm * p.bn * 4 : 0);
   p.total = o;
   return p;
+}
+
+// What a call may need: the copying plan where the weight's address decides.
+inline size_t head_bytes(const sv_head_shape_t *s, bool kd) {
+  const size_t copied = plan_for(s, kd, false).total;
+  if (!weight_direct(s, 0)) return copied;
+  const size_t direct = plan_for(s, kd, true).total;
+  return direct > copied ? direct : copied;
 }
 
 inline int check_head(const sv_head_shape_t *s, bool kd, const void *hidden, const void *hidden_scale,
@@ -192,7 +203,7 @@ inline int check_head(const sv_head_shape_t *s, bool kd, const void *hidden, con
   if (!hidden || !weight || !a || !rows || !loss || (s->hidden_dtype == SV_I8 && !hidden_scale)) return SV_ERR_NULL;
   if (kd && (!b || !c || !d)) return SV_ERR_NULL;
   if (((s->grads & SV_GRAD_HIDDEN) && !gh) || ((s->grads & SV_GRAD_WEIGHT) && !gw)) return SV_ERR_NULL;
-  if (!ws || wsb < plan_for(s, kd).total || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
+  if (!ws || wsb < head_bytes(s, kd) || ((uintptr_t)ws & 255)) return SV_ERR_WORKSPACE;
   return SV_OK;
 }
 
