@@ -83,14 +83,16 @@ struct Pack {
 };
 
 // The largest magnitude (its bit pattern, as an integer maximum, keeps NaN and
-// infinity above every number), then the codes.  HBM bound.  A wave takes a row and
-// holds it in registers, REGS 16-byte vectors a lane (the last one may be short), so
-// it is read once; rows too long for that, or codes that four-byte stores do not fit,
-// take a workgroup and a second read from the caches.
-template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_kernel(Pack P, int N) {
-  constexpr int E = In<DT>::E, W = 16 / E;
-  const int lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+// infinity above every number), then the codes.  HBM bound.  A wave takes a row, or
+// the four of a workgroup do where there are too few rows to fill the chip with (32
+// rows of 4096: 8.4 to 4 us); they hold it in registers, REGS 16-byte vectors a lane,
+// so it is read once.  Rows too long for that, or codes that four-byte stores do not
+// fit, take a workgroup and a second read from the caches.
+template <int DT, int REGS, int WAVES> __global__ __launch_bounds__(256) void pack_rows_kernel(Pack P, int N) {
+  constexpr int E = In<DT>::E, W = 16 / E, L = 64 * WAVES;
+  static_assert(WAVES == 1 || WAVES == 4, "a wave or a workgroup per row");
+  const int lane = threadIdx.x % L;
+  const int64_t n = WAVES == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (n >= N) return;
   const char *x = P.x + n * P.x_ld;
   int8_t *c = P.codes + n * P.c_ld;
@@ -99,7 +101,7 @@ template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_ker
 #pragma unroll
   for (int r = 0; r < REGS; ++r) {
     v[r] = 0;
-    if (r * 64 + lane < nv) v[r] = __builtin_nontemporal_load((const u32x4_any *)x + r * 64 + lane);
+    if (r * L + lane < nv) v[r] = __builtin_nontemporal_load((const u32x4_any *)x + r * L + lane);
   }
   const int k = nv * W + lane;
   const float rest = k < P.H ? In<DT>::one(x + (int64_t)k * E) : 0.f;
@@ -111,18 +113,26 @@ template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_ker
       const uint32_t u = __float_as_uint(In<DT>::of(v[r], i)) & 0x7fffffffu;
       top = u > top ? u : top;
     }
-  const float s = scale_of((uint32_t)sv_dev::wave_max_i((int)top));
+  top = (uint32_t)sv_dev::wave_max_i((int)top);
+  if constexpr (WAVES == 4) {
+    __shared__ uint32_t tops[4];
+    if ((lane & 63) == 0) tops[lane >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = tops[w] > top ? tops[w] : top;
+  }
+  const float s = scale_of(top);
   if (lane == 0) P.scale[n] = s;
   const bool none = !(s > 0.f);          // a row of zeros, of magnitudes whose scale rounds to 0, or NaN
   if (!(s > 1e-30f)) {                   // or one whose 1 / s or s / 2 is no ordinary number
-    for (int i = lane; i < P.Hp; i += 64)
+    for (int i = lane; i < P.Hp; i += L)
       c[i] = i < P.H && !none ? (int8_t)code_of(In<DT>::one(x + (int64_t)i * E), s) : (int8_t)0;
     return;
   }
   const float inv = 1.f / s, half = 0.5f * s;
 #pragma unroll
   for (int r = 0; r < REGS; ++r) {
-    const int q = r * 64 + lane;
+    const int q = r * L + lane;
     if (q >= nv) continue;
     uint32_t o[W / 4];
     bool edge = false;
@@ -145,7 +155,7 @@ template <int DT, int REGS> __global__ __launch_bounds__(256) void pack_rows_ker
     if constexpr (W == 8) *(uint64_t *)(c + (int64_t)q * 8) = ((uint64_t)o[1] << 32) | o[0];
     else *(uint32_t *)(c + (int64_t)q * 4) = o[0];
   }
-  for (int i = k; i < P.Hp; i += 64) c[i] = i < P.H ? (int8_t)code_of(rest, s) : (int8_t)0;
+  for (int i = k; i < P.Hp; i += L) c[i] = i < P.H ? (int8_t)code_of(rest, s) : (int8_t)0;
 }
 
 template <int DT> __global__ __launch_bounds__(256) void pack_kernel(Pack P) {
@@ -199,12 +209,14 @@ template <int DT> void pack_as(int N, Pack P, hipStream_t st) {
   constexpr int E = In<DT>::E, W = 16 / E;
   const bool codes = ((uintptr_t)P.codes & (W - 1)) == 0 && (P.c_ld & (W - 1)) == 0;
   P.vec = codes && ((uintptr_t)P.x & 15) == 0 && (P.x_ld & 15) == 0 ? 1 : 0;
-  const dim3 rows((unsigned)((N + 3) / 4)), block(256);
-  if (codes && P.H <= 4 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 4>), rows, block, 0, st, P, N);
-  else if (DT == SV_BF16 && codes && P.H <= 8 * W * 64)
-    hipLaunchKernelGGL((pack_rows_kernel<DT, 8>), rows, block, 0, st, P, N);
-  else if (codes && P.H <= 16 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 16>), rows, block, 0, st, P, N);
-  else hipLaunchKernelGGL((pack_kernel<DT>), dim3(N), block, 0, st, P);
+  const dim3 rows((unsigned)((N + 3) / 4)), each((unsigned)N), block(256);
+  constexpr int MID = DT == SV_BF16 ? 8 : 16;   // (eight registers of fp32 compile to many more)
+  if (codes && N <= 2048 && P.H > 4 * W * 16 && P.H <= 4 * W * 256)
+    hipLaunchKernelGGL((pack_rows_kernel<DT, 4, 4>), each, block, 0, st, P, N);
+  else if (codes && P.H <= 4 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 4, 1>), rows, block, 0, st, P, N);
+  else if (codes && P.H <= MID * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, MID, 1>), rows, block, 0, st, P, N);
+  else if (codes && P.H <= 16 * W * 64) hipLaunchKernelGGL((pack_rows_kernel<DT, 16, 1>), rows, block, 0, st, P, N);
+  else hipLaunchKernelGGL((pack_kernel<DT>), each, block, 0, st, P);
 }
 
 inline void pack(int dtype, int N, const Pack &P, hipStream_t st) {

@@ -342,7 +342,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
   clear<DT, T>(acc);
   const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
   const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
-  product<DT, T>(acc, lds, X, Y, 0, G.nk);
+  product<DT, T>(acc, lds, X, Y, 0, G.nk, T::BM == 32 ? in % G.nk : 0);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   __syncthreads();                       // the tiles are done with: their LDS takes the waves' results
   float2 *red = (float2 *)lds;           // [WN][BM]
@@ -459,7 +459,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   if (m0 < M && n0 < G.N) {
     const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
     const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
-    product<DT, T>(acc, lds, X, Y, 0, G.nk);
+    product<DT, T>(acc, lds, X, Y, 0, G.nk, T::BM == 32 ? in % G.nk : 0);
   }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   const Turn turn;

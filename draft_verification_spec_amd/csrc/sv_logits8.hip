@@ -93,7 +93,7 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void logits_kern
   clear<SV_I8, T>(acc);
   const Part X = {P.x + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, (int64_t)P.nk * STEP};
   const Part Y = {P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
-  product<SV_I8, T>(acc, lds, X, Y, 0, P.nk);
+  product<SV_I8, T>(acc, lds, X, Y, 0, P.nk, T::BM < 256 ? in % P.nk : 0);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
 #pragma unroll
   for (int g = 0; g < T::FN; ++g) {
