@@ -12,14 +12,15 @@
 // operands agree, so the types differ in one instruction (four for fp32, whose
 // instruction takes one element a lane) and in how columns are read.
 //
-// Tiles go from memory to LDS by direct 16-byte loads (no registers between),
-// into two buffers for the rows' operand and three for the columns', whose data
-// comes from farther (the weight from HBM).  A wave holds two sets of fragments:
-// while the matrix instructions work on one half step, the next half step's
-// fragments are read.  The one barrier of a step stands in its middle: by then
-// every wave has read all of the step's buffers, which later loads may overwrite,
-// and the next step's tiles have landed, one and two whole steps after they were
-// asked for.
+// Tiles go from memory to LDS by direct 16-byte loads (no registers between).  A wave
+// holds two sets of fragments: while the matrix instructions work on one half step,
+// the next half step's fragments are read.  The one barrier of a step stands in its
+// middle: by then every wave has read all of the step's buffers, which later loads may
+// overwrite, and the next step's tiles have landed.  Loads land in order, so how long
+// they may take is the smaller number of an operand's buffers, less one, in steps: the
+// large tiles have room for two and three (the columns' operand comes from farther),
+// and three of both pay for a few tokens against 8-bit weights, which only read (one
+// token of 4096 x 151936 120 to 111 us; four no more).
 //
 // A direct load writes 64 consecutive 16-byte pieces, so pieces are permuted on
 // the memory side to keep LDS reads off each other's banks.  Rows: piece p of row
@@ -76,13 +77,15 @@ template <> struct Mma<SV_I8> {
   }
 };
 
-// A workgroup's tile: WM x WN waves, each of FM x FN fragments of 16 x 16.
-template <int FM_, int FN_, int WM_, int WN_> struct Tile {
-  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
+// A workgroup's tile: WM x WN waves, each of FM x FN fragments of 16 x 16; XB and YB
+// buffers of the operands (2 and 3, or as many of both).
+template <int FM_, int FN_, int WM_, int WN_, int XB_ = 2, int YB_ = 3> struct Tile {
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, XB = XB_, YB = YB_;
+  static_assert(XB == YB || (XB == 2 && YB == 3), "buffers");
   static constexpr int NW = WM * WN, TPB = 64 * NW;
   static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   static constexpr int XBUF = BM * STEP, YBUF = BN * STEP;   // bytes of one LDS buffer
-  static constexpr int LDS = 2 * XBUF + 3 * YBUF;
+  static constexpr int LDS = XB * XBUF + YB * YBUF;
 };
 
 // One tile's part of an operand.
@@ -252,6 +255,20 @@ template <int MM, int RD, int LD> __device__ __forceinline__ void mix() {
 }
 #endif
 
+#ifdef __HIP_DEVICE_COMPILE__
+// This wave's LDS reads are done, and its loads but for the last g groups of NL
+// (g at most G).
+template <int G, int NL> __device__ __forceinline__ void wait_loads(int g) {
+  if constexpr (G == 0) {
+    __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0)
+  } else {
+    static_assert(G * NL < 64, "the counter's range");
+    if (g >= G) __builtin_amdgcn_s_waitcnt(0x0070 | ((G * NL) & 15) | ((G * NL) >> 4) << 14);
+    else wait_loads<G - 1, NL>(g);
+  }
+}
+#endif
+
 // The products of one tile over steps [s0, s0 + nk); from: the step of them to begin
 // with, where both operands are rows.  Rows a power of two apart lie on few memory
 // channels at any one step, so where reading the columns' operand is the bound, tiles
@@ -270,22 +287,26 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
   SY sy;
   sx.start(X, s0, nk, from);
   sy.start(Y, s0, nk, from);
-  char *const yl = lds + 2 * T::XBUF;
+  constexpr bool EVEN = T::XB == T::YB;                  // as many buffers of both
+  constexpr int B = T::YB;
+  char *const yl = lds + T::XB * T::XBUF;
   u32x4 x0[T::FM], y0[T::FN], x1[T::FM], y1[T::FN];
-  auto read = [&](u32x4 (&x)[T::FM], u32x4 (&y)[T::FN], int s, int yb, int h) {
-    SX::read(x, lds + (s & 1) * T::XBUF, gx, h);
-    SY::read(y, yl + yb * T::YBUF, gy, h);
+  auto read = [&](u32x4 (&x)[T::FM], u32x4 (&y)[T::FN], int s, int b, int h) {
+    SX::read(x, lds + (EVEN ? b : s & 1) * T::XBUF, gx, h);
+    SY::read(y, yl + b * T::YBUF, gy, h);
   };
-  // One barrier: this wave's LDS reads are done and its loads have landed, but for
-  // the columns' tile of the step after next.  Written out, because a fence would
-  // wait for that one too; the empty asm keeps the compiler's accesses on their side.
-  auto landed = [&](bool ahead) {
+  // One barrier: this wave's LDS reads are done and its loads have landed, but for g
+  // groups of later steps: even buffers, of both operands' loads of a step; else of the
+  // columns' loads of the step after next.  Written out, because a fence would wait for
+  // those too; the empty asm keeps the compiler's accesses on their side.
+  constexpr int NL = EVEN ? SX::NL + SY::NL : SY::NL;
+  auto landed = [&](auto most, int g) {
     asm volatile("" ::: "memory");
-    if (ahead) __builtin_amdgcn_s_waitcnt(0x0070 | SY::NL);   // vmcnt(NL) lgkmcnt(0)
-    else __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0)
+    wait_loads<decltype(most)::value, NL>(g);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  typedef std::integral_constant<int, EVEN ? B - 2 : 1> Later;
   typedef typename Mma<DT>::Acc Acc;
   auto mul = [&](Acc (&c)[T::FM][T::FN], u32x4 (&x)[T::FM], u32x4 (&y)[T::FN]) {
     SX::finish(x);
@@ -296,29 +317,39 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
       for (int g = 0; g < T::FN; ++g) Mma<DT>::mul(c[f][g], y[g], x[f]);
   };
   const int wx = sx.whole(nk), wy = sy.whole(nk), full = wx < wy ? wx : wy;
-  sx.issue(lds, false, nk);
-  sy.issue(yl, false, nk);
-  if (nk > 1) sy.issue(yl + T::YBUF, false, nk);
-  landed(nk > 1);
-  if (nk > 1) sx.issue(lds + T::XBUF, false, nk);
-  if (nk > 2) sy.issue(yl + 2 * T::YBUF, false, nk);
+  if constexpr (EVEN) {
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (j < nk) {
+        sx.issue(lds + j * T::XBUF, false, nk);
+        sy.issue(yl + j * T::YBUF, false, nk);
+      }
+    landed(std::integral_constant<int, B - 1>(), nk - 1);
+  } else {
+    sx.issue(lds, false, nk);
+    sy.issue(yl, false, nk);
+    if (nk > 1) sy.issue(yl + T::YBUF, false, nk);
+    landed(Later(), nk - 1);
+    if (nk > 1) sx.issue(lds + T::XBUF, false, nk);
+    if (nk > 2) sy.issue(yl + 2 * T::YBUF, false, nk);
+  }
   read(x0, y0, 0, 0, 0);
-  int yb = 0;                                            // the columns' buffer of this step
+  int b = 0;                                             // this step's buffer
   // One step.  Loads and LDS reads are spread between the matrix instructions: a
   // wave issues in order, and eight waves that all ask for their fragments first
   // keep the matrix units waiting for the LDS.
   constexpr int MM = T::FM * T::FN * (DT == SV_F32 ? 4 : 1);
   constexpr int RD = SX::READS + SY::READS, LD = SX::NL + SY::NL;
   auto step = [&](int s, Acc (&c)[T::FM][T::FN], auto whole) {
-    constexpr bool W = decltype(whole)::value;           // three more whole steps follow
-    read(x1, y1, s, yb, 1);
+    constexpr bool W = decltype(whole)::value;           // B more whole steps follow
+    read(x1, y1, s, b, 1);
     mul(c, x0, y0);
     mix<MM, RD, 0>();
-    landed(W || s + 2 < nk);
-    if (W || s + 2 < nk) sx.issue(lds + (s & 1) * T::XBUF, W, nk);
-    if (W || s + 3 < nk) sy.issue(yl + yb * T::YBUF, W, nk);
-    yb = yb == 2 ? 0 : yb + 1;
-    if (W || s + 1 < nk) read(x0, y0, s + 1, yb, 0);
+    landed(Later(), W ? B : nk - 2 - s);
+    if (W || s + T::XB < nk) sx.issue(lds + (EVEN ? b : s & 1) * T::XBUF, W, nk);
+    if (W || s + B < nk) sy.issue(yl + b * T::YBUF, W, nk);
+    b = b == B - 1 ? 0 : b + 1;
+    if (W || s + 1 < nk) read(x0, y0, s + 1, b, 0);
     mul(c, x1, y1);
     if constexpr (W) mix<MM, RD, LD>();
   };
@@ -341,7 +372,7 @@ __device__ __forceinline__ void product(typename Mma<DT>::Acc (&acc)[T::FM][T::F
     }
   };
   int s = 0;
-  for (; s + 3 < full; ++s) sum(s, std::true_type());
+  for (; s + B < full; ++s) sum(s, std::true_type());
   for (; s < nk; ++s) sum(s, std::false_type());
 #endif
 }
@@ -374,6 +405,40 @@ __device__ __forceinline__ void tile_at(int id, int mt, int nt, int band, int &i
   const int h = mt - g * band < band ? mt - g * band : band;
   in = in_band / h;
   im = g * band + (in_band - in * h);
+}
+
+// Rows of `bytes` bytes that the products cannot read where they lie, at any
+// alignment, into rows of whole steps with zeros behind them: 16 bytes a lane, as
+// many lanes a row (1 << lg) as share it out evenly (53559 rows of 144 bytes 16 to
+// 9 us, 50000 of 2000 bytes 70 to 38 us, against a workgroup a row and an element a lane).
+static __global__ __launch_bounds__(256) void copy_rows_kernel(const char *src, int64_t ld, int64_t bytes, char *dst,
+                                                               int64_t d_ld, int chunks, int rows, int lg) {
+  typedef u32x4 u32x4_any __attribute__((aligned(1)));   // (the GPU takes 16-byte loads at any address)
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
+  if (row >= rows) return;
+  const char *s = src + row * ld;
+  char *d = dst + row * d_ld;
+  for (int c = threadIdx.x & ((1 << lg) - 1); c < chunks; c += 1 << lg) {
+    const int64_t at = (int64_t)c * 16;
+    u32x4 v = 0;
+    if (at + 16 <= bytes) {
+      v = *(const u32x4_any *)(s + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (at + i < bytes) v[i / 4] |= (uint32_t)(uint8_t)s[at + i] << (i % 4 * 8);
+    }
+    *(u32x4 *)(d + at) = v;
+  }
+}
+
+static inline void copy_rows(const void *src, int64_t ld, int64_t bytes, char *dst, int64_t d_ld, int64_t d_bytes,
+                             int64_t rows, hipStream_t st) {
+  const int chunks = (int)(d_bytes / 16);
+  int lg = 3;                                            // (whole steps: 8 chunks or more)
+  while (lg < 6 && (1 << lg) < chunks) ++lg;
+  hipLaunchKernelGGL(copy_rows_kernel, dim3((unsigned)((rows + (256 >> lg) - 1) / (256 >> lg))), dim3(256), 0, st,
+                     (const char *)src, ld, bytes, dst, d_ld, chunks, (int)rows, lg);
 }
 
 }  // namespace sv_gemm

@@ -920,14 +920,6 @@ template <int DT> __global__ __launch_bounds__(256) void loss_kernel(Head P) {
   if (threadIdx.x == 0) P.loss[0] = (float)(((red[0] + red[1]) + red[2]) + red[3]);
 }
 
-// rows of the weight into rows of whole steps, zeros behind them
-template <int DT> __global__ __launch_bounds__(256) void copy_weight_kernel(const char *src, int64_t ld, int H, char *dst,
-                                                                            int64_t d_ld, int64_t Kp) {
-  const char *s = src + (int64_t)blockIdx.x * ld;
-  char *d = dst + (int64_t)blockIdx.x * d_ld;
-  for (int k = threadIdx.x; k < (int)Kp; k += 256) store_real<DT>(d, k, k < H ? load_real<DT>(s, k) : 0.f);
-}
-
 // ------------------------------------------------------------------------ host
 static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile<2, 2, 2, 2>::BM == 64 &&
                   Tile<2, 2, 1, 4>::BM == 32,
@@ -968,14 +960,13 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
   F.x = P.xs;
   F.x_ld = L.x_ld;
   F.nk = (int32_t)(L.Kp * E / STEP);
-  auto weight_piece = [&](Prod &G, int64_t v0, int64_t cnt) {
+  auto weight_piece = [&](Prod &G, int64_t v0, int64_t cnt, bool copy) {
     G.v0 = v0;
     if (direct) {
       G.y = P.weight + v0 * P.w_ld;
       G.y_ld = P.w_ld;
     } else {
-      hipLaunchKernelGGL((copy_weight_kernel<DT>), dim3((unsigned)cnt), b256, 0, st, P.weight + v0 * P.w_ld, P.w_ld,
-                         P.H, P.wt, L.x_ld, L.Kp);
+      if (copy) copy_rows(P.weight + v0 * P.w_ld, P.w_ld, (int64_t)P.H * E, P.wt, L.x_ld, L.Kp * E, cnt, st);
       G.y = P.wt;
       G.y_ld = L.x_ld;
     }
@@ -985,7 +976,7 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
   for (int64_t v0 = 0; v0 < P.V; v0 += fstep) {
     const int64_t cnt = P.V - v0 < fstep ? P.V - v0 : fstep;
     Prod G = tiled<TS>(F, P.N, cnt);
-    weight_piece(G, v0, cnt);
+    weight_piece(G, v0, cnt, true);
     G.tile0 = tiles;
     hipLaunchKernelGGL((stats_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
     tiles += G.nt;
@@ -1010,7 +1001,7 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
     Prod G = tiled<TS>(F, L.Np, cp);
-    if (!P.keep || P.gh) weight_piece(G, v0, cnt);
+    weight_piece(G, v0, cnt, L.pieces > 1);              // (a single copied piece is still there)
     G.N = (int32_t)cnt;
     if (P.keep) {
       G.M = (int32_t)cp;

@@ -63,13 +63,6 @@ template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(const int
   }
 }
 
-// rows of bytes into rows of whole steps, zeros behind them
-__global__ __launch_bounds__(256) void copy_rows_kernel(const int8_t *src, int64_t ld, int H, int8_t *dst, int64_t Kp) {
-  const int8_t *s = src + (int64_t)blockIdx.x * ld;
-  int8_t *d = dst + (int64_t)blockIdx.x * Kp;
-  for (int i = threadIdx.x; i < (int)Kp; i += 256) d[i] = i < H ? s[i] : (int8_t)0;
-}
-
 struct LogitsP {
   const char *x;                         // token codes, rows of whole steps
   int64_t x_ld;
@@ -195,7 +188,7 @@ extern "C" int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden
   P.x_ld = L.Kp;
   P.sx = (float *)(ws + L.scale);
   if (s.hidden_dtype == SV_I8) {
-    hipLaunchKernelGGL(copy_rows_kernel, dim3(s.N), dim3(256), 0, st, (const int8_t *)hidden, hs, s.H, codes, L.Kp);
+    copy_rows(hidden, hs, s.H, ws + L.codes, L.Kp, L.Kp, s.N, st);
     P.sx = hidden_scale;
   } else {
     sv_act8::Pack Q = {(const char *)hidden, hs * sv_head_host::esize(s.hidden_dtype), codes, L.Kp,
@@ -217,8 +210,7 @@ extern "C" int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden
       // codes are 0 past H, so what else it holds adds nothing
       P.w_bytes = sv_head_host::up(s.H, 4);
     } else {
-      hipLaunchKernelGGL(copy_rows_kernel, dim3(P.V), dim3(256), 0, st, weight_codes + v0 * wst, wst, s.H,
-                         (int8_t *)(ws + L.weight), L.Kp);
+      copy_rows(weight_codes + v0 * wst, wst, s.H, ws + L.weight, L.Kp, L.Kp, P.V, st);
       P.w = ws + L.weight;
       P.w_ld = P.w_bytes = L.Kp;
     }
@@ -227,7 +219,7 @@ extern "C" int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden
     P.out_vec = (os * oe) % (4 * oe) == 0 && ((uintptr_t)P.out & (4 * oe - 1)) == 0;
     if (s.N >= 192) launch_logits<Tile<8, 4, 2, 4>>(P, s.out_dtype, st);
     else if (s.N > 32) launch_logits<Tile<4, 4, 2, 2>>(P, s.out_dtype, st);
-    else launch_logits<Tile<2, 2, 1, 4>>(P, s.out_dtype, st);
+    else launch_logits<Tile<2, 2, 1, 4, 3, 3>>(P, s.out_dtype, st);
   }
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
