@@ -443,6 +443,50 @@ struct Turn {                            // the lane's bits, and the bits of the
   }
 };
 
+// Workgroup 0 of these: the loss terms, in order (a fixed run per thread, then the
+// waves).  The others put the rows that the sum of dW runs over into blocks, with zeros for
+// rows without a term of their own: those with a data error (their values may be NaN)
+// and those up to a whole step.
+// 256 threads, more leave; red: 4 in LDS.  Where there are gradients they are the last workgroups of
+// the first piece's dz, which needs nothing of theirs: no launch of their own (4 to 5
+// us of 24 rows' 73).
+template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int block, double *red) {
+  if (threadIdx.x >= 256) return;
+  if (block > 0) {
+    constexpr int E = Mma<DT>::E, Q = STEP / E, B = 16 / E;
+    const int at = B * (block - 1), M = P.counts[0];
+    if (at >= (M + Q - 1) / Q * Q) return;
+    bool on[B];
+#pragma unroll
+    for (int r = 0; r < B; ++r) on[r] = at + r < M && P.ga[at + r] != 0.f;
+    const char *x = P.xs + at * P.x_ld;
+    u32x4 *o = (u32x4 *)(P.xw + at / B * P.xw_ld);
+    for (int k = threadIdx.x; k < (int)P.Kp; k += 256) {
+      u32x4 v;
+      if constexpr (DT == SV_BF16) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t a = on[2 * r] ? ((const uint16_t *)(x + 2 * r * P.x_ld))[k] : 0u;
+          const uint32_t b = on[2 * r + 1] ? ((const uint16_t *)(x + (2 * r + 1) * P.x_ld))[k] : 0u;
+          v[r] = a | b << 16;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = on[r] ? ((const uint32_t *)(x + r * P.x_ld))[k] : 0u;
+      }
+      o[k] = v;
+    }
+    return;
+  }
+  const int M = P.counts[1], per = (M + 255) / 256;
+  double s = 0.0;
+  for (int i = threadIdx.x * per; i < M && i < (int)(threadIdx.x + 1) * per; ++i) s += P.term[i];
+  s = wave_sum_d(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) P.loss[0] = (float)(((red[0] + red[1]) + red[2]) + red[3]);
+}
+
 // Backward tile of a piece: dz = u (2^(z log2 e - lse2)), rounded to the
 // operands' type; zeros in the rows up to a whole step and in the columns up to a
 // whole tile, so that both gradients can sum whole steps.
@@ -450,6 +494,10 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   __shared__ __align__(16) char lds[T::LDS];
   constexpr int Q = STEP / Mma<DT>::E;
   const int M = P.counts[0], Mp = (M + Q - 1) / Q * Q, mt = (Mp + T::BM - 1) / T::BM;
+  if ((int)blockIdx.x >= G.mt * G.nt) {
+    loss_part<DT>(P, blockIdx.x - G.mt * G.nt, (double *)lds);
+    return;
+  }
   if ((int)blockIdx.x >= mt * G.nt) return;
   int im, in;
   tile_at(run_of_xcd(blockIdx.x, mt * G.nt), mt, G.nt, G.band, im, in);
@@ -518,6 +566,11 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
 // the vocabulary.  A thread takes 4 rows x 4 columns.
 __global__ __launch_bounds__(256) void dz_kept_kernel(Head P, Prod G) {
   const int M = P.counts[0], Mp = (M + 31) / 32 * 32;
+  if ((int)blockIdx.x >= G.mt) {         // (G.mt: groups of rows)
+    __shared__ double red[4];
+    if (blockIdx.y == 0) loss_part<SV_F32>(P, blockIdx.x - G.mt, red);
+    return;
+  }
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4, r0 = blockIdx.x * 4;
   if (r0 >= Mp || c >= G.M) return;      // (G.M: columns in whole tiles)
   f32x4 w[4];
@@ -629,11 +682,12 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
 // waves adds a run of the tile's sums, four loads under way at a time, and the first
 // joins the runs.  (Few rows have many sums of a few steps each: 79 at 24 rows of 512
 // in fp32, which one wave took 21 us for.)
-template <int DT, class T, int WS> __global__ __launch_bounds__(64 * WS) void dx_rows_kernel(Head P, Prod G) {
-  __shared__ f32x4 red[WS > 1 ? WS - 1 : 1][T::FN][64];
+template <class T, int WS> using Runs = f32x4[WS > 1 ? WS - 1 : 1][T::FN][64];
+template <int DT, class T, int WS>
+__device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int block, Runs<T, WS> &red) {
   const int M = P.counts[0], lane = threadIdx.x & 63, ws = threadIdx.x >> 6;
   constexpr int PER = T::NW * T::FM;
-  const int tile = blockIdx.x / PER, f = blockIdx.x % PER / T::NW, wid = blockIdx.x % T::NW;
+  const int tile = block / PER, f = block % PER / T::NW, wid = block % T::NW;
   const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
   const int wm = wid / T::WN, wn = wid % T::WN;
   const int m = m0 + index_of<T::FM, ROWS>(wm, f, lane & 15);
@@ -681,6 +735,11 @@ template <int DT, class T, int WS> __global__ __launch_bounds__(64 * WS) void dx
                            v);
 }
 
+template <int DT, class T, int WS> __global__ __launch_bounds__(64 * WS) void dx_rows_kernel(Head P, Prod G) {
+  __shared__ Runs<T, WS> red;
+  dx_rows_part<DT, T, WS>(P, G, blockIdx.x, red);
+}
+
 // dW of a piece: complete, in the weight's type.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
@@ -720,12 +779,18 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
 // wave keeps its 64 entries' dz in registers and runs along the hidden width, 64
 // columns at a time; blocks come straight from memory, each lane's 16 bytes being a
 // fragment's, so no LDS and no barrier stand between the stores (20000 x 1024 in
-// bf16: 18 us through the tiled product).
-template <int DT> __global__ __launch_bounds__(256) void dw_few_kernel(Head P, Prod G, int span) {
+// bf16: 18 us through the tiled product).  The first `sums` workgroups join dx's sums
+// (X), which saves that launch: 5 us of 24 rows' 75.
+template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(Head P, Prod G, int span, Prod X, int sums) {
   typedef typename Mma<DT>::Acc Acc;
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  const int nm = (G.M + 255) / 256, m0 = (blockIdx.x % nm) * 256 + (threadIdx.x >> 6) * 64;
-  const int c0 = blockIdx.x / nm * span, c1 = c0 + span < G.N ? c0 + span : G.N;
+  if ((int)blockIdx.x < sums) {
+    __shared__ Runs<T, 4> red;
+    dx_rows_part<DT, T, 4>(P, X, blockIdx.x, red);
+    return;
+  }
+  const int block = blockIdx.x - sums, lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int nm = (G.M + 255) / 256, m0 = (block % nm) * 256 + (threadIdx.x >> 6) * 64;
+  const int c0 = block / nm * span, c1 = c0 + span < G.N ? c0 + span : G.N;
   constexpr int Q = STEP / Mma<DT>::E;
   const int halves = P.counts[0] > Q / 2 ? 2 : P.counts[0] > 0 ? 1 : 0;   // 64-byte half steps with rows in them
   if (m0 >= G.M) return;
@@ -879,45 +944,10 @@ template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Hea
   }
 }
 
-// Workgroup 0: the loss terms, in order (a fixed run per thread, then the waves).
-// The others put the rows that the sum of dW runs over into blocks, with zeros for
-// rows without a term of their own: those with a data error (their values may be NaN)
-// and those up to a whole step.
-template <int DT> __global__ __launch_bounds__(256) void loss_kernel(Head P) {
-  if (blockIdx.x > 0) {
-    constexpr int E = Mma<DT>::E, Q = STEP / E, B = 16 / E;
-    const int at = B * (blockIdx.x - 1), M = P.counts[0];
-    if (at >= (M + Q - 1) / Q * Q) return;
-    bool on[B];
-#pragma unroll
-    for (int r = 0; r < B; ++r) on[r] = at + r < M && P.ga[at + r] != 0.f;
-    const char *x = P.xs + at * P.x_ld;
-    u32x4 *o = (u32x4 *)(P.xw + at / B * P.xw_ld);
-    for (int k = threadIdx.x; k < (int)P.Kp; k += 256) {
-      u32x4 v;
-      if constexpr (DT == SV_BF16) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t a = on[2 * r] ? ((const uint16_t *)(x + 2 * r * P.x_ld))[k] : 0u;
-          const uint32_t b = on[2 * r + 1] ? ((const uint16_t *)(x + (2 * r + 1) * P.x_ld))[k] : 0u;
-          v[r] = a | b << 16;
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = on[r] ? ((const uint32_t *)(x + r * P.x_ld))[k] : 0u;
-      }
-      o[k] = v;
-    }
-    return;
-  }
+// The loss alone.
+__global__ __launch_bounds__(256) void loss_kernel(Head P) {
   __shared__ double red[4];
-  const int M = P.counts[1], per = (M + 255) / 256;
-  double s = 0.0;
-  for (int i = threadIdx.x * per; i < M && i < (int)(threadIdx.x + 1) * per; ++i) s += P.term[i];
-  s = wave_sum_d(s);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) P.loss[0] = (float)(((red[0] + red[1]) + red[2]) + red[3]);
+  loss_part<SV_BF16>(P, 0, red);
 }
 
 // ------------------------------------------------------------------------ host
@@ -986,8 +1016,10 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
   const dim3 ng((unsigned)cdiv(P.N, per));
   if (kd) hipLaunchKernelGGL((normaliser_kernel<true>), ng, b1024, 0, st, P, tiles, per);
   else hipLaunchKernelGGL((normaliser_kernel<false>), ng, b1024, 0, st, P, tiles, per);
-  hipLaunchKernelGGL((loss_kernel<DT>), dim3((unsigned)(P.gw ? L.Np * E / 16 + 1 : 1)), b256, 0, st, P);
-  if (!P.grads) return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+  if (!P.grads) {
+    hipLaunchKernelGGL(loss_kernel, dim3(1), b256, 0, st, P);
+    return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+  }
 
   Prod X = tiled<T>(Prod{}, P.N, P.H);
   X.x = P.dz;
@@ -997,17 +1029,22 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
   X.slots = L.slots;
   X.per0 = sv_head_host::RUN;
   X.vec = P.H % 4 == 0 && ((uintptr_t)P.gh & 15) == 0;
+  constexpr bool FEW = T::BM == 32 || (DT == SV_BF16 && T::BM == 128);   // tiles that rows of one step take
+  const bool few = FEW && P.gw && L.Np * E == STEP;
+  const int64_t frags = (int64_t)X.mt * X.nt * T::NW * T::FM;            // fragment rows of dx's tiles
   for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
     Prod G = tiled<TS>(F, L.Np, cp);
     weight_piece(G, v0, cnt, L.pieces > 1);              // (a single copied piece is still there)
     G.N = (int32_t)cnt;
+    const int64_t loss = v0 ? 0 : P.gw ? L.Np * E / 16 + 1 : 1;
     if (P.keep) {
       G.M = (int32_t)cp;
-      hipLaunchKernelGGL(dz_kept_kernel, dim3((unsigned)(L.Np / 4), (unsigned)cdiv(cp, 1024)), b256, 0, st, P, G);
+      G.mt = (int32_t)(L.Np / 4);
+      hipLaunchKernelGGL(dz_kept_kernel, dim3((unsigned)(G.mt + loss), (unsigned)cdiv(cp, 1024)), b256, 0, st, P, G);
     } else {
-      hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
+      hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt + loss)), dim3(TS::TPB), 0, st, P, G);
     }
     if (kd) hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 256)), b256, 0, st, P, G);
     if (P.gh) {
@@ -1026,20 +1063,22 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
       W.y = P.xw;
       W.y_ld = L.xw_ld;
       W.vec = P.H % 4 == 0 && ((uintptr_t)P.gw & 15) == 0;
-      if (L.Np * E == STEP) {            // (columns in parts that give every CU a few workgroups)
-        W.vec = P.H * E % 16 == 0 && ((uintptr_t)P.gw & 15) == 0;
-        const int64_t parts = cdiv(1024, cdiv(cnt, 256)), span = sv_head_host::up(cdiv(P.H, parts), 64);
-        hipLaunchKernelGGL((dw_few_kernel<DT>), dim3((unsigned)(cdiv(cnt, 256) * cdiv(P.H, span))), b256, 0, st, P, W,
-                           (int)span);
+      if (few) {
+        if constexpr (FEW) {             // (columns in parts that give every CU a few workgroups)
+          W.vec = P.H * E % 16 == 0 && ((uintptr_t)P.gw & 15) == 0;
+          const int64_t parts = cdiv(1024, cdiv(cnt, 256)), span = sv_head_host::up(cdiv(P.H, parts), 64);
+          const int64_t sums = P.gh && v0 + cnt == P.V ? frags : 0;
+          hipLaunchKernelGGL((dw_few_kernel<DT, T>), dim3((unsigned)(cdiv(cnt, 256) * cdiv(P.H, span) + sums)), b256, 0,
+                             st, P, W, (int)span, X, (int)sums);
+        }
       } else {
         hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
       }
     }
   }
   constexpr int WS = T::BM == 256 ? 1 : 8;   // waves that share a row's sums: few with as many tiles as workgroups
-  if (P.gh)
-    hipLaunchKernelGGL((dx_rows_kernel<DT, T, WS>), dim3((unsigned)(X.mt * X.nt * T::NW * T::FM)), dim3(64 * WS), 0, st,
-                       P, X);
+  if (P.gh && !few)
+    hipLaunchKernelGGL((dx_rows_kernel<DT, T, WS>), dim3((unsigned)frags), dim3(64 * WS), 0, st, P, X);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

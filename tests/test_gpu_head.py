@@ -252,6 +252,16 @@ def test_ce_several_pieces(sv, n, h, v, dtype):
     check_ce(sv, hidden, x, w, t, u, 1.0, dtype)
 
 
+@pytest.mark.parametrize("n,v,dtype", [(9, 250000, BF), (50, 240000, BF), (9, 130000, F)])
+def test_ce_few_rows_copied_pieces(sv, n, v, dtype):
+    """Few rows against a head that no step divides: copied a piece at a time, and
+    the last piece's launch joins the sums of all of them."""
+    log(f"head_ce copied pieces n={n} v={v} {dtype}")
+    hidden, x, w, t, u = ce_case(sv, n, 1001, v, dtype, "same", 1.0, 12)
+    check_ce(sv, hidden, x, w, t, u, 1.0, dtype)
+    check_ce(sv, hidden, x, w, t, u, 1.0, dtype, "hidden")
+
+
 def test_ce_strides(sv):
     """Rows and head as parts of wider tensors, aligned or not, transposed, and
     32-bit targets: what the contiguous call gives."""
