@@ -49,6 +49,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// at any address (the GPU takes such accesses; on elements' addresses they are as fast)
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+typedef f32x4 f32x4_any __attribute__((aligned(1)));
 
 constexpr int STEP = 128;                // bytes of k a step
 
@@ -413,7 +417,6 @@ __device__ __forceinline__ void tile_at(int id, int mt, int nt, int band, int &i
 // 9 us, 50000 of 2000 bytes 70 to 38 us, against a workgroup a row and an element a lane).
 static __global__ __launch_bounds__(256) void copy_rows_kernel(const char *src, int64_t ld, int64_t bytes, char *dst,
                                                                int64_t d_ld, int chunks, int rows, int lg) {
-  typedef u32x4 u32x4_any __attribute__((aligned(1)));   // (the GPU takes 16-byte loads at any address)
   const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lg;
   if (row >= rows) return;
   const char *s = src + row * ld;
