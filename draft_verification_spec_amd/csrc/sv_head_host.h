@@ -97,7 +97,8 @@ struct Plan {
   int bm, bn;                            // tile of the products
   bool keep;                             // the forward product's logits stay in dz (fp32, one piece)
   bool narrow;                           // tiles of 64 columns against the weight's rows
-  int groups, slots;                     // workgroups of the hidden gradient, tiles each may touch
+  // the hidden gradient: chunks of a piece, steps of one; workgroups, tiles each may touch
+  int chunks, full, groups, slots;
   // workspace sections
   size_t counts, perm, alpha, ga, lse2, w, flags, zt, pt, term, part, xs, xw, dz, dzw, wt, acc, total;
 };
@@ -149,12 +150,14 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   p.keep = s->grads && s->dtype == SV_F32 && p.pieces == 1;
   // the hidden gradient's workgroups: as many as run at once (LDS: one tile of
   // 256, two of 128 or 32, four of 64 rows a CU), fewer where a run would be short
-  const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), full = p.piece * e / STEP;
-  int64_t g = CUS * (p.bm == 256 ? 1 : p.bm == 64 ? 4 : 2);
-  if (g > cdiv(tiles * full, RUN)) g = cdiv(tiles * full, RUN);
-  p.groups = (int)(g < 1 ? 1 : g);
-  const int64_t run = cdiv(tiles * full, p.groups);
-  p.slots = (int)(cdiv(run > RUN ? run : RUN, full) + 1);
+  const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), steps = p.piece * e / STEP;
+  const int64_t most_groups = CUS * (p.bm == 256 ? 1 : p.bm == 64 ? 4 : 2), g = cdiv(tiles * steps, RUN);
+  p.groups = (int)(g < most_groups ? g < 1 ? 1 : g : most_groups);
+  p.chunks = 1;
+  while (p.groups == most_groups && p.chunks < 8 && 2 * p.chunks * tiles <= p.groups) p.chunks *= 2;
+  p.full = (int)cdiv(steps, p.chunks);
+  const int64_t run = cdiv(tiles * p.full, p.groups / p.chunks);
+  p.slots = (int)(cdiv(run > RUN ? run : RUN, p.full) + 1);
   const bool gh = s->grads & SV_GRAD_HIDDEN, gw = s->grads & SV_GRAD_WEIGHT;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) & ~(size_t)255; return at; };
