@@ -49,9 +49,6 @@ template <int DT> __device__ __forceinline__ void store_real(char *p, int64_t i,
   if constexpr (DT == SV_BF16) ((__bf16 *)p)[i] = (__bf16)v;
   else ((float *)p)[i] = v;
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
-}
 // four consecutive elements, wherever they begin (40 rows of 1001 x 50000 in fp32: dW
 // 132 to 83 us against a store an element)
 template <int DT> __device__ __forceinline__ void store4(char *p, int64_t i, const float (&v)[4]) {
@@ -505,6 +502,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   const Turn turn;
+  const Beside beside;
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
     const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
@@ -526,8 +524,15 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
       }
     const int n = n0 + wn * T::FN * 16 + (lane >> 4) * 4;
     if (P.gh && m < Mp) {
+      if constexpr (DT == SV_BF16) {
 #pragma unroll
-      for (int g = 0; g < T::FN; ++g) store4<DT>(P.dz + m * P.dz_ld, n + g * 16, d[g]);
+        for (int g = 0; g < T::FN; g += 2)
+          *(u32x4 *)(P.dz + m * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + beside.at) * 2) =
+              Beside::eight(d[g], d[g + 1]);
+      } else {
+#pragma unroll
+        for (int g = 0; g < T::FN; ++g) store4<DT>(P.dz + m * P.dz_ld, n + g * 16, d[g]);
+      }
     }
     if (P.gw) {
       char *at = P.dzw + m / (16 / Mma<DT>::E) * P.dzw_ld;
@@ -757,21 +762,31 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   product<DT, T, BLOCKS, BLOCKS>(acc, lds, X, Y, 0, nk);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
+  const Beside beside;
 #pragma unroll
   for (int f = 0; f < T::FM; ++f) {
     const int m = m0 + index_of<T::FM, BLOCKS>(wm, f, lane & 15);
     if (m >= G.M) continue;
+    const int64_t row = (int64_t)m * P.H;
+    if constexpr (DT == SV_BF16) {
 #pragma unroll
-    for (int g = 0; g < T::FN; ++g) {
-      const int n = n0 + index_of<T::FN, BLOCKS>(wn, g, (lane >> 4) * 4);
-      const int64_t o = (int64_t)m * P.H + n;
-      const float v[4] = {acc[f][g][0], acc[f][g][1], acc[f][g][2], acc[f][g][3]};
-      if (n + 4 <= G.N) {
-        store4<DT>(out, o, v);
-      } else {
+      for (int g = 0; g < T::FN; g += 2) {
+        const float a[4] = {acc[f][g][0], acc[f][g][1], acc[f][g][2], acc[f][g][3]};
+        const float b[4] = {acc[f][g + 1][0], acc[f][g + 1][1], acc[f][g + 1][2], acc[f][g + 1][3]};
+        store8(out, row, n0 + index_of<T::FN, BLOCKS>(wn, g, 0) + beside.at, G.N, Beside::eight(a, b));
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < G.N) store_real<DT>(out, o + i, v[i]);
+      for (int g = 0; g < T::FN; ++g) {
+        const int n = n0 + index_of<T::FN, BLOCKS>(wn, g, (lane >> 4) * 4);
+        const float v[4] = {acc[f][g][0], acc[f][g][1], acc[f][g][2], acc[f][g][3]};
+        if (n + 4 <= G.N) {
+          store4<DT>(out, row + n, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < G.N) store_real<DT>(out, row + n + i, v[i]);
+        }
       }
     }
   }
@@ -838,13 +853,7 @@ template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(
         if constexpr (DT == SV_BF16) {
           const f32x4 a = acc[f][g], b = acc[f][g + 1];
           const u32x4 v = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
-          if (n + 8 <= G.N) {
-            *(u32x4_any *)(out + (row + n) * 2) = v;
-          } else {
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-              if (n + r < G.N) ((uint16_t *)out)[row + n + r] = (uint16_t)(v[r / 2] >> (r % 2 * 16));
-          }
+          store8(out, row, n, G.N, v);
         } else if (n + 4 <= G.N) {
           *(f32x4_any *)(out + (row + n) * 4) = acc[f][g];
         } else {

@@ -82,39 +82,40 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void logits_kern
   const Part Y = {P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
   product<SV_I8, T>(acc, lds, X, Y, 0, P.nk, T::BM < 256 ? in % P.nk : 0);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
+  const Beside beside;
+  float sw[T::FN][4];
 #pragma unroll
-  for (int g = 0; g < T::FN; ++g) {
-    const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4;
-    float sw[4];
+  for (int g = 0; g < T::FN; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = n + i < P.V ? P.sw[n + i] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + (wn * T::FN + g) * 16 + (lane >> 4) * 4 + i;
+      sw[g][i] = n < P.V ? P.sw[n] : 0.f;
+    }
 #pragma unroll
-    for (int f = 0; f < T::FM; ++f) {
-      const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
-      if (m >= P.N) continue;
-      const float sx = P.sx[m];
-      float v[4];
+  for (int f = 0; f < T::FM; ++f) {
+    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
+    if (m >= P.N) continue;
+    const float sx = P.sx[m];
+    const int64_t row = (int64_t)m * P.out_ld;
+    float v[T::FN][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (float)acc[f][g][i] * (sx * sw[i]);
-      const int64_t o = (int64_t)m * P.out_ld + n;
-      if (n + 4 <= P.V) {
-        if constexpr (OT == SV_F32) {
-          *(f32x4_any *)(P.out + o * 4) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-          u32x2 u;
+    for (int g = 0; g < T::FN; ++g)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            u[k] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k]) |
-                   (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v[2 * k + 1]) << 16;
-          *(u32x2_any *)(P.out + o * 2) = u;
-        }
+      for (int i = 0; i < 4; ++i) v[g][i] = (float)acc[f][g][i] * (sx * sw[g][i]);
+#pragma unroll
+    for (int g = 0; g < T::FN; g += OT == SV_BF16 ? 2 : 1) {
+      const int n = n0 + (wn * T::FN + g) * 16;
+      if constexpr (OT == SV_BF16) {
+        store8(P.out, row, n + beside.at, P.V, Beside::eight(v[g], v[g + 1]));
       } else {
+        const int c = n + (lane >> 4) * 4;
+        if (c + 4 <= P.V) {
+          *(f32x4_any *)(P.out + (row + c) * 4) = f32x4{v[g][0], v[g][1], v[g][2], v[g][3]};
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < P.V) {
-            if constexpr (OT == SV_F32) ((float *)P.out)[o + i] = v[i];
-            else ((__bf16 *)P.out)[o + i] = (__bf16)v[i];
-          }
+          for (int i = 0; i < 4; ++i)
+            if (c + i < P.V) ((float *)P.out)[row + c + i] = v[g][i];
+        }
       }
     }
   }
