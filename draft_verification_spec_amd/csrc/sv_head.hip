@@ -678,33 +678,37 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
 }
 
 // dx of every row: its tile's sums in a fixed order, rounded once; zeros for rows
-// without a gradient.  A workgroup per fragment row of a tile's wave: each of its WS
-// waves adds a run of the tile's sums, four loads under way at a time, and the first
-// joins the runs.  (Few rows have many sums of a few steps each: 79 at 24 rows of 512
-// in fp32, which one wave took 21 us for.)
-template <class T, int WS> using Runs = f32x4[WS > 1 ? WS - 1 : 1][T::FN][64];
+// without a gradient.  A workgroup per fragment row of a tile's wave: the tile's sums
+// are added in RUNS runs, four loads under way at a time, shared out over WS waves, and
+// the first wave joins them.  (Few rows have many sums of a few steps each: 79 at 24
+// rows of 512 in fp32, which one run took 21 us for; tiles of 256 rows are about as
+// many as workgroups and have few.)
+template <class T> constexpr int RUNS = T::BM == 256 ? 1 : 8;
+template <class T> using Runs = f32x4[RUNS<T> > 1 ? RUNS<T> - 1 : 1][T::FN][64];
 template <int DT, class T, int WS>
-__device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int block, Runs<T, WS> &red) {
+__device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int block, Runs<T> &red) {
   const int M = P.counts[0], lane = threadIdx.x & 63, ws = threadIdx.x >> 6;
   constexpr int PER = T::NW * T::FM;
   const int tile = block / PER, f = block % PER / T::NW, wid = block % T::NW;
   const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
   const int wm = wid / T::WN, wn = wid % T::WN;
   const int m = m0 + index_of<T::FM, ROWS>(wm, f, lane & 15);
+  const Share S(G, M, T::BM);
+  const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
+  const int64_t t = m0 < M ? (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band) : 0;
+  const int b0 = (int)(t * S.full / S.per), b1 = (int)(((t + 1) * S.full - 1) / S.per);
+  const int n = b1 - b0 + 1, all = m0 < M ? n * G.chunks : 0;   // sums: a chunk's, all
+  const int run = (all + RUNS<T> - 1) / RUNS<T>;
+  // in a run of dx that begins before the tile, the tile's sum lies behind those of its
+  // other tiles; in the others it is the first
+  const int k0 = (int)(t - (int64_t)b0 * S.per / S.full);
+  const float *s = P.acc + f * T::FN * (T::TPB * 4) + (wid * 64 + lane) * 4;
   f32x4 v[T::FN];
 #pragma unroll
-  for (int q = 0; q < T::FN; ++q) v[q] = 0;
-  if (m0 < M) {
-    const Share S(G, M, T::BM);
-    const int mt = (M + T::BM - 1) / T::BM, g = im / G.band, h = mt - g * G.band < G.band ? mt - g * G.band : G.band;
-    const int64_t t = (int64_t)g * G.band * G.nt + (int64_t)in * h + (im - g * G.band);
-    const int b0 = (int)(t * S.full / S.per), b1 = (int)(((t + 1) * S.full - 1) / S.per);
-    const int n = b1 - b0 + 1, all = n * G.chunks;       // sums: a chunk's, all
-    const int run = (all + WS - 1) / WS, first = ws * run, end = first + run < all ? first + run : all;
-    const float *s = P.acc + f * T::FN * (T::TPB * 4) + (wid * 64 + lane) * 4;
-    // in a run that begins before the tile, the tile's sum lies behind those of its other
-    // tiles; in the others it is the first
-    const int k0 = (int)(t - (int64_t)b0 * S.per / S.full);
+  for (int p = RUNS<T> - WS + ws; p >= 0; p -= WS) {
+#pragma unroll
+    for (int q = 0; q < T::FN; ++q) v[q] = 0;
+    const int first = p * run, end = first + run < all ? first + run : all;
     int c = first / n, r = first - c * n;
     for (int b = first; b < end; b += 4) {
       f32x4 o[4][T::FN];
@@ -723,15 +727,15 @@ __device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int b
 #pragma unroll
         for (int q = 0; q < T::FN; ++q) v[q] += o[e][q];
     }
-  }
-  if constexpr (WS > 1) {
-    if (ws > 0) {
+    if (RUNS<T> > 1 && p > 0) {
 #pragma unroll
-      for (int q = 0; q < T::FN; ++q) red[ws - 1][q][lane] = v[q];
+      for (int q = 0; q < T::FN; ++q) red[p - 1][q][lane] = v[q];
     }
+  }
+  if constexpr (RUNS<T> > 1) {
     __syncthreads();
     if (ws > 0) return;
-    for (int w = 0; w < WS - 1; ++w)
+    for (int w = 0; w < RUNS<T> - 1; ++w)
 #pragma unroll
       for (int q = 0; q < T::FN; ++q) v[q] += red[w][q][lane];
   }
@@ -742,9 +746,9 @@ __device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int b
   store_columns<DT, T::FN>(P.gh, (int64_t)P.perm[m] * P.H, n0 + index_of<T::FN, COLS>(wn, 0, (lane >> 4) * 4), P.H, v);
 }
 
-template <int DT, class T, int WS> __global__ __launch_bounds__(64 * WS) void dx_rows_kernel(Head P, Prod G) {
-  __shared__ Runs<T, WS> red;
-  dx_rows_part<DT, T, WS>(P, G, blockIdx.x, red);
+template <int DT, class T> __global__ __launch_bounds__(64 * RUNS<T>) void dx_rows_kernel(Head P, Prod G) {
+  __shared__ Runs<T> red;
+  dx_rows_part<DT, T, RUNS<T>>(P, G, blockIdx.x, red);
 }
 
 // dW of a piece: complete, in the weight's type.
@@ -801,7 +805,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
 template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(Head P, Prod G, int span, Prod X, int sums) {
   typedef typename Mma<DT>::Acc Acc;
   if ((int)blockIdx.x < sums) {
-    __shared__ Runs<T, 4> red;
+    __shared__ Runs<T> red;
     dx_rows_part<DT, T, 4>(P, X, blockIdx.x, red);
     return;
   }
@@ -1085,9 +1089,8 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
       }
     }
   }
-  constexpr int WS = T::BM == 256 ? 1 : 8;   // waves that share a row's sums: few with as many tiles as workgroups
   if (P.gh && !few)
-    hipLaunchKernelGGL((dx_rows_kernel<DT, T, WS>), dim3((unsigned)frags), dim3(64 * WS), 0, st, P, X);
+    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)frags), dim3(64 * RUNS<T>), 0, st, P, X);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

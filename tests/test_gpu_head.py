@@ -244,6 +244,20 @@ def test_ce_some_gradients(sv, grad):
     check_ce(sv, hidden, x, w, t, None, 1.0, BF, grad)
 
 
+@pytest.mark.parametrize("n", [8, 40, 64, 150, 300])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_ce_one_gradient_is_the_same(sv, n, dtype):
+    """The loss and each gradient alone: the bits of the call for both."""
+    hidden, x, w, t, u = ce_case(sv, n, 200, 3000, dtype, "same", 1.0, n + 3)
+    both = sv.head_ce(hidden, w, t, u)
+    for grad in (False, "hidden", "weight"):
+        r = sv.head_ce(hidden, w, t, u, grad=grad)
+        for name in ("loss", "nll", "lse", "status"):
+            assert torch.equal(getattr(r, name), getattr(both, name)), name
+        assert r.grad_hidden is None if grad != "hidden" else torch.equal(r.grad_hidden, both.grad_hidden)
+        assert r.grad_weight is None if grad != "weight" else torch.equal(r.grad_weight, both.grad_weight)
+
+
 @pytest.mark.parametrize("n,h,v,dtype", [(2048, 256, 151936, BF), (40, 1024, 151936, BF), (1500, 128, 151936, F)])
 def test_ce_several_pieces(sv, n, h, v, dtype):
     """Vocabularies that take several pieces, the last one ragged."""
@@ -539,6 +553,75 @@ def test_own_workspace(sv):
         sv.head_ce(hidden, w, t, u, workspace=buf[:need - 256])
     with pytest.raises(ValueError):
         sv.head_ce(hidden, w, t, u, workspace=torch.empty(need, dtype=torch.uint8))
+
+
+def ptr(t):
+    import ctypes
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def stream_now():
+    import ctypes
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("off", [0, 1, 3])
+@pytest.mark.parametrize("dtype,code", [(BF, 1), (F, 0)])
+def test_c_strides_and_guards(sv, dtype, code, off):
+    """The C entries with rows at odd distances from any element: what the front end
+    gives, and what lies between the rows and around them stays as it was."""
+    import ctypes
+    lib = sv.load_library()
+    g = gen(90 + off)
+    for n, h, v in ((5, 37, 203), (40, 128, 1030), (300, 200, 515)):
+        log(f"strides and guards n={n} h={h} v={v} {dtype} off={off}")
+        x = torch.randn(n, h, generator=g, device="cuda").to(dtype)
+        w = sv.act8_pack(torch.randn(v, h, generator=g, device="cuda"))
+        a = sv.act8_pack(x)
+        codes = torch.full((16 + n * (h + off),), 77, dtype=torch.int8, device="cuda")
+        scale = torch.empty(n, device="cuda")
+        body = codes[off:off + n * (h + off)].view(n, h + off)
+        assert lib.sv_act8_pack(n, h, code, ptr(x), 0, ptr(body), h + off, ptr(scale), stream_now()) == 0
+        assert torch.equal(body[:, :h], a.codes) and torch.equal(scale, a.scale)
+        assert (body[:, h:] == 77).all() and (codes[:off] == 77).all() and (codes[off + n * (h + off):] == 77).all()
+        y = torch.full((n * h + 16,), 5.0, dtype=dtype, device="cuda")
+        assert lib.sv_act8_unpack(n, h, ptr(body), h + off, ptr(scale), code, ptr(y[off:]), stream_now()) == 0
+        assert torch.equal(y[off:off + n * h].view(n, h), sv.act8_unpack(a, dtype))
+        assert (y[:off] == 5).all() and (y[off + n * h:] == 5).all()
+        out = torch.full((off + n * (v + off) + 16,), 5.0, dtype=dtype, device="cuda")
+        rows = out[off:off + n * (v + off)].view(n, v + off)
+        shape = sv.sv_logits_shape_t(n, h, v, 2, code, h + off, w.codes.stride(0), v + off)
+        ws = torch.empty(lib.sv_head_logits_workspace_bytes(ctypes.byref(shape)), dtype=torch.uint8, device="cuda")
+        assert lib.sv_head_logits(ctypes.byref(shape), ptr(body), ptr(scale), ptr(w.codes), ptr(w.scale), ptr(rows), ptr(ws),
+                                  ws.numel(), stream_now()) == 0
+        assert torch.equal(rows[:, :v], sv.head_logits(a, w, out_dtype=dtype))
+        assert (rows[:, v:] == 5).all() and (out[:off] == 5).all() and (out[off + n * (v + off):] == 5).all()
+
+
+@pytest.mark.parametrize("n,h,v,dtype,code", [(24, 512, 3000, F, 0), (24, 77, 3001, BF, 1), (40, 100, 900, F, 0),
+                                              (60, 1000, 4000, BF, 1), (150, 200, 5000, BF, 1), (260, 500, 70000, BF, 1)])
+def test_ce_guards(sv, n, h, v, dtype, code):
+    """A workspace of exactly the stated size and gradients that begin at any element:
+    the front end's bits, and nothing around them is written."""
+    import ctypes
+    log(f"head_ce guards n={n} h={h} v={v} {dtype}")
+    lib = sv.load_library()
+    hidden, x, w, t, u = ce_case(sv, n, h, v, dtype, "same", 1.0, n + h)
+    want = sv.head_ce(hidden, w, t, u)
+    t = t.int()
+    shape = sv.sv_head_shape_t(n, h, v, code, code, 3, 0, 0, 1.0, -1, 0, 0, float("inf"))
+    need = lib.sv_head_ce_workspace_bytes(ctypes.byref(shape))
+    ws = torch.full((need + 65536,), 0xff, dtype=torch.uint8, device="cuda")
+    res = torch.full((n + 1 + 8,), 5.0, device="cuda")
+    gh, gw = (torch.full((k * h + 16,), 5.0, dtype=dtype, device="cuda") for k in (n, v))
+    assert lib.sv_head_ce(ctypes.byref(shape), ptr(hidden), None, ptr(w), ptr(t), ptr(u), ptr(res), None, None, ptr(res[n:]),
+                          ptr(gh[3:]), ptr(gw[1:]), ptr(ws), need, stream_now()) == 0
+    assert torch.equal(res[:n], want.nll) and torch.equal(res[n:n + 1], want.loss) and (res[n + 1:] == 5).all()
+    assert torch.equal(gh[3:3 + n * h].view(n, h), want.grad_hidden)
+    assert torch.equal(gw[1:1 + v * h].view(v, h), want.grad_weight)
+    for b, lo, k in ((gh, 3, n * h), (gw, 1, v * h)):
+        assert (b[:lo] == 5).all() and (b[lo + k:] == 5).all()
+    assert (ws[need:] == 0xff).all()
 
 
 def test_rollout_step_together(sv):
