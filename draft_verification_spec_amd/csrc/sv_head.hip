@@ -599,8 +599,11 @@ __global__ __launch_bounds__(256) void dz_kept_kernel(Head P, Prod G) {
       *(f32x4 *)(P.dzw + (r0 >> 2) * P.dzw_ld + (int64_t)(c + i) * 16) = f32x4{w[0][i], w[1][i], w[2][i], w[3][i]};
 }
 
-// Distillation: dz at the stored entries of a piece, u (q - pt), from the entries' own
-// logits, over what the tiles stored there.
+// Distillation: dz at the stored entries of a piece, u (q - pt), over what the tiles
+// stored there.  bf16: from the entries' own logits, as the tiles' u q was rounded.
+// fp32: from the tiles' u q, whose logit is the one in the normaliser: where a few
+// entries hold most of q, the roundings of two different sums of it do not cancel
+// (24 rows of 512 x 20000 whose first four entries do: 1.7e-6 of dx, so 2.7e-7).
 template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod G) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int at = (int)(i / TOP), j = (int)(i - (int64_t)at * TOP);
@@ -609,11 +612,18 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
   if (ga == 0.f) return;
   const int64_t n = P.perm[at], c = P.tidx[n * TOP + j] - G.v0;
   if (c < 0 || c >= G.N || !(P.tval[n * TOP + j] > NEG_INF)) return;   // another piece, or padding
-  // ga holds the normaliser's part beyond fp32, which is q's alone
-  const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -P.w[n] * P.pt[i]);
   constexpr int B = 16 / Mma<DT>::E;
-  if (P.gh) store_real<DT>(P.dz + at * P.dz_ld, c, d);
-  if (P.gw) store_real<DT>(P.dzw + at / B * P.dzw_ld, c * B + at % B, P.h_scale ? d * P.h_scale[n] : d);
+  const float u = P.w[n] * P.pt[i], s = P.h_scale ? P.h_scale[n] : 1.f;
+  char *const z = P.dz + at * P.dz_ld, *const zw = P.dzw + at / B * P.dzw_ld;
+  if constexpr (DT == SV_F32) {          // (an entry stands once in a row)
+    if (P.gh) store_real<DT>(z, c, load_real<DT>(z, c) - u);
+    if (P.gw) store_real<DT>(zw, c * B + at % B, fmaf(-u, s, load_real<DT>(zw, c * B + at % B)));
+  } else {
+    // ga holds the normaliser's part beyond fp32, which is q's alone
+    const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -u);
+    if (P.gh) store_real<DT>(z, c, d);
+    if (P.gw) store_real<DT>(zw, c * B + at % B, d * s);
+  }
 }
 
 // How a piece's dx is shared out: its steps are cut into a few chunks (as many as
