@@ -28,9 +28,10 @@
 // Columns: a lane reads, for each of its k, the neighbouring columns that its F
 // fragments hold (fragment f's index i is column i F + f), and bf16 pairs of k are
 // put together by byte permutes; the parts of k read together are turned against
-// each other.  Blocks: a piece is a lane's, as with rows.  (The LDS read that transposes by itself does not serve: the compiler
-// lets it wait for every load into LDS, those for later steps among them; dW ran
-// at 1.0 PFLOP/s with it, measured at 2048 x 4096 x 65536.)
+// each other.  Blocks: a piece is a lane's, as with rows.  (The LDS read that
+// transposes by itself does not serve: the compiler lets it wait for every load into
+// LDS, those for later steps among them; dW ran at 1.0 PFLOP/s with it, measured at
+// 2048 x 4096 x 65536.)
 // The columns' fragment is the instruction's first operand: a lane then holds
 // four n of one m; index_of tells which.
 #pragma once

@@ -123,7 +123,8 @@ struct Head {
 };
 
 // ---------------------------------------------------------------- rows' inputs
-// The distillation's weight and data errors of a row: one wave per row.
+// The distillation's weight and data errors of a row: one wave per row (a launch's
+// time: 4.5 us at 24 rows, 6.4 at 4096).
 __global__ __launch_bounds__(256) void kd_rows_kernel(Head P) {
   const int lane = threadIdx.x & 63;
   const int n = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -237,7 +238,9 @@ template <bool KD> __global__ __launch_bounds__(1024) void order_kernel(Head P) 
 // distillation also z of the stored entries (fp32 sums, an entry a wave).  8-bit codes
 // are exact in bf16 and fp32; their scale goes into alpha.  FIND: a workgroup per row
 // that finds its place itself, for batches of at most FIND_ROWS rows (each looks at
-// all of them), which saves the order's launch.
+// all of them), which saves the order's launch.  Bound by reading: 4096 rows of 4096 in
+// bf16 26 us; with the stored entries' logits 32 rows of the head a row, 4096 of 2048
+// 109 us (537 MB, 4.9 TB/s).
 constexpr int FIND_ROWS = 1024;
 
 template <int HT, int DT, bool KD, bool FIND>
@@ -321,7 +324,10 @@ struct Prod {
 };
 
 // Forward tile: each row's maximum m (base 2) and sum of 2^(z log2 e - m) over
-// the tile's columns.  A NaN makes both NaN, +inf alone only the sum.
+// the tile's columns.  A NaN makes both NaN, +inf alone only the sum.  Bound by the
+// matrix instructions (3072 rows of 4096 x 151936 in bf16 2.85 ms, 1.34 PFLOP/s; a
+// library's product of 8192^3 reaches 1.43), and by reading the head where rows are few
+// (24 rows 280 us, 4.4 TB/s).
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   const int M = P.counts[1], mt = (M + T::BM - 1) / T::BM;
@@ -480,7 +486,9 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
 
 // Backward tile of a piece: dz = u (2^(z log2 e - lse2)), rounded to the
 // operands' type; zeros in the rows up to a whole step and in the columns up to a
-// whole tile, so that both gradients can sum whole steps.
+// whole tile, so that both gradients can sum whole steps.  The product again: keeping
+// the logits would be 2.5 GB at 4096 rows, and their reading and writing as long as a
+// third of it.  3072 rows of 4096 x 151936 3.4 ms, with 1.9 GB written for dx and dW.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   constexpr int Q = STEP / Mma<DT>::E;
@@ -562,7 +570,8 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
 
 // The same from logits that the forward product kept: fp32 products are slow enough
 // (154 TFLOP/s) that a piece's logits are worth their memory where the piece is all of
-// the vocabulary.  A thread takes 4 rows x 4 columns.
+// the vocabulary.  A thread takes 4 rows x 4 columns (24 rows x 20000 6.6 us, most of it
+// the launch).
 __global__ __launch_bounds__(256) void dz_kept_kernel(Head P, Prod G) {
   const int M = P.counts[0], Mp = (M + 31) / 32 * 32;
   if ((int)blockIdx.x >= G.mt) {         // (G.mt: groups of rows)
@@ -633,6 +642,8 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
 // chunk in one line, cut into equal runs, one per workgroup, so that the chip is full
 // whatever the number of tiles.  A run touches a few tiles and adds its part of each to
 // a sum of its own (fp32, kept from piece to piece); a tile's sums are joined at the end.
+// 3072 rows of 4096 x 151936 3.2 ms, 1.19 PFLOP/s: beside the matrix instructions the
+// byte permutes that pair up the head's rows take the vector units' time.
 struct Share {
   int nt, full, per, runs;               // column tiles, steps of a tile's chunk, of a run; runs of a chunk
   __device__ __forceinline__ Share(const Prod &G, int M, int bm) {
@@ -761,7 +772,8 @@ template <int DT, class T> __global__ __launch_bounds__(64 * RUNS<T>) void dx_ro
   dx_rows_part<DT, T, RUNS<T>>(P, G, blockIdx.x, red);
 }
 
-// dW of a piece: complete, in the weight's type.
+// dW of a piece: complete, in the weight's type.  3072 rows of 4096 x 151936 2.95 ms,
+// 1.30 PFLOP/s; 750 of 2048 500 us, of which its 622 MB take 120.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   int im, in;
@@ -915,7 +927,8 @@ __device__ __forceinline__ void kd_row(const Head &P, int at, int n, int F, doub
 
 // The normaliser of each row from its tiles and the row's results.  Lanes take (row,
 // part of the tiles), waves take parts too, all joined in a fixed order; then one
-// thread per row, and for the distillation one wave per row.
+// thread per row, and for the distillation one wave per row.  14 us at 4096 rows, 6 at
+// 24: a chain of dependent steps, not bytes.
 template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Head P, int tiles, int per) {
   __shared__ float ms[16][64];
   __shared__ double ss[16][64], l2s[64];
@@ -1148,10 +1161,11 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.dzw_ld = L.dzw_ld;
   P.wt = ws + L.wt;
   P.acc = (float *)(ws + L.acc);
-  // tiles by the number of rows: 256 rows a tile read each operand least; fewer
-  // rows than a tile would be multiplied in vain, and where 128 columns a tile leave
-  // CUs without one, 64 do (24 x 1024 x 20000: dz 12.3 to 10.8 us).  The fp32 matrix
-  // rate leaves time to read 64 x 64 tiles, which fill the chip sooner.
+  // tiles by rows and entries (large_tiles); up to 32 rows 32 a tile, as the rest would
+  // be multiplied in vain (33 to 64 rows of 4096 x 151936 in two of them 1340 to 1370 us
+  // against 1240 to 1260), and where 128 columns a tile leave CUs without one, 64 do (24 x
+  // 1024 x 20000: dz 12.3 to 10.8 us).  The fp32 matrix rate leaves time to read 64 x 64
+  // tiles, which fill the chip sooner.
   if (s.dtype == SV_BF16)
     return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
            : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)

@@ -26,6 +26,12 @@ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int64_t spread(int64_t n) { return (cdiv(n, 128) | 1) * 128; }
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 inline int esize(int dtype) { return dtype == SV_F32 ? 4 : dtype == SV_BF16 ? 2 : 1; }
+// Tiles of 256 x 256 instead of 128 x 128: they read each operand half as often (190 rows
+// of 4096 x 151936: 8-bit logits 214 to 199 us, cross entropy 1740 to 1510), but where
+// those of 128, two a CU, are one round, they would leave CUs without one (250 rows of
+// 1024 x 32000, 125 tiles: 24 to 21 and 164 to 140; 250 of 4096 x 8000: 48 to 30 and 247
+// to 165), and 128 rows or fewer are one row of the smaller tiles.
+inline bool large_tiles(int64_t N, int64_t V) { return N > 128 && cdiv(N, 128) * cdiv(V, 128) > 2 * CUS; }
 inline bool real_dtype(int dt) { return dt == SV_F32 || dt == SV_BF16; }
 
 // ------------------------------------------------------------------- 8-bit rows
@@ -130,7 +136,7 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   const int64_t N = s->N, H = s->H, T = kd ? TOP : 1;
   p.Kp = up(H, q);
   p.Np = up(N, q);
-  p.bm = N <= 32 ? 32 : s->dtype == SV_F32 ? 64 : N < 192 ? 128 : 256;
+  p.bm = N <= 32 ? 32 : s->dtype == SV_F32 ? 64 : large_tiles(N, s->V) ? 256 : 128;
   p.bn = p.bm == 32 ? 128 : p.bm;
   p.narrow = p.bm == 32 && s->V < 2 * CUS * 128;
   // A piece: its dz, for dx and for dW, and a copied weight take PIECE bytes together;
@@ -148,8 +154,10 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   p.piece = up(cdiv(s->V, p.pieces), 256);
   p.pieces = cdiv(s->V, p.piece);
   p.keep = s->grads && s->dtype == SV_F32 && p.pieces == 1;
-  // the hidden gradient's workgroups: as many as run at once (LDS: one tile of
-  // 256, two of 128 or 32, four of 64 rows a CU), fewer where a run would be short
+  // the hidden gradient.  Workgroups: as many as run at once (LDS: one tile of 256, two
+  // of 128 or 32, four of 64 rows a CU), fewer where a run would be short.  Chunks: no
+  // more than workgroups share a tile (4096 rows of 4096 x 151936 in eight: 3220 to 3820
+  // us, for the sums)
   const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), steps = p.piece * e / STEP;
   const int64_t most_groups = CUS * (p.bm == 256 ? 1 : p.bm == 64 ? 4 : 2), g = cdiv(tiles * steps, RUN);
   p.groups = (int)(g < most_groups ? g < 1 ? 1 : g : most_groups);

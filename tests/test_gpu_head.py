@@ -237,6 +237,22 @@ def test_ce(sv, n, h, v, dtype, kind, tau):
     check_ce(sv, hidden, x, w, t, u, tau, dtype)
 
 
+@pytest.mark.parametrize("kind,tau", [("same", 0.7), ("i8", 1.0)])
+@pytest.mark.parametrize("n,h,v", [(129, 100, 33000), (257, 64, 22017), (300, 192, 21900), (600, 72, 13111), (1100, 128, 7300)])
+def test_ce_large_tiles(sv, n, h, v, kind, tau):
+    """Enough tiles of 128 for those of 256 to take their place, ragged both ways."""
+    log(f"head_ce large n={n} h={h} v={v} {kind}")
+    hidden, x, w, t, u = ce_case(sv, n, h, v, BF, kind, tau, n + h)
+    t[n // 3::4] = -1
+    check_ce(sv, hidden, x, w, t, u, tau, BF)
+
+
+@pytest.mark.parametrize("kind,out", [(BF, BF), (F, F), ("i8", BF), ("i8", F)])
+@pytest.mark.parametrize("n,h,v", [(129, 200, 33001), (300, 384, 22000), (128, 100, 33000), (1000, 65, 8255)])
+def test_logits_large_tiles(sv, n, h, v, kind, out):
+    test_logits(sv, n, h, v, kind, out)
+
+
 @pytest.mark.parametrize("grad", [False, "hidden", "weight"])
 def test_ce_some_gradients(sv, grad):
     log(f"head_ce grad={grad}")
@@ -417,6 +433,12 @@ def check_kd(sv, hidden, x, w, val, ids, rs, rewards, group, dtype, w_max=float(
 def test_kd(sv, n, h, v, dtype, kind):
     log(f"head_kd n={n} h={h} v={v} {dtype} {kind}")
     check_kd(sv, *kd_case(sv, n, h, v, dtype, kind, n + h + v), dtype)
+
+
+@pytest.mark.parametrize("kind", ["same", "i8"])
+@pytest.mark.parametrize("n,h,v", [(140, 72, 33000), (520, 128, 13100)])
+def test_kd_large_tiles(sv, n, h, v, kind):
+    test_kd(sv, n, h, v, BF, kind)
 
 
 def test_kd_clip_and_pieces(sv):
