@@ -325,9 +325,9 @@ struct Prod {
 
 // Forward tile: each row's maximum m (base 2) and sum of 2^(z log2 e - m) over
 // the tile's columns.  A NaN makes both NaN, +inf alone only the sum.  Bound by the
-// matrix instructions (3072 rows of 4096 x 151936 in bf16 2.85 ms, 1.34 PFLOP/s; a
-// library's product of 8192^3 reaches 1.43), and by reading the head where rows are few
-// (24 rows 280 us, 4.4 TB/s).
+// matrix instructions (a rollout of 4096 rows of 4096 x 151936 in bf16, a quarter of
+// them left out: 2.85 ms, 1.34 PFLOP/s; a library's product of 8192^3 reaches 1.43), and
+// by reading the head where rows are few (24 rows 280 us, 4.4 TB/s).
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   const int M = P.counts[1], mt = (M + T::BM - 1) / T::BM;
@@ -488,7 +488,7 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
 // operands' type; zeros in the rows up to a whole step and in the columns up to a
 // whole tile, so that both gradients can sum whole steps.  The product again: keeping
 // the logits would be 2.5 GB at 4096 rows, and their reading and writing as long as a
-// third of it.  3072 rows of 4096 x 151936 3.4 ms, with 1.9 GB written for dx and dW.
+// third of it.  The rollout of the forward tile: 3.4 ms, with 1.9 GB written for dx, dW.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   constexpr int Q = STEP / Mma<DT>::E;
@@ -642,8 +642,8 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
 // chunk in one line, cut into equal runs, one per workgroup, so that the chip is full
 // whatever the number of tiles.  A run touches a few tiles and adds its part of each to
 // a sum of its own (fp32, kept from piece to piece); a tile's sums are joined at the end.
-// 3072 rows of 4096 x 151936 3.2 ms, 1.19 PFLOP/s: beside the matrix instructions the
-// byte permutes that pair up the head's rows take the vector units' time.
+// The rollout of the forward tile: 3.2 ms, 1.19 PFLOP/s; beside the matrix instructions
+// the byte permutes that pair up the head's rows take the vector units' time.
 struct Share {
   int nt, full, per, runs;               // column tiles, steps of a tile's chunk, of a run; runs of a chunk
   __device__ __forceinline__ Share(const Prod &G, int M, int bm) {
@@ -772,8 +772,8 @@ template <int DT, class T> __global__ __launch_bounds__(64 * RUNS<T>) void dx_ro
   dx_rows_part<DT, T, RUNS<T>>(P, G, blockIdx.x, red);
 }
 
-// dW of a piece: complete, in the weight's type.  3072 rows of 4096 x 151936 2.95 ms,
-// 1.30 PFLOP/s; 750 of 2048 500 us, of which its 622 MB take 120.
+// dW of a piece: complete, in the weight's type.  The rollout of the forward tile: 2.95
+// ms, 1.30 PFLOP/s; 750 rows of 2048 x 151936 500 us, of which its 622 MB take 120.
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   int im, in;
