@@ -74,6 +74,15 @@ __device__ __forceinline__ void store_columns(char *p, int64_t row, int n, int N
   }
 }
 
+// Up to PAIR rows in bf16 take half a step of dW's sum and half a tile of dx's, whose
+// times are the head's and dW's bytes anyway: the other halves hold what dz's rounding to
+// bf16 leaves, in rows PAIR further on.  Few rows' gradients hang on few entries of dz,
+// whose roundings do not average: 24 rows of 1024 x 20000, distillation, an error of 0.0023
+// to 0.0026 of the norm with one term, 0.0017 with two, which is the results' own
+// rounding; 65 to 70 us, and 24 rows of 4096 x 151936 1115 to 1080.
+constexpr int PAIR = 32;
+__device__ __forceinline__ float rest_of(float d) { return d - (float)(__bf16)d; }
+
 // What the kernels share: the call's arrays and the workspace.
 struct Head {
   int32_t N, H, V, T;                    // T: targets per row
@@ -84,6 +93,7 @@ struct Head {
   int64_t x_ld, dz_ld;                   // bytes between rows of xs, of dz
   int64_t xw_ld, dzw_ld;                 // bytes between rows of blocks
   int32_t keep;                          // the forward product leaves its logits in dz (fp32, one piece)
+  int32_t split;                         // dz in two bf16 terms (PAIR)
   const char *hidden;
   int64_t h_ld;                          // bytes
   const float *h_scale;
@@ -492,7 +502,8 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   constexpr int Q = STEP / Mma<DT>::E;
-  const int M = P.counts[0], Mp = (M + Q - 1) / Q * Q, mt = (Mp + T::BM - 1) / T::BM;
+  constexpr bool SPLIT = DT == SV_BF16 && T::BM == PAIR;
+  const int M = P.counts[0], Mp = SPLIT ? (M ? PAIR : 0) : (M + Q - 1) / Q * Q, mt = (Mp + T::BM - 1) / T::BM;
   if ((int)blockIdx.x >= G.mt * G.nt) {
     loss_part<DT>(P, blockIdx.x - G.mt * G.nt, (double *)lds);
     return;
@@ -535,8 +546,14 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
       if constexpr (DT == SV_BF16) {
 #pragma unroll
         for (int g = 0; g < T::FN; g += 2)
-          *(u32x4 *)(P.dz + m * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + beside.at) * 2) =
-              Beside::eight(d[g], d[g + 1]);
+#pragma unroll
+          for (int k = 0; k < (SPLIT ? 2 : 1); ++k) {
+            float r[2][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i / 4][i % 4] = k ? rest_of(d[g + i / 4][i % 4]) : d[g + i / 4][i % 4];
+            *(u32x4 *)(P.dz + (m + k * PAIR) * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + beside.at) * 2) =
+                Beside::eight(r[0], r[1]);
+          }
       } else {
 #pragma unroll
         for (int g = 0; g < T::FN; ++g) store4<DT>(P.dz + m * P.dz_ld, n + g * 16, d[g]);
@@ -544,7 +561,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
     }
     if (P.gw) {
       char *at = P.dzw + m / (16 / Mma<DT>::E) * P.dzw_ld;
-      u32x4 o[T::FN];                    // bf16: every second one
+      u32x4 o[T::FN];                    // bf16: every second one, and in the others what is left of it
 #pragma unroll
       for (int g = 0; g < T::FN; ++g) {
 #pragma unroll
@@ -554,15 +571,24 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
       if constexpr (DT == SV_BF16) {
 #pragma unroll
         for (int g = 0; g < T::FN; g += 2)
-          o[g] = turn.eight(turn.four(pack2(d[g][0], d[g][1]), pack2(d[g][2], d[g][3])),
-                            turn.four(pack2(d[g + 1][0], d[g + 1][1]), pack2(d[g + 1][2], d[g + 1][3])));
+#pragma unroll
+          for (int k = 0; k < (SPLIT ? 2 : 1); ++k) {
+            float r[2][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i / 4][i % 4] = k ? rest_of(d[g + i / 4][i % 4]) : d[g + i / 4][i % 4];
+            o[g + k] = turn.eight(turn.four(pack2(r[0][0], r[0][1]), pack2(r[0][2], r[0][3])),
+                                  turn.four(pack2(r[1][0], r[1][1]), pack2(r[1][2], r[1][3])));
+          }
         at += (n + 2 * turn.k0 + turn.k1 + 16 * turn.b2) * 16;
       } else {
         at += (n + turn.b0 + 2 * turn.b1) * 16;
       }
       if (m < Mp) {
 #pragma unroll
-        for (int g = 0; g < T::FN; g += DT == SV_BF16 ? 2 : 1) *(u32x4 *)(at + g * 256) = o[g];
+        for (int g = 0; g < T::FN; g += DT == SV_BF16 ? 2 : 1) {
+          *(u32x4 *)(at + g * 256) = o[g];
+          if constexpr (SPLIT) *(u32x4 *)(at + PAIR / 8 * P.dzw_ld + g * 256) = o[g + 1];
+        }
       }
     }
   }
@@ -632,6 +658,10 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
     const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -u);
     if (P.gh) store_real<DT>(z, c, d);
     if (P.gw) store_real<DT>(zw, c * B + at % B, d * s);
+    if (P.split) {
+      if (P.gh) store_real<DT>(z + PAIR * P.dz_ld, c, rest_of(d));
+      if (P.gw) store_real<DT>(zw + PAIR / B * P.dzw_ld, c * B + at % B, rest_of(d * s));
+    }
   }
 }
 
@@ -656,9 +686,15 @@ struct Share {
   }
 };
 
+// whether tile T of dx holds dz's two terms
+template <int DT, class T> constexpr bool BOTH = DT == SV_BF16 && T::BM == 2 * PAIR;
+// a wave's fragment rows of one term (the other's lie in the same wave), and a tile's sums
+template <int DT, class T> constexpr int TERM = BOTH<DT, T> ? T::FM / 2 : T::FM;
+template <int DT, class T> constexpr int SUM = T::BM * T::BN / (T::FM / TERM<DT, T>);
+
 template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
-  const int M = P.counts[0];
+  const int M = BOTH<DT, T> ? (P.counts[0] ? 2 * PAIR : 0) : P.counts[0];
   const Share S(G, M, T::BM);
   const int mt = (M + T::BM - 1) / T::BM;
   const int64_t total = (int64_t)mt * S.nt * S.full;
@@ -667,8 +703,8 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
   if (at >= total) return;
   int left = __builtin_amdgcn_readfirstlane((int)(at + S.per < total ? S.per : total - at));
   int t = __builtin_amdgcn_readfirstlane((int)(at / S.full)), from = __builtin_amdgcn_readfirstlane((int)(at % S.full));
-  float *out = P.acc + (int64_t)b * G.slots * (T::BM * T::BN) + threadIdx.x * 4;
-  for (; left > 0; ++t, from = 0, out += T::BM * T::BN) {
+  float *out = P.acc + (int64_t)b * G.slots * SUM<DT, T> + threadIdx.x * 4;
+  for (; left > 0; ++t, from = 0, out += SUM<DT, T>) {
     int ns = left < S.full - from ? left : S.full - from;
     left -= ns;
     const int s0 = c * S.full + from;
@@ -686,11 +722,12 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
     const Part Y = {G.y + (int64_t)n0 * Mma<DT>::E, G.y_ld, G.M, (P.Kp - n0) * Mma<DT>::E};
     product<DT, T, ROWS, COLS>(acc, lds, X, Y, s0, ns);
 #pragma unroll
-    for (int f = 0; f < T::FM; ++f)
+    for (int f = 0; f < TERM<DT, T>; ++f)
 #pragma unroll
       for (int g = 0; g < T::FN; ++g) {
         f32x4 *o = (f32x4 *)(out + (f * T::FN + g) * (T::TPB * 4));
         f32x4 v = acc[f][g];
+        if constexpr (BOTH<DT, T>) v += acc[f + TERM<DT, T>][g];
         if (!G.first) v += *o;
         *o = v;
       }
@@ -709,7 +746,7 @@ template <class T> using Runs = f32x4[RUNS<T> > 1 ? RUNS<T> - 1 : 1][T::FN][64];
 template <int DT, class T, int WS>
 __device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int block, Runs<T> &red) {
   const int M = P.counts[0], lane = threadIdx.x & 63, ws = threadIdx.x >> 6;
-  constexpr int PER = T::NW * T::FM;
+  constexpr int PER = T::NW * TERM<DT, T>;
   const int tile = block / PER, f = block % PER / T::NW, wid = block % T::NW;
   const int in = tile % G.nt, im = tile / G.nt, m0 = im * T::BM, n0 = in * T::BN;
   const int wm = wid / T::WN, wn = wid % T::WN;
@@ -740,7 +777,7 @@ __device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int b
 #pragma unroll
         for (int q = 0; q < T::FN; ++q) {
           o[e][q] = 0;
-          if (b + e < end) o[e][q] = *(const f32x4 *)(s + slot * (T::BM * T::BN) + q * (T::TPB * 4));
+          if (b + e < end) o[e][q] = *(const f32x4 *)(s + slot * SUM<DT, T> + q * (T::TPB * 4));
         }
       }
 #pragma unroll
@@ -835,7 +872,8 @@ template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(
   const int nm = (G.M + 255) / 256, m0 = (block % nm) * 256 + (threadIdx.x >> 6) * 64;
   const int c0 = block / nm * span, c1 = c0 + span < G.N ? c0 + span : G.N;
   constexpr int Q = STEP / Mma<DT>::E;
-  const int halves = P.counts[0] > Q / 2 ? 2 : P.counts[0] > 0 ? 1 : 0;   // 64-byte half steps with rows in them
+  // 64-byte half steps with rows in them
+  const int halves = P.counts[0] > Q / 2 || (P.split && P.counts[0]) ? 2 : P.counts[0] > 0 ? 1 : 0;
   if (m0 >= G.M) return;
   u32x4 x[2][4];
 #pragma unroll
@@ -850,6 +888,7 @@ template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(
   char *out = P.gw + G.v0 * P.H * Mma<DT>::E;
   for (int c = c0; c < c1; c += 64) {
     Acc acc[4][4];
+    u32x4 y[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -857,9 +896,9 @@ template <int DT, class T> __global__ __launch_bounds__(256) void dw_few_kernel(
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h >= halves) break;
-      u32x4 y[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        if (h && P.split) break;         // both terms meet the same rows
         const int n = c + column(g, i);
         y[g] = *(const u32x4 *)(G.y + (h * 4 + q) * G.y_ld + (int64_t)(n < G.N ? n : G.N - 1) * 16);
       }
@@ -990,12 +1029,13 @@ __global__ __launch_bounds__(256) void loss_kernel(Head P) {
 
 // ------------------------------------------------------------------------ host
 static_assert(Tile<8, 4, 2, 4>::BM == 256 && Tile<4, 4, 2, 2>::BM == 128 && Tile<2, 2, 2, 2>::BM == 64 &&
-                  Tile<2, 2, 1, 4>::BM == 32,
+                  Tile<2, 2, 1, 4>::BM == 32 && Tile<4, 2, 1, 4>::BM == 2 * PAIR,
               "plan_for's bm");
 typedef Tile<8, 4, 2, 4> Big;            // 256 x 256
 typedef Tile<4, 4, 2, 2> Mid;            // 128 x 128
 typedef Tile<2, 2, 2, 2> Square;         // 64 x 64
 typedef Tile<2, 2, 1, 4> Few;            // 32 x 128
+typedef Tile<4, 2, 1, 4> Pair;           // 64 x 128: dx of few rows in bf16
 typedef Tile<1, 2, 2, 2> Narrow;         // 32 x 64
 
 template <class T> Prod tiled(Prod G, int64_t M, int64_t N) {
@@ -1061,7 +1101,7 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
   }
 
-  Prod X = tiled<T>(Prod{}, P.N, P.H);
+  Prod X = tiled<T>(Prod{}, BOTH<DT, T> ? 2 * PAIR : P.N, P.H);
   X.x = P.dz;
   X.x_ld = L.dz_ld;
   X.chunks = L.chunks;
@@ -1069,13 +1109,13 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
   X.groups = L.groups;
   X.slots = L.slots;
   X.per0 = sv_head_host::RUN;
-  constexpr bool FEW = T::BM == 32 || (DT == SV_BF16 && T::BM == 128);   // tiles that rows of one step take
+  constexpr bool FEW = T::BM == 32 || (DT == SV_BF16 && T::BM < 256);    // tiles that rows of one step take
   const bool few = FEW && P.gw && L.Np * E == STEP;
-  const int64_t frags = (int64_t)X.mt * X.nt * T::NW * T::FM;            // fragment rows of dx's tiles
+  const int64_t frags = (int64_t)X.mt * X.nt * T::NW * TERM<DT, T>;      // fragment rows of dx's tiles
   for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
     const int64_t cp = sv_head_host::up(cnt, 256);       // columns of dz: whole tiles and steps
-    Prod G = tiled<TS>(F, L.Np, cp);
+    Prod G = tiled<TS>(F, BOTH<DT, T> ? PAIR : L.Np, cp);
     weight_piece(G, v0, cnt, L.pieces > 1);              // (a single copied piece is still there)
     G.N = (int32_t)cnt;
     const int64_t loss = v0 ? 0 : P.gw ? L.Np * E / 16 + 1 : 1;
@@ -1136,6 +1176,7 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.x_ld = L.x_ld;
   P.dz_ld = L.dz_ld;
   P.keep = L.keep;
+  P.split = s.dtype == SV_BF16 && L.bm == PAIR;
   P.Np = L.Np;
   P.hidden = (const char *)hidden;
   P.h_ld = (s.hidden_stride ? s.hidden_stride : s.H) * (int64_t)he;
@@ -1171,8 +1212,8 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   if (s.dtype == SV_BF16)
     return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
            : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
-           : L.narrow    ? enqueue<SV_BF16, Few, Mid, Narrow>(P, L, kd, direct, st)
-                         : enqueue<SV_BF16, Few, Mid>(P, L, kd, direct, st);
+           : L.narrow    ? enqueue<SV_BF16, Pair, Mid, Narrow>(P, L, kd, direct, st)
+                         : enqueue<SV_BF16, Pair, Mid, Few>(P, L, kd, direct, st);
   return L.bm == 64 ? enqueue<SV_F32, Square, Square>(P, L, kd, direct, st)
          : L.narrow ? enqueue<SV_F32, Few, Square, Narrow>(P, L, kd, direct, st)
                     : enqueue<SV_F32, Few, Square>(P, L, kd, direct, st);

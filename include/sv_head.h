@@ -105,7 +105,8 @@ int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden, const flo
  * Gradients of both: dx[n,k] = (1/T) sum_v dz[n,v] w[v,k],
  *                    dw[v,k] = (1/T) sum_n dz[n,v] x[n,k].
  * Products of bf16 operands are summed in fp32; for them dz is rounded to bf16
- * (it is an operand of the gradients' products), everything else is fp32 or fp64.
+ * (it is an operand of the gradients' products; up to 32 rows in two bf16 terms),
+ * everything else is fp32 or fp64.
  */
 #define SV_GRAD_HIDDEN 1
 #define SV_GRAD_WEIGHT 2
