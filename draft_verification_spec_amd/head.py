@@ -143,11 +143,16 @@ def act8_pack(x, *, stream=None) -> Act8:
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "rows")
-        N, Hp = r.shape[0], -(-H // 128) * 128
-        codes = torch.empty((*lead, Hp), dtype=torch.int8, device=dev)
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
-        _check(_lib().sv_act8_pack(N, H, dt, r.data_ptr(), ld, codes.data_ptr(), Hp, scale.data_ptr(), st))
-    return Act8(codes if H == Hp else codes[..., :H], scale)
+        Hp = -(-H // 128) * 128
+        steps, ones, n = [1], [], 1              # strides: rows of codes Hp apart, scales without gaps
+        for k in reversed(lead):
+            steps.append(n * Hp)
+            ones.append(n)
+            n *= max(k, 1)
+        codes = torch.empty_strided(x.shape, steps[::-1], dtype=torch.int8, device=dev)
+        scale = torch.empty_strided(lead, ones[::-1], dtype=torch.float32, device=dev)
+        _check(_lib().sv_act8_pack(r.shape[0], H, dt, r.data_ptr(), ld, codes.data_ptr(), Hp, scale.data_ptr(), st))
+    return Act8(codes, scale)
 
 
 def act8_unpack(a: Act8, dtype=None, *, stream=None):
