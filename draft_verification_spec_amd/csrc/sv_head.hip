@@ -79,7 +79,7 @@ __device__ __forceinline__ void store_columns(char *p, int64_t row, int n, int N
 // bf16 leaves, in rows PAIR further on.  Few rows' gradients hang on few entries of dz,
 // whose roundings do not average: 24 rows of 1024 x 20000, distillation, an error of 0.0023
 // to 0.0026 of the norm with one term, 0.0017 with two, which is the results' own
-// rounding; 65 to 70 us, and 24 rows of 4096 x 151936 1115 to 1080.
+// rounding; 3 us of 66, and 24 rows of 4096 x 151936 no more at all.
 constexpr int PAIR = 32;
 __device__ __forceinline__ float rest_of(float d) { return d - (float)(__bf16)d; }
 
@@ -738,7 +738,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dx_kernel(H
 // dx of every row: its tile's sums in a fixed order, rounded once; zeros for rows
 // without a gradient.  A workgroup per fragment row of a tile's wave: the tile's sums
 // are added in RUNS runs, four loads under way at a time, shared out over WS waves, and
-// the first wave joins them.  (Few rows have many sums of a few steps each: 79 at 24
+// the first wave joins them.  (Few rows have many sums of a few steps each: 128 at 24
 // rows of 512 in fp32, which one run took 21 us for; tiles of 256 rows are about as
 // many as workgroups and have few.)
 template <class T> constexpr int RUNS = T::BM == 256 ? 1 : 8;

@@ -16,7 +16,9 @@ constexpr int TOP = 32;                  // stored entries per row (sv_head_kd)
 constexpr int STEP = 128;                // bytes of k per step of the tiled product
 constexpr int CUS = 256;                 // compute units of the GPU
 constexpr int64_t PIECE = (int64_t)512 << 20;   // bytes of a piece's dz and weight
-constexpr int RUN = 8;                   // least steps of a workgroup of the hidden gradient
+// least steps of a workgroup of the hidden gradient (24 rows of 1024 x 20000 56 us with 8,
+// 54 with 4, whose sums ride with dW; 5 of 72 x 53559 49.0 and 50.4)
+constexpr int RUN = 4;
 constexpr int64_t MAX_LD = (int64_t)1 << 22;   // bytes between rows of a tiled operand: a tile's offsets fit 31 bits
 
 inline int64_t cdiv(int64_t x, int64_t m);
@@ -158,11 +160,12 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   // of 128 or 32, four of 64 rows a CU), fewer where a run would be short.  Chunks: no
   // more than workgroups share a tile (4096 rows of 4096 x 151936 in eight: 3220 to 3820
   // us, for the sums)
-  const int64_t tiles = cdiv(N, p.bm) * cdiv(H, p.bn), steps = p.piece * e / STEP;
+  const int64_t tiles = cdiv(N < 1 ? 1 : N, p.bm) * cdiv(H, p.bn), steps = p.piece * e / STEP;
   const int64_t most_groups = CUS * (p.bm == 256 ? 1 : p.bm == 64 ? 4 : 2), g = cdiv(tiles * steps, RUN);
   p.groups = (int)(g < most_groups ? g < 1 ? 1 : g : most_groups);
   p.chunks = 1;
-  while (p.groups == most_groups && p.chunks < 8 && 2 * p.chunks * tiles <= p.groups) p.chunks *= 2;
+  while (p.chunks < 8 && 2 * p.chunks * tiles <= p.groups) p.chunks *= 2;
+  p.groups -= p.groups % p.chunks;
   p.full = (int)cdiv(steps, p.chunks);
   const int64_t run = cdiv(tiles * p.full, p.groups / p.chunks);
   p.slots = (int)(cdiv(run > RUN ? run : RUN, p.full) + 1);

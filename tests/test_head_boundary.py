@@ -103,6 +103,16 @@ def test_loss_refusals(lib, kd):
     assert need(head(g=0)) < need(head(g=2)) <= need(head(g=3))
 
 
+@pytest.mark.parametrize("kd", [False, True])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_workspace_of_an_empty_batch(lib, kd, dt):
+    """A batch without rows has a size like any other, whatever gradients are asked for."""
+    f = lib.sv_head_kd_workspace_bytes if kd else lib.sv_head_ce_workspace_bytes
+    for g in range(4):
+        for h, v in ((1, 1), (64, 100), (4096, 151936), (131072, 1 << 24)):
+            assert f(ctypes.byref(head(N=0, H=h, V=v, dt=dt, g=g, S=0))) > 0
+
+
 def test_workspace_does_not_grow_with_the_logits(lib):
     """A rollout batch: the workspace is a fraction of its float32 logits, and a
     larger vocabulary adds two numbers per row and 128 entries at most, 1/64 of
