@@ -1047,7 +1047,7 @@ template <class T> Prod tiled(Prod G, int64_t M, int64_t N) {
   return G;
 }
 
-template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, const Plan &L, bool kd, bool direct, hipStream_t st) {
+template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &L, bool kd, bool direct, hipStream_t st) {
   constexpr int E = Mma<DT>::E;
   const dim3 b256(256), b1024(1024);
   if (kd) hipLaunchKernelGGL(kd_rows_kernel, dim3((unsigned)cdiv(P.N, 4)), b256, 0, st, P);
@@ -1136,7 +1136,9 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
       hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)L.groups), dim3(T::TPB), 0, st, P, X);
     }
     if (P.gw) {
-      Prod W = tiled<TW>(Prod{}, cnt, P.H);
+      Prod W = {};
+      W.M = (int32_t)cnt;
+      W.N = P.H;
       W.v0 = v0;
       W.x = P.dzw;
       W.x_ld = L.dzw_ld;
@@ -1150,7 +1152,21 @@ template <int DT, class T, class TW, class TS = T> int enqueue(const Head &P, co
                              st, P, W, (int)span, X, (int)sums);
         }
       } else {
-        hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(W.mt * W.nt)), dim3(TW::TPB), 0, st, P, W);
+        auto product = [&](auto tile) {
+          typedef decltype(tile) TW;
+          const Prod Y = tiled<TW>(W, cnt, P.H);
+          hipLaunchKernelGGL((dw_kernel<DT, TW>), dim3((unsigned)(Y.mt * Y.nt)), dim3(TW::TPB), 0, st, P, Y);
+        };
+        // by dW's own size: a small head would leave most CUs without one of the large tiles
+        // (2772 rows of 192 x 4343: 42 us with 256, 23.5 with 128, 15.3 with 64; 4096 of 1024
+        // x 8000, 504 tiles of 128: 57, and 77 with 64)
+        if constexpr (DT == SV_BF16) {
+          if (sv_head_host::large_tiles(cnt, P.H)) product(Big());
+          else if (cdiv(cnt, 128) * cdiv(P.H, 128) >= sv_head_host::CUS) product(Mid());
+          else product(Square());
+        } else {
+          product(Square());
+        }
       }
     }
   }
@@ -1210,13 +1226,13 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   // 1024 x 20000: dz 12.3 to 10.8 us).  The fp32 matrix rate leaves time to read 64 x 64
   // tiles, which fill the chip sooner.
   if (s.dtype == SV_BF16)
-    return L.bm == 256 ? enqueue<SV_BF16, Big, Big>(P, L, kd, direct, st)
-           : L.bm == 128 ? enqueue<SV_BF16, Mid, Mid>(P, L, kd, direct, st)
-           : L.narrow    ? enqueue<SV_BF16, Pair, Mid, Narrow>(P, L, kd, direct, st)
-                         : enqueue<SV_BF16, Pair, Mid, Few>(P, L, kd, direct, st);
-  return L.bm == 64 ? enqueue<SV_F32, Square, Square>(P, L, kd, direct, st)
-         : L.narrow ? enqueue<SV_F32, Few, Square, Narrow>(P, L, kd, direct, st)
-                    : enqueue<SV_F32, Few, Square>(P, L, kd, direct, st);
+    return L.bm == 256 ? enqueue<SV_BF16, Big>(P, L, kd, direct, st)
+           : L.bm == 128 ? enqueue<SV_BF16, Mid>(P, L, kd, direct, st)
+           : L.narrow    ? enqueue<SV_BF16, Pair, Narrow>(P, L, kd, direct, st)
+                         : enqueue<SV_BF16, Pair, Few>(P, L, kd, direct, st);
+  return L.bm == 64 ? enqueue<SV_F32, Square>(P, L, kd, direct, st)
+         : L.narrow ? enqueue<SV_F32, Few, Narrow>(P, L, kd, direct, st)
+                    : enqueue<SV_F32, Few>(P, L, kd, direct, st);
 }
 
 }  // namespace

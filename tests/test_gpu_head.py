@@ -247,6 +247,14 @@ def test_ce_large_tiles(sv, n, h, v, kind, tau):
     check_ce(sv, hidden, x, w, t, u, tau, BF)
 
 
+@pytest.mark.parametrize("n,h,v", [(2772, 192, 4343), (300, 1000, 4999), (1500, 72, 1300), (100, 2000, 3001), (700, 520, 9001)])
+def test_ce_sizes_of_dw(sv, n, h, v):
+    """Heads whose dW takes each of its tiles, beside each tile of the other products."""
+    log(f"head_ce dw n={n} h={h} v={v}")
+    hidden, x, w, t, u = ce_case(sv, n, h, v, BF, "same", 1.0, n + v)
+    check_ce(sv, hidden, x, w, t, u, 1.0, BF)
+
+
 @pytest.mark.parametrize("kind,out", [(BF, BF), (F, F), ("i8", BF), ("i8", F)])
 @pytest.mark.parametrize("n,h,v", [(129, 200, 33001), (300, 384, 22000), (128, 100, 33000), (1000, 65, 8255)])
 def test_logits_large_tiles(sv, n, h, v, kind, out):
