@@ -34,8 +34,14 @@ template <> struct In<SV_F32> {
 
 // The code of x under scale s > 0: x / s rounded to even as if it were exact.
 // The fp32 quotient may round across a border k + 1/2; the remainder
-// x - (k +- 1/2) s is exact in sign as one fused step, and puts the code back.
+// x - (k +- 1/2) s is exact in sign as one fused step, and puts the code back.  Its last
+// place is half of the scale's: below 2^-125 that is no fp32 number (a remainder of
+// 2^-150 would round to a tie), so small rows are taken 2^64 larger, which is exact.
 __device__ __forceinline__ int code_of(float x, float s) {
+  if (s < 0x1p-100f) {
+    x *= 0x1p64f;
+    s *= 0x1p64f;
+  }
   float r = __builtin_rintf(x / s);
   if (fmaf(-(r + 0.5f), s, x) > 0.f) r += 1.f;
   else if (fmaf(-(r - 0.5f), s, x) < 0.f) r -= 1.f;
