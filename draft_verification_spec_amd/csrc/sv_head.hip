@@ -333,6 +333,13 @@ struct Prod {
   int32_t chunks, full, per0, groups, slots;
 };
 
+// The step with which a tile of few rows begins: by its place in the vocabulary, not in
+// the piece, so that a logit's sum has one order however the vocabulary is cut, which
+// depends on whether there are gradients (pieces are whole tiles).
+template <class T> __device__ __forceinline__ int first_step(const Prod &G, int in) {
+  return T::BM == 32 ? (int)((G.v0 / T::BN + in) % G.nk) : 0;
+}
+
 // Forward tile: each row's maximum m (base 2) and sum of 2^(z log2 e - m) over
 // the tile's columns.  A NaN makes both NaN, +inf alone only the sum.  Bound by the
 // matrix instructions (a rollout of 4096 rows of 4096 x 151936 in bf16, a quarter of
@@ -349,7 +356,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void stats_kerne
   clear<DT, T>(acc);
   const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
   const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
-  product<DT, T>(acc, lds, X, Y, 0, G.nk, T::BM == 32 ? in % G.nk : 0);
+  product<DT, T>(acc, lds, X, Y, 0, G.nk, first_step<T>(G, in));
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   __syncthreads();                       // the tiles are done with: their LDS takes the waves' results
   float2 *red = (float2 *)lds;           // [WN][BM]
@@ -517,7 +524,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
   if (m0 < M && n0 < G.N) {
     const Part X = {G.x + (int64_t)m0 * G.x_ld, G.x_ld, M - m0 < T::BM ? M - m0 : T::BM, (int64_t)G.nk * STEP};
     const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
-    product<DT, T>(acc, lds, X, Y, 0, G.nk, T::BM == 32 ? in % G.nk : 0);
+    product<DT, T>(acc, lds, X, Y, 0, G.nk, first_step<T>(G, in));
   }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   const Turn turn;

@@ -34,3 +34,21 @@ def test_act8_smallest_magnitudes(sv, h, dtype):  # noqa: F811
     got = sv.head_logits(x, sv.Act8(ones, torch.ones(1, device="cuda")), out_dtype=F)
     s = codes.double().sum(1)
     within(got[:, 0], s * scale.double(), (s * scale.double()).abs() * 3 * HALF[F] + 2.0 ** -149, "row sums")
+
+
+# --------------------------------------------------------------- cross entropy
+@pytest.mark.parametrize("n,h,v,dtype", [(9, 1001, 130000, F), (24, 1152, 262144, F), (20, 1001, 250000, BF), (9, 1000, 300000, BF)])
+def test_ce_pieces_keep_the_bits(sv, n, h, v, dtype):  # noqa: F811
+    """Few rows whose vocabulary is cut otherwise with gradients than without: the
+    same bits of the loss and of each gradient whatever is asked for."""
+    log(f"head_ce bits over pieces n={n} h={h} v={v} {dtype}")
+    hidden, _, w, t, u = ce_case(sv, n, h, v, dtype, "same", 1.0, n + h)
+    both = sv.head_ce(hidden, w, t, u)
+    for grad in (False, "hidden", "weight"):
+        r = sv.head_ce(hidden, w, t, u, grad=grad)
+        for name in ("loss", "nll", "lse", "status"):
+            assert torch.equal(getattr(r, name), getattr(both, name)), (grad, name)
+        if grad == "hidden":
+            assert torch.equal(r.grad_hidden, both.grad_hidden)
+        if grad == "weight":
+            assert torch.equal(r.grad_weight, both.grad_weight)
