@@ -39,6 +39,9 @@ using sv_head_host::TOP;
 
 constexpr float LOG2E = 1.44269504f;
 constexpr double LN2 = 0.6931471805599453;
+// A logit from its exponent z * LOG2E.  LOG2E is low by 1.3e-8 of itself; ln 2 in place of
+// this would leave that in lse alone (a sure row of z = 1000: nll -1.3e-5).
+constexpr double PER_LOG2E = 1.0 / (double)LOG2E;
 
 template <int DT> __device__ __forceinline__ float load_real(const char *p, int64_t i) {
   if constexpr (DT == SV_BF16) return __uint_as_float((uint32_t)((const uint16_t *)p)[i] << 16);
@@ -960,7 +963,7 @@ __device__ __forceinline__ void kd_row(const Head &P, int at, int n, int F, doub
   const double sv = wave_sum_d(e);
   const double pt = use ? e / sv : 0.0;
   double t = 0.0;
-  if (use && pt > 0.0) t = pt * (a - log(sv) - ((double)P.zt[(int64_t)at * TOP + lane] - l2 * LN2));
+  if (use && pt > 0.0) t = pt * (a - log(sv) - ((double)P.zt[(int64_t)at * TOP + lane] - l2 * PER_LOG2E));
   const double kl = wave_sum_d(t);
   if (lane < TOP) P.pt[(int64_t)at * TOP + lane] = (float)pt;
   if (lane == 0) {
@@ -1013,8 +1016,10 @@ template <bool KD> __global__ __launch_bounds__(1024) void normaliser_kernel(Hea
       u = P.w[n];
     } else {
       u = P.row_weight ? P.row_weight[n] : 1.f;
-      const double lse = l2 * LN2;
-      const float nll = F ? __builtin_nanf("") : (float)(lse - (double)P.zt[at]);
+      const double lse = l2 * PER_LOG2E;
+      // (the target's logit is one of the normaliser's, so less than 0 is rounding)
+      const double less = lse - (double)P.zt[at];
+      const float nll = F ? __builtin_nanf("") : less < 0.0 ? 0.f : (float)less;
       P.rows[n] = nll;
       if (P.lse) P.lse[n] = F ? __builtin_nanf("") : (float)lse;
       if (P.status) P.status[n] = F;

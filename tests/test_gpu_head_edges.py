@@ -52,3 +52,38 @@ def test_ce_pieces_keep_the_bits(sv, n, h, v, dtype):  # noqa: F811
             assert torch.equal(r.grad_hidden, both.grad_hidden)
         if grad == "weight":
             assert torch.equal(r.grad_weight, both.grad_weight)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("n", [4, 40, 300])
+def test_sure_rows(sv, n, dtype):  # noqa: F811
+    """Rows whose target stands far above the others: nll is what the exponentials'
+    rounding leaves of 0, at any size of the logits, and never negative.  Logits are
+    exact here (one product each, of powers of two and small numbers).  The largest
+    exponential is 2 to the rounding of its own exponent: one rounding, one of the
+    hardware's last place, 2^-23 each; the distillation's the same."""
+    log(f"head_ce, head_kd sure rows n={n} {dtype}")
+    z = torch.tensor([30.0, 100, 300, 1000, 1100, 9984, 28672], device="cuda")
+    v = 700
+    for sign in (1, -1):                              # 28672 above the others, which are at 0, or 0 above them
+        w = torch.zeros(v, 64, device="cuda")
+        w[7, 0] = 1
+        x = torch.zeros(n, 64, device="cuda")
+        x[:, 0] = z[torch.arange(n, device="cuda") % len(z)]
+        if sign < 0:
+            w[:, 0] -= 1
+        x, w = x.to(dtype), w.to(dtype)
+        t = torch.full((n,), 7, device="cuda")
+        r = sv.head_ce(x, w, t)
+        top = x[:, 0].double() if sign > 0 else torch.zeros(n, device="cuda").double()
+        rest = (v - 1) * torch.exp(-x[:, 0].double())
+        bound = rest + 2.0 ** -22
+        assert not r.status.any() and (r.nll >= 0).all() and float(r.loss) >= 0
+        within(r.nll, torch.zeros_like(top), bound, "nll")
+        within(r.lse, top, bound + HALF[F] * top, "lse")
+        val = torch.full((n, 32), -float("inf"), device="cuda")
+        val[:, 3] = 1
+        ids = torch.full((n, 32), -1, device="cuda")
+        ids[:, 3] = 7
+        k = sv.head_kd(x, w, val, ids, torch.arange(n, device="cuda") % 4, torch.ones(4, device="cuda"), 4)
+        within(k.kl, torch.zeros_like(top), bound, "kl")
