@@ -7,6 +7,7 @@
 
 #include "sv_device.h"
 #include "sv_head.h"
+#include "sv_head_host.h"
 
 namespace sv_act8 {
 
@@ -225,9 +226,15 @@ template <int DT> void pack_as(int N, Pack P, hipStream_t st) {
   else hipLaunchKernelGGL((pack_kernel<DT>), each, block, 0, st, P);
 }
 
-inline void pack(int dtype, int N, const Pack &P, hipStream_t st) {
-  if (dtype == SV_BF16) pack_as<SV_BF16>(N, P, st);
-  else pack_as<SV_F32>(N, P, st);
+inline void pack(int dtype, int N, Pack P, hipStream_t st) {
+  for (int64_t left = N; left > 0; left -= sv_head_host::MAX_ROWS) {
+    const int n = (int)(left < sv_head_host::MAX_ROWS ? left : sv_head_host::MAX_ROWS);
+    if (dtype == SV_BF16) pack_as<SV_BF16>(n, P, st);
+    else pack_as<SV_F32>(n, P, st);
+    P.x += n * P.x_ld;
+    P.codes += n * P.c_ld;
+    P.scale += n;
+  }
 }
 
 }  // namespace sv_act8

@@ -42,6 +42,7 @@
 #include <type_traits>
 
 #include "sv_head.h"
+#include "sv_head_host.h"
 
 namespace sv_gemm {
 
@@ -478,8 +479,11 @@ static inline void copy_rows(const void *src, int64_t ld, int64_t bytes, char *d
   const int chunks = (int)(d_bytes / 16);
   int lg = 3;                                            // (whole steps: 8 chunks or more)
   while (lg < 6 && (1 << lg) < chunks) ++lg;
-  hipLaunchKernelGGL(copy_rows_kernel, dim3((unsigned)((rows + (256 >> lg) - 1) / (256 >> lg))), dim3(256), 0, st,
-                     (const char *)src, ld, bytes, dst, d_ld, chunks, (int)rows, lg);
+  for (int64_t r = 0; r < rows; r += sv_head_host::MAX_ROWS) {
+    const int64_t n = rows - r < sv_head_host::MAX_ROWS ? rows - r : sv_head_host::MAX_ROWS;
+    hipLaunchKernelGGL(copy_rows_kernel, dim3((unsigned)((n + (256 >> lg) - 1) / (256 >> lg))), dim3(256), 0, st,
+                       (const char *)src + r * ld, ld, bytes, dst + r * d_ld, d_ld, chunks, (int)n, lg);
+  }
 }
 
 }  // namespace sv_gemm

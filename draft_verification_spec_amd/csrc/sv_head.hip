@@ -814,9 +814,9 @@ __device__ __forceinline__ void dx_rows_part(const Head &P, const Prod &G, int b
   store_columns<DT, T::FN>(P.gh, (int64_t)P.perm[m] * P.H, n0 + index_of<T::FN, COLS>(wn, 0, (lane >> 4) * 4), P.H, v);
 }
 
-template <int DT, class T> __global__ __launch_bounds__(64 * RUNS<T>) void dx_rows_kernel(Head P, Prod G) {
+template <int DT, class T> __global__ __launch_bounds__(64 * RUNS<T>) void dx_rows_kernel(Head P, Prod G, int block0) {
   __shared__ Runs<T> red;
-  dx_rows_part<DT, T, RUNS<T>>(P, G, blockIdx.x, red);
+  dx_rows_part<DT, T, RUNS<T>>(P, G, block0 + blockIdx.x, red);
 }
 
 // dW of a piece: complete, in the weight's type.  The rollout of the forward tile: 2.95
@@ -1092,14 +1092,20 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
     }
   };
   const int64_t fstep = direct ? P.V : L.piece;
+  const int64_t most = sv_head_host::launch_columns(cdiv(P.N, TS::BM), TS::BN, TS::TPB);
   int tiles = 0;
   for (int64_t v0 = 0; v0 < P.V; v0 += fstep) {
     const int64_t cnt = P.V - v0 < fstep ? P.V - v0 : fstep;
-    Prod G = tiled<TS>(F, P.N, cnt);
-    weight_piece(G, v0, cnt, true);
-    G.tile0 = tiles;
-    hipLaunchKernelGGL((stats_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
-    tiles += G.nt;
+    weight_piece(F, v0, cnt, true);
+    // (logits that are kept are one piece of one launch: their columns count from its first)
+    for (int64_t c = 0; c < cnt; c += most) {
+      Prod G = tiled<TS>(F, P.N, cnt - c < most ? cnt - c : most);
+      G.v0 = v0 + c;
+      G.y += c * G.y_ld;
+      G.tile0 = tiles;
+      hipLaunchKernelGGL((stats_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt)), dim3(TS::TPB), 0, st, P, G);
+      tiles += G.nt;
+    }
   }
   // rows of a normaliser workgroup: a CU has one where that takes fewer than 64 (4096 rows 14.3
   // to 8.9 us, with the distillation's own part 24 to 11.6; 24 rows 9.1 to 6.5)
@@ -1182,8 +1188,13 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
       }
     }
   }
-  if (P.gh && !few)
-    hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)frags), dim3(64 * RUNS<T>), 0, st, P, X);
+  if (P.gh && !few) {
+    constexpr int TPB = 64 * RUNS<T>;
+    constexpr int64_t MOST = sv_head_host::max_groups(TPB);   // (2^20 rows of 4096 in fp32 are more)
+    for (int64_t b = 0; b < frags; b += MOST)
+      hipLaunchKernelGGL((dx_rows_kernel<DT, T>), dim3((unsigned)(frags - b < MOST ? frags - b : MOST)), dim3(TPB), 0, st, P,
+                         X, (int)b);
+  }
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

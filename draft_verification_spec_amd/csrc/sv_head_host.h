@@ -19,6 +19,10 @@ constexpr int64_t PIECE = (int64_t)512 << 20;   // bytes of a piece's dz and wei
 // least steps of a workgroup of the hidden gradient (24 rows of 1024 x 20000 56 us with 8,
 // 54 with 4, whose sums ride with dW; 5 of 72 x 53559 49.0 and 50.4)
 constexpr int RUN = 4;
+// A launch holds fewer than 2^32 work items in a dimension: rows (of at most 256 work
+// items) a launch, and the largest number of workgroups of `threads`.
+constexpr int64_t MAX_ROWS = (int64_t)1 << 23;
+constexpr int64_t max_groups(int threads) { return 0xffffffffLL / threads; }
 constexpr int64_t MAX_LD = (int64_t)1 << 22;   // bytes between rows of a tiled operand: a tile's offsets fit 31 bits
 
 inline int64_t cdiv(int64_t x, int64_t m);
@@ -61,8 +65,8 @@ inline bool logits_shape_ok(const sv_logits_shape_t *s) {
   if ((s->hidden_stride && s->hidden_stride < s->H) || (s->weight_stride && s->weight_stride < s->H) ||
       (s->out_stride && s->out_stride < s->V))
     return false;
-  // a workgroup's index is 31 bits
-  return cdiv(s->N, 16) * cdiv(s->V, 64) < 0x7fffffffLL;
+  // one launch of whichever tiles (more would be logits of 500 GB)
+  return cdiv(s->N, 128) * cdiv(s->V, 128) <= max_groups(256) && cdiv(s->N, 256) * cdiv(s->V, 256) <= max_groups(512);
 }
 
 // Whether weight code rows can be read in 16-byte pieces where they lie.
@@ -196,6 +200,11 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   p.total = o;
   return p;
 }
+
+// Vocabulary entries of one launch of the forward product, whose tiles are mt x (a
+// column of `bn` entries), `threads` each: whole tiles of 256.  (450,000 rows of fp32 x
+// 151936 are 2^32 work items.)
+inline int64_t launch_columns(int64_t mt, int bn, int threads) { return max_groups(threads) / mt * bn / 256 * 256; }
 
 // What a call may need: the copying plan where the weight's address decides.
 inline size_t head_bytes(const sv_head_shape_t *s, bool kd) {

@@ -149,11 +149,18 @@ extern "C" int sv_act8_unpack(int32_t N, int32_t H, const int8_t *codes, int64_t
   const int rc = sv_head_host::check_act8(N, H, y_dtype, y, 0, codes, codes_stride, scale);
   if (rc != SV_OK || N == 0) return rc;
   const int64_t ld = codes_stride ? codes_stride : H;
-  const dim3 grid((unsigned)cdiv(N, 4)), block(256);
-  if (y_dtype == SV_BF16)
-    hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H, N);
-  else
-    hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, (char *)y, H, N);
+  char *o = (char *)y;
+  for (int64_t left = N; left > 0; left -= sv_head_host::MAX_ROWS) {
+    const int n = (int)(left < sv_head_host::MAX_ROWS ? left : sv_head_host::MAX_ROWS);
+    const dim3 grid((unsigned)cdiv(n, 4)), block(256);
+    if (y_dtype == SV_BF16)
+      hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, o, H, n);
+    else
+      hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, codes, ld, scale, o, H, n);
+    codes += n * ld;
+    scale += n;
+    o += (int64_t)n * H * sv_head_host::esize(y_dtype);
+  }
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

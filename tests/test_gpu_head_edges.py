@@ -5,7 +5,8 @@ vocabulary or one gradient.  Tolerances as in test_gpu_head.py.
 """
 import pytest
 
-from test_gpu_head import BF, F, HALF, ce_case, check_ce, check_kd, gen, kd_case, log, plain_pack, sv, within  # noqa: F401
+from test_gpu_head import (BF, F, HALF, ce_case, check_ce, check_gradients, check_kd, gen, kd_case, log,  # noqa: F401
+                           plain_pack, reference, sv, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -15,7 +16,7 @@ torch = pytest.importorskip("torch")
 # ------------------------------------------------------------------ 8-bit rows
 @pytest.mark.parametrize("h", [7, 300, 5000, 20001])
 @pytest.mark.parametrize("dtype", [F, BF])
-def test_act8_smallest_magnitudes(sv, h, dtype):  # noqa: F811
+def test_act8_smallest_magnitudes(sv, h, dtype):
     """Scales that are subnormal, or next to the smallest normal number: the codes of
     the quotient rounded to even as if it were exact, in each of the row kernels."""
     log(f"act8 smallest magnitudes h={h} {dtype}")
@@ -38,7 +39,7 @@ def test_act8_smallest_magnitudes(sv, h, dtype):  # noqa: F811
 
 # --------------------------------------------------------------- cross entropy
 @pytest.mark.parametrize("n,h,v,dtype", [(9, 1001, 130000, F), (24, 1152, 262144, F), (20, 1001, 250000, BF), (9, 1000, 300000, BF)])
-def test_ce_pieces_keep_the_bits(sv, n, h, v, dtype):  # noqa: F811
+def test_ce_pieces_keep_the_bits(sv, n, h, v, dtype):
     """Few rows whose vocabulary is cut otherwise with gradients than without: the
     same bits of the loss and of each gradient whatever is asked for."""
     log(f"head_ce bits over pieces n={n} h={h} v={v} {dtype}")
@@ -56,7 +57,7 @@ def test_ce_pieces_keep_the_bits(sv, n, h, v, dtype):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", [F, BF])
 @pytest.mark.parametrize("n", [4, 40, 300])
-def test_sure_rows(sv, n, dtype):  # noqa: F811
+def test_sure_rows(sv, n, dtype):
     """Rows whose target stands far above the others: nll is what the exponentials'
     rounding leaves of 0, at any size of the logits, and never negative.  Logits are
     exact here (one product each, of powers of two and small numbers).  The largest
@@ -87,3 +88,82 @@ def test_sure_rows(sv, n, dtype):  # noqa: F811
         ids[:, 3] = 7
         k = sv.head_kd(x, w, val, ids, torch.arange(n, device="cuda") % 4, torch.ones(4, device="cuda"), 4)
         within(k.kl, torch.zeros_like(top), bound, "kl")
+
+
+# ------------------------------------- launches of more than 2^32 work items
+def test_act8_rows_beyond_one_launch(sv):
+    """2^24 rows where a workgroup takes a row, 2^26 where it takes four: all rows, by
+    the C entries at an odd distance and by the front end; then into a product."""
+    import ctypes
+    lib = sv.load_library()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    n, h = (1 << 24) + 5, 3
+    log(f"act8 n={n} h={h}")
+    x = torch.randn(n, h, generator=gen(5), device="cuda").to(BF)
+    codes, scale = torch.full((n, h), 99, dtype=torch.int8, device="cuda"), torch.full((n,), -1.0, device="cuda")
+    assert lib.sv_act8_pack(n, h, 1, p(x), 0, p(codes), 0, p(scale), st) == 0
+    c, s = plain_pack(x)
+    assert torch.equal(codes, c) and torch.equal(scale, s)
+    del x, codes, scale, c, s
+    n = (1 << 26) + 7
+    log(f"act8 n={n} h=1")
+    x = torch.randn(n, 1, generator=gen(6), device="cuda").to(BF)
+    a = sv.act8_pack(x)
+    c, s = plain_pack(x)
+    assert torch.equal(a.codes, c) and torch.equal(a.scale, s)
+    y = (c.float() * s[:, None]).to(BF)
+    assert torch.equal(sv.act8_unpack(a), y)
+    log("head_logits of as many rows")
+    w = sv.Act8(torch.full((1, 1), 127, dtype=torch.int8, device="cuda"), torch.full((1,), 2.0 ** -7, device="cuda"))
+    want = (c.double() * 127) * (s.double() * 2.0 ** -7)[:, None]
+    for hidden in (a, x):
+        got = sv.head_logits(hidden, w, out_dtype=F)
+        assert bool(((got.double() - want).abs() <= want.abs() * 2 * HALF[F]).all())
+
+
+@pytest.mark.parametrize("h", [32, 20])
+def test_ce_forward_beyond_one_launch(sv, h):
+    """2^20 rows of 65700 entries in fp32, a head read in place and one that is copied:
+    the tiles of the forward product are more than a launch holds.  64 rows, each
+    many times; targets in the last columns too."""
+    n, v, k = 1 << 20, 65700, 64
+    log(f"head_ce n={n} h={h} v={v}")
+    g = gen(h)
+    base = torch.randn(k, h, generator=g, device="cuda")
+    w = torch.randn(v, h, generator=g, device="cuda") * 3 / h ** 0.5
+    at = torch.cat([torch.arange(32, device="cuda") * 97, v - 1 - torch.arange(32, device="cuda") * 13])
+    z = base.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    nll = lse - z.gather(1, at[:, None])[:, 0]
+    # as in test_gpu_head.py: both logits' sums, and the exponents
+    e = 2 * (h + 8) * 2.0 ** -24 * (base.double().abs() @ w.double().abs().T).amax(1) + 2.0 ** -18 * (1 + lse.abs() / 16) + 2.0 ** -22 * nll
+    r = sv.head_ce(base.repeat(n // k, 1), w, at.repeat(n // k), grad=False)
+    assert not r.status.any()
+    for got, want in ((r.nll, nll), (r.lse, lse)):
+        rows = got.view(-1, k)
+        assert bool((rows == rows[:1]).all())
+        within(rows[0], want, e, "rows")
+    total = r.nll.double().sum()
+    within(r.loss, total[None], total.abs()[None] * 2.0 ** -23, "loss")
+
+
+def test_ce_hidden_gradient_beyond_one_launch(sv):
+    """2^20 rows of 4096 in fp32: the sums of the hidden gradient take more than a launch."""
+    n, h, v, k = 1 << 20, 4096, 60, 64
+    log(f"head_ce grad_hidden n={n} h={h} v={v}")
+    g = gen(3)
+    base = torch.randn(k, h, generator=g, device="cuda")
+    w = torch.randn(v, h, generator=g, device="cuda") * 3 / h ** 0.5
+    at = torch.arange(k, device="cuda") % v
+    x = base.repeat(n // k, 1)
+    r = sv.head_ce(x, w, at.repeat(n // k), grad="hidden")
+    del x
+    assert not r.status.any()
+    rows = r.grad_hidden.view(-1, k, h)
+    for i in range(0, n // k, 2048):                  # each row's sums are its own
+        assert bool((rows[i:i + 2048] == rows[:1]).all()), i
+    pt = torch.nn.functional.one_hot(at, v).double()
+    ones = torch.ones(k, device="cuda").double()
+    ref = reference(base.double(), w.double(), pt, ones, 1.0)
+    check_gradients(r._replace(grad_hidden=rows[0]), ref, base.double(), w.double(), F, ("hidden",))
