@@ -101,6 +101,13 @@ def _on(dev, stream):
     return both, stream
 
 
+def _fits(*sizes):
+    """Sizes that the C structures hold; ctypes would keep the low 32 bits of others."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            _check(-2)                                # SV_ERR_SHAPE
+
+
 def _rows(t, H, what):
     """A tensor [..., H] as rows with unit element stride: (tensor, row stride)."""
     if t.dim() < 1 or t.shape[-1] != H:
@@ -140,6 +147,7 @@ def act8_pack(x, *, stream=None) -> Act8:
     if x.dim() < 1 or not 1 <= x.shape[-1] <= MAX_H:
         raise ValueError(f"rows must be [..., H] with H of 1 .. {MAX_H}")
     lead, H, dev = x.shape[:-1], x.shape[-1], x.device
+    _fits(x.numel() // H)
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "rows")
@@ -165,6 +173,7 @@ def act8_unpack(a: Act8, dtype=None, *, stream=None):
     if codes.dtype != torch.int8 or codes.dim() < 1 or not 1 <= codes.shape[-1] <= MAX_H:
         raise TypeError("codes must be int8 [..., H]")
     H = codes.shape[-1]
+    _fits(codes.numel() // H)
     here, st = _on(dev, stream)
     with here:
         scale = _scales(a.scale, codes.shape[:-1], dev, "scale")
@@ -201,6 +210,7 @@ def head_logits(hidden, weight: Act8, *, out_dtype=None, workspace=None, stream=
     hc = SV_I8 if xs is not None else _code(x.dtype, "hidden rows")
     if weight.codes.device != dev:
         raise ValueError("hidden and weight must be on one device")
+    _fits(V, H, x.numel() // (H or 1))
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "hidden")
@@ -251,6 +261,7 @@ def _loss(fn, result, hidden, weight, grad, temperature, workspace, stream, inpu
     if grads is None:
         raise ValueError('grad must be True, False, "hidden" or "weight"')
     N = x.shape[0]
+    _fits(N, V, H, kw.get("S", 0), kw.get("group", 0))
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "hidden")

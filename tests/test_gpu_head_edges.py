@@ -167,3 +167,31 @@ def test_ce_hidden_gradient_beyond_one_launch(sv):
     ones = torch.ones(k, device="cuda").double()
     ref = reference(base.double(), w.double(), pt, ones, 1.0)
     check_gradients(r._replace(grad_hidden=rows[0]), ref, base.double(), w.double(), F, ("hidden",))
+
+
+def test_sizes_beyond_32_bits_are_refused(sv):
+    """Counts of 2^32 and a few: refused, not taken for the few (broadcast rows, so that
+    they need no memory)."""
+    def many(shape, dtype, value=0):
+        return torch.full((1,) * len(shape), value, dtype=dtype, device="cuda").expand(*shape)
+    n = (1 << 32) + 5
+    codes, scale = many((n, 1), torch.int8), many((n,), F)
+    w = sv.Act8(torch.ones(3, 1, dtype=torch.int8, device="cuda"), torch.ones(3, device="cuda"))
+    x, t = torch.zeros(4, 1, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    log("sizes beyond 32 bits")
+    calls = [lambda: sv.act8_pack(many((n, 1), BF)), lambda: sv.act8_pack(many((1 << 16, 1 << 16, 1), BF)),
+             lambda: sv.act8_unpack(sv.Act8(codes, scale)),
+             lambda: sv.head_logits(sv.Act8(codes, scale), w), lambda: sv.head_logits(many((n, 1), BF), w),
+             lambda: sv.head_logits(x, sv.Act8(codes, scale)),
+             lambda: sv.head_ce(many((n, 1), F), torch.ones(3, 1, device="cuda"), many((n,), torch.int32)),
+             lambda: sv.head_ce(x, many((n, 1), F), t)]
+    val, ids, rs = torch.zeros(4, 32, device="cuda"), torch.arange(32, device="cuda").expand(4, 32), t
+    head, one = torch.zeros(40, 1, device="cuda"), torch.ones(4, device="cuda")
+    calls += [lambda: sv.head_kd(x, head, val, ids, rs, one, (1 << 32) + 4),
+              lambda: sv.head_kd(x, head, val, ids, rs, one, 4 - (1 << 32)),
+              lambda: sv.head_kd(x, head, val, ids, rs, many((1 << 32,), F, 1), 4)]
+    assert sv.head_kd(x, head, val, ids, rs, one, 4).status.tolist() == [0] * 4
+    for i, call in enumerate(calls):
+        with pytest.raises(sv.SpecVerifyError) as e:
+            call()
+        assert e.value.code == sv.SV_ERR_SHAPE, i
