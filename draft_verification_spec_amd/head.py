@@ -227,13 +227,17 @@ def head_logits(hidden, weight: Act8, *, out_dtype=None, workspace=None, stream=
     return out
 
 
-def _int32(t, dev, what, shape):
-    """Integer indices as int32, values outside its range held at its ends."""
+def _int32(t, dev, what, shape, ignore=-1):
+    """Integer indices as int32, values outside its range held at its ends, unless an
+    end is the index to ignore: then they become another that is no entry."""
     import torch
     if t.dtype not in (torch.int32, torch.int64) or tuple(t.shape) != tuple(shape) or t.device != dev:
         raise ValueError(f"{what} must be int32 or int64 {list(shape)} on the rows' device")
     if t.dtype == torch.int64:
-        t = t.clamp(-(1 << 31), (1 << 31) - 1).to(torch.int32)
+        low, high = -(1 << 31), (1 << 31) - 1
+        if ignore in (low, high):
+            t = torch.where((t < low) | (t > high), -1, t)
+        t = t.clamp(low, high).to(torch.int32)
     return t.contiguous()
 
 
@@ -306,7 +310,7 @@ def head_ce(hidden, weight, targets, row_weight=None, *, temperature: float = 1.
         raise ValueError("ignore_index must fit in 32 bits")
 
     def inputs(N, dev):
-        return (_int32(targets, dev, "targets", (N,)),
+        return (_int32(targets, dev, "targets", (N,), int(ignore_index)),
                 None if row_weight is None else _float(row_weight, dev, "row_weight", (N,)))
     return _loss("sv_head_ce", HeadCEResult, hidden, weight, grad, temperature, workspace, stream, inputs,
                  ignore_index=int(ignore_index))

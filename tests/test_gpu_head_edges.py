@@ -195,3 +195,18 @@ def test_sizes_beyond_32_bits_are_refused(sv):
         with pytest.raises(sv.SpecVerifyError) as e:
             call()
         assert e.value.code == sv.SV_ERR_SHAPE, i
+
+
+@pytest.mark.parametrize("ignore", [-(1 << 31), (1 << 31) - 1, -1, 3, -100])
+def test_targets_beyond_32_bits_are_not_ignored(sv, ignore):
+    """64-bit targets outside 32 bits are bad targets, whatever index is ignored; those
+    that are that index are left out."""
+    log(f"targets beyond 32 bits, ignore_index={ignore}")
+    x = torch.randn(9, 64, generator=gen(1), device="cuda")
+    w = torch.randn(50, 64, generator=gen(2), device="cuda")
+    far = [-(1 << 40), 1 << 40, -(1 << 31) - 1, 1 << 31, (1 << 32) + 3, -(1 << 63), (1 << 63) - 1]
+    t = torch.tensor([1, ignore, *far], device="cuda")
+    r = sv.head_ce(x, w, t, ignore_index=ignore)
+    assert r.status.tolist() == [0, 0] + [sv.HEAD_BAD_TARGET] * len(far)
+    assert float(r.nll[0]) > 0 and float(r.nll[1]) == 0 and torch.isnan(r.nll[2:]).all()
+    assert not r.grad_hidden[1:].any()
