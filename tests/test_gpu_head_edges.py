@@ -6,7 +6,7 @@ vocabulary or one gradient.  Tolerances as in test_gpu_head.py.
 import pytest
 
 from test_gpu_head import (BF, F, HALF, ce_case, check_ce, check_gradients, check_kd, gen, kd_case, log,  # noqa: F401
-                           plain_pack, reference, sv, within)
+                           plain_pack, reference, rows_of, sv, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +210,67 @@ def test_targets_beyond_32_bits_are_not_ignored(sv, ignore):
     assert r.status.tolist() == [0, 0] + [sv.HEAD_BAD_TARGET] * len(far)
     assert float(r.nll[0]) > 0 and float(r.nll[1]) == 0 and torch.isnan(r.nll[2:]).all()
     assert not r.grad_hidden[1:].any()
+
+
+# ---------------------------------------------------------------- distillation
+#: rows, width, vocabulary, type, kind of rows, and the pieces of the vocabulary that the
+#: call takes with gradients (test_head_plans.py holds them against the host's plan)
+KD_PIECES = [(2048, 128, 151936, BF, "same", 3, 50688), (1500, 128, 100000, F, "same", 3, 33536),
+             (1100, 64, 151936, BF, "i8", 2, 76032), (1030, 64, 151936, F, "i8", 3, 50688),
+             (20, 1001, 250000, BF, "same", 2, 125184), (9, 1001, 130000, F, "same", 2, 65024)]
+
+
+def kd_piece_case(sv, n, h, v, dtype, kind, piece, seed):
+    """Stored ids on both sides of every piece's border, the last entry and the first."""
+    g = gen(seed)
+    hidden, x = rows_of(kind, n, h, g, dtype, sv)
+    w = (torch.randn(v, h, generator=g, device="cuda") * 3 / h ** 0.5).to(dtype)
+    edge = sorted({0, v - 1} | {b + d for b in range(piece, v, piece) for d in (-1, 0, 1) if b + d < v})
+    ids = torch.empty(n, 32, dtype=torch.int64, device="cuda")
+    ids[:, :len(edge)] = torch.tensor(edge, device="cuda")
+    # the others: steps of 40 from a place of the row's own, none of them an edge
+    start = 4 + torch.randint(0, piece - 2000, (n, 1), generator=g, device="cuda") + torch.arange(n, device="cuda")[:, None] % 2 * piece
+    ids[:, len(edge):] = start.clamp(max=v - 1400) + 40 * torch.arange(32 - len(edge), device="cuda")
+    ids = ids.gather(1, torch.argsort(torch.rand(n, 32, generator=g, device="cuda"), 1))
+    val = 10 + 2 * torch.randn(n, 32, generator=g, device="cuda")
+    val[0, 3] = -float("inf")
+    ids[n // 2, 5] = -1
+    rewards = torch.rand(4 * -(-n // 12), generator=g, device="cuda")
+    rewards[::5] = 0                                  # rows without a gradient, between the others
+    return hidden, x, w, val, ids, torch.arange(n, device="cuda") // 3, rewards, 4
+
+
+@pytest.mark.parametrize("n,h,v,dtype,kind,pieces,piece", KD_PIECES)
+def test_kd_several_pieces(sv, n, h, v, dtype, kind, pieces, piece):
+    """Distillation over several pieces, of more rows than find their own places (and of
+    few): all results, and each gradient alone with the same bits."""
+    log(f"head_kd pieces n={n} h={h} v={v} {dtype} {kind}")
+    case = kd_piece_case(sv, n, h, v, dtype, kind, piece, n)
+    check_kd(sv, *case, dtype, w_max=0.6)
+    same_kd_bits(sv, case, w_max=0.6)
+
+
+def same_kd_bits(sv, case, **kw):
+    hidden, _, w, val, ids, rs, rewards, group = case
+    call = lambda grad: sv.head_kd(hidden, w, val, ids, rs, rewards, group, grad=grad, **kw)  # noqa: E731
+    both = call(True)
+    assert both.grad_hidden.any() and both.grad_weight.any()
+    for grad in (False, "hidden", "weight"):
+        r = call(grad)
+        for name in ("loss", "kl", "weight", "status"):
+            assert torch.equal(getattr(r, name), getattr(both, name)), (grad, name)
+        assert r.grad_hidden is None if grad != "hidden" else torch.equal(r.grad_hidden, both.grad_hidden)
+        assert r.grad_weight is None if grad != "weight" else torch.equal(r.grad_weight, both.grad_weight)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("kind", ["same", "i8"])
+@pytest.mark.parametrize("n,h,v", [(8, 200, 3000), (40, 200, 3000), (64, 72, 501), (150, 130, 2500), (1100, 64, 900),
+                                   (300, 100, 22000)])
+def test_kd_one_gradient_is_the_same(sv, n, h, v, dtype, kind):
+    """The distillation's loss and each gradient alone: the bits of the call for both,
+    which are checked against the formulas."""
+    log(f"head_kd one gradient n={n} h={h} v={v} {dtype} {kind}")
+    case = kd_case(sv, n, h, v, dtype, kind, n + v)
+    check_kd(sv, *case, dtype)
+    same_kd_bits(sv, case)
