@@ -274,3 +274,82 @@ def test_kd_one_gradient_is_the_same(sv, n, h, v, dtype, kind):
     case = kd_case(sv, n, h, v, dtype, kind, n + v)
     check_kd(sv, *case, dtype)
     same_kd_bits(sv, case)
+
+
+# ---------------------------------------------------- how near the gradients are
+def near_case(sv, op, n, h, v, dtype, kind, seed):
+    """Rows near a few entries of the head, as a trained drafter's are: the gradients
+    hang on few entries of dz.  The call, and the exact dz, rows and head."""
+    g = gen(seed)
+    w = (torch.randn(v, h, generator=g, device="cuda") * 3 / h ** 0.5).to(dtype)
+    ids = (torch.randint(0, v, (n, 1), generator=g, device="cuda") + 37 * torch.arange(32, device="cuda")) % v
+    x = torch.randn(n, h, generator=g, device="cuda") + w[ids[:, :4 if op == "kd" else 1]].float().sum(1)
+    if kind == "i8":
+        hidden = sv.act8_pack(x)
+        x = hidden.codes.double() * hidden.scale.double()[:, None]
+    else:
+        hidden = x.to(dtype)
+        x = hidden.double()
+    rows = torch.arange(n, device="cuda")
+    pt = torch.zeros(n, v, dtype=torch.double, device="cuda")
+    if op == "kd":
+        val = 10 + 2 * torch.randn(n, 32, generator=g, device="cuda")
+        rewards = 0.25 + torch.rand(4, generator=g, device="cuda")
+        pt[rows[:, None], ids] = torch.softmax(val.double(), 1)
+        u = (rewards.double() / rewards.double().sum())[rows % 4]
+        call = lambda **kw: sv.head_kd(hidden, w, val, ids, rows % 4, rewards, 4, **kw)  # noqa: E731
+    else:
+        weight = torch.randn(n, generator=g, device="cuda") / n
+        pt[rows, ids[:, 0]] = 1
+        u = weight.double()
+        call = lambda **kw: sv.head_ce(hidden, w, ids[:, 0], weight, **kw)  # noqa: E731
+    return call, reference(x, w.double(), pt, u, 1.0), x, w.double(), u
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+#: a bf16 result's rounding alone: uniform within half a step, 2^-7 / sqrt(12) of the power of two below it, 0.0016 to
+#: 0.0017 of the norm of results whose leading digits are spread; what two terms leave of dz is 2^-17
+ROUNDED = 0.002
+
+
+def check_two_terms(r, ref, x, w):
+    dz, edz = ref["dz"], ref["edz"] + 2.0 ** -16 * ref["dz"].abs() + 1e-40
+    for name, got, a, ea, b in (("hidden", r.grad_hidden, dz, edz, w), ("weight", r.grad_weight, dz.T, edz.T, x)):
+        want = a @ b
+        tol = ea @ b.abs() + (b.shape[0] + 8) * 2.0 ** -24 * (a.abs() @ b.abs())
+        within(got, want, tol + HALF[BF] * (want.abs() + tol) + 1e-38, name)
+        assert off(got, want) <= ROUNDED, name
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("kind", ["same", "i8"])
+@pytest.mark.parametrize("n,h,v", [(24, 1024, 20000), (5, 520, 3001), (32, 200, 70000), (17, 1001, 9000)])
+def test_few_rows_in_two_terms(sv, op, n, h, v, kind):
+    """Up to 32 rows in bf16: the gradients are off by their own rounding, which dz in
+    one term exceeds."""
+    log(f"two terms {op} n={n} h={h} v={v} {kind}")
+    call, ref, x, w, _ = near_case(sv, op, n, h, v, BF, kind, n + h)
+    check_two_terms(call(), ref, x, w)
+    if (n, kind) == (24, "same"):                     # what one term would give
+        want = ref["dz"] @ w
+        assert off((ref["dz"].to(BF).double() @ w).to(BF), want) > ROUNDED
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("kind", ["same", "i8"])
+@pytest.mark.parametrize("n,h,v", [(24, 512, 20000), (9, 1001, 130000), (100, 512, 9000), (300, 256, 60000), (1100, 64, 30000)])
+def test_float32_gradients_are_near(sv, op, n, h, v, kind):
+    """fp32: dz is off by the rounding of its logits (below 32), of their sum and of its
+    scaling, each uniform within half a step of 2^-20: 2^-20 sqrt(2 / 3) of u exp(z - lse)
+    in the mean.  Roundings of different entries are independent, so the gradients' norms
+    are off by no larger a share; 2^-20 leaves the exponentials a part."""
+    log(f"float32 {op} n={n} h={h} v={v} {kind}")
+    call, ref, x, w, u = near_case(sv, op, n, h, v, F, kind, n + h)
+    assert float(ref["z"].abs().max()) < 32
+    r = call()
+    share = float((torch.exp(ref["z"] - ref["lse"][:, None]) * u[:, None]).norm() / ref["dz"].norm())
+    for name, got, want in (("hidden", r.grad_hidden, ref["dz"] @ w), ("weight", r.grad_weight, ref["dz"].T @ x)):
+        assert off(got, want) <= 2.0 ** -20 * max(share, 1.0), (name, off(got, want), share)
