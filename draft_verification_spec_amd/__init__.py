@@ -16,9 +16,9 @@ import re
 from collections import namedtuple
 from typing import Optional
 
-from .head import (Act8, GRAD_HIDDEN, GRAD_WEIGHT, HEAD_BAD_TARGET, HEAD_BAD_WEIGHT, HEAD_EMPTY, HEAD_NAN,  # noqa: F401
-                   HEAD_POSINF, HeadCEResult, HeadKDResult, SV_I8, act8_pack, act8_unpack, bind as _bind_head, head_ce,
-                   head_kd, head_logits, sv_head_shape_t, sv_logits_shape_t)
+from .head import (Act8, GRAD_HIDDEN, GRAD_TWO_TERMS, GRAD_WEIGHT, HEAD_BAD_TARGET, HEAD_BAD_WEIGHT,  # noqa: F401
+                   HEAD_EMPTY, HEAD_NAN, HEAD_POSINF, HeadCEResult, HeadKDResult, SV_I8, act8_pack, act8_unpack,
+                   bind as _bind_head, head_ce, head_kd, head_logits, sv_head_shape_t, sv_logits_shape_t)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspec_verify.so")

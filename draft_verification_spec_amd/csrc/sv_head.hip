@@ -83,6 +83,11 @@ __device__ __forceinline__ void store_columns(char *p, int64_t row, int n, int N
 // whose roundings do not average: 24 rows of 1024 x 20000, distillation, an error of 0.0023
 // to 0.0026 of the norm with one term, 0.0017 with two, which is the results' own
 // rounding; 3 us of 66, and 24 rows of 4096 x 151936 no more at all.
+//
+// At more rows the caller may ask for the second term (SV_GRAD_TWO_TERMS), for a second
+// product of each gradient: its rows lie behind all rows of the first term for dx,
+// which takes them in a product of their own, and behind those with a gradient, in whole
+// steps, for dW, whose sum runs over both and whose rows of x are there twice.
 constexpr int PAIR = 32;
 __device__ __forceinline__ float rest_of(float d) { return d - (float)(__bf16)d; }
 
@@ -97,6 +102,7 @@ struct Head {
   int64_t xw_ld, dzw_ld;                 // bytes between rows of blocks
   int32_t keep;                          // the forward product leaves its logits in dz (fp32, one piece)
   int32_t split;                         // dz in two bf16 terms (PAIR)
+  int32_t terms;                         // 2: dz in two bf16 terms, in rows of their own
   const char *hidden;
   int64_t h_ld;                          // bytes
   const float *h_scale;
@@ -471,8 +477,8 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
   if (threadIdx.x >= 256) return;
   if (block > 0) {
     constexpr int E = Mma<DT>::E, Q = STEP / E, B = 16 / E;
-    const int at = B * (block - 1), M = P.counts[0];
-    if (at >= (M + Q - 1) / Q * Q) return;
+    const int at = B * (block - 1), M = P.counts[0], whole = (M + Q - 1) / Q * Q;
+    if (at >= whole) return;
     bool on[B];
 #pragma unroll
     for (int r = 0; r < B; ++r) on[r] = at + r < M && P.ga[at + r] != 0.f;
@@ -492,6 +498,7 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
         for (int r = 0; r < 4; ++r) v[r] = on[r] ? ((const uint32_t *)(x + r * P.x_ld))[k] : 0u;
       }
       o[k] = v;
+      if (DT == SV_BF16 && P.terms > 1) ((u32x4 *)(P.xw + (at + whole) / B * P.xw_ld))[k] = v;
     }
     return;
   }
@@ -509,10 +516,11 @@ template <int DT> __device__ __forceinline__ void loss_part(const Head &P, int b
 // whole tile, so that both gradients can sum whole steps.  The product again: keeping
 // the logits would be 2.5 GB at 4096 rows, and their reading and writing as long as a
 // third of it.  The rollout of the forward tile: 3.4 ms, with 1.9 GB written for dx, dW.
-template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
+template <int DT, class T, bool TERMS>
+__global__ __launch_bounds__(T::TPB) void dz_kernel(Head P, Prod G) {
   __shared__ __align__(16) char lds[T::LDS];
   constexpr int Q = STEP / Mma<DT>::E;
-  constexpr bool SPLIT = DT == SV_BF16 && T::BM == PAIR;
+  constexpr bool SPLIT = DT == SV_BF16 && T::BM == PAIR, TWO = SPLIT || TERMS;
   const int M = P.counts[0], Mp = SPLIT ? (M ? PAIR : 0) : (M + Q - 1) / Q * Q, mt = (Mp + T::BM - 1) / T::BM;
   if ((int)blockIdx.x >= G.mt * G.nt) {
     loss_part<DT>(P, blockIdx.x - G.mt * G.nt, (double *)lds);
@@ -529,6 +537,8 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
     const Part Y = {G.y + (int64_t)n0 * G.y_ld, G.y_ld, G.N - n0 < T::BN ? G.N - n0 : T::BN, (int64_t)G.nk * STEP};
     product<DT, T>(acc, lds, X, Y, 0, G.nk, first_step<T>(G, in));
   }
+  // rows from a term to the next
+  const int64_t next = SPLIT ? PAIR : P.Np, next_w = SPLIT ? PAIR : Mp;
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
   const Turn turn;
   const Beside beside;
@@ -557,11 +567,11 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
 #pragma unroll
         for (int g = 0; g < T::FN; g += 2)
 #pragma unroll
-          for (int k = 0; k < (SPLIT ? 2 : 1); ++k) {
+          for (int k = 0; k < (TWO ? 2 : 1); ++k) {
             float r[2][4];
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i / 4][i % 4] = k ? rest_of(d[g + i / 4][i % 4]) : d[g + i / 4][i % 4];
-            *(u32x4 *)(P.dz + (m + k * PAIR) * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + beside.at) * 2) =
+            *(u32x4 *)(P.dz + (m + k * next) * P.dz_ld + (int64_t)(n0 + (wn * T::FN + g) * 16 + beside.at) * 2) =
                 Beside::eight(r[0], r[1]);
           }
       } else {
@@ -582,7 +592,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
 #pragma unroll
         for (int g = 0; g < T::FN; g += 2)
 #pragma unroll
-          for (int k = 0; k < (SPLIT ? 2 : 1); ++k) {
+          for (int k = 0; k < (TWO ? 2 : 1); ++k) {
             float r[2][4];
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i / 4][i % 4] = k ? rest_of(d[g + i / 4][i % 4]) : d[g + i / 4][i % 4];
@@ -597,7 +607,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dz_kernel(H
 #pragma unroll
         for (int g = 0; g < T::FN; g += DT == SV_BF16 ? 2 : 1) {
           *(u32x4 *)(at + g * 256) = o[g];
-          if constexpr (SPLIT) *(u32x4 *)(at + PAIR / 8 * P.dzw_ld + g * 256) = o[g + 1];
+          if constexpr (TWO) *(u32x4 *)(at + next_w / 8 * P.dzw_ld + g * 256) = o[g + 1];
         }
       }
     }
@@ -668,9 +678,10 @@ template <int DT> __global__ __launch_bounds__(256) void fix_kernel(Head P, Prod
     const float d = fmaf(__builtin_amdgcn_exp2f(fmaf(P.zt[i], LOG2E, -P.lse2[at])), ga, -u);
     if (P.gh) store_real<DT>(z, c, d);
     if (P.gw) store_real<DT>(zw, c * B + at % B, d * s);
-    if (P.split) {
-      if (P.gh) store_real<DT>(z + PAIR * P.dz_ld, c, rest_of(d));
-      if (P.gw) store_real<DT>(zw + PAIR / B * P.dzw_ld, c * B + at % B, rest_of(d * s));
+    if (P.split || P.terms > 1) {
+      const int64_t next = P.split ? PAIR : P.Np, next_w = P.split ? PAIR : (P.counts[0] + 63) / 64 * 64;
+      if (P.gh) store_real<DT>(z + next * P.dz_ld, c, rest_of(d));
+      if (P.gw) store_real<DT>(zw + next_w / B * P.dzw_ld, c * B + at % B, rest_of(d * s));
     }
   }
 }
@@ -829,7 +840,7 @@ template <int DT, class T> __global__ __launch_bounds__(T::TPB) void dw_kernel(H
   typename Mma<DT>::Acc acc[T::FM][T::FN];
   clear<DT, T>(acc);
   constexpr int Q = STEP / Mma<DT>::E;
-  const int nk = (P.counts[0] + Q - 1) / Q;
+  const int nk = (P.counts[0] + Q - 1) / Q * P.terms;
   const Part X = {G.x + (int64_t)m0 * 16, G.x_ld, (int64_t)nk * (STEP / 16), G.x_ld - (int64_t)m0 * 16};
   const Part Y = {G.y + (int64_t)n0 * 16, G.y_ld, (int64_t)nk * (STEP / 16), G.y_ld - (int64_t)n0 * 16};
   product<DT, T, BLOCKS, BLOCKS>(acc, lds, X, Y, 0, nk);
@@ -1120,7 +1131,6 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
   }
 
   Prod X = tiled<T>(Prod{}, BOTH<DT, T> ? 2 * PAIR : P.N, P.H);
-  X.x = P.dz;
   X.x_ld = L.dz_ld;
   X.chunks = L.chunks;
   X.full = L.full;
@@ -1128,7 +1138,7 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
   X.slots = L.slots;
   X.per0 = sv_head_host::RUN;
   constexpr bool FEW = T::BM == 32 || (DT == SV_BF16 && T::BM < 256);    // tiles that rows of one step take
-  const bool few = FEW && P.gw && L.Np * E == STEP;
+  const bool few = FEW && P.gw && L.Np * E == STEP && P.terms == 1;
   const int64_t frags = (int64_t)X.mt * X.nt * T::NW * TERM<DT, T>;      // fragment rows of dx's tiles
   for (int64_t v0 = 0; v0 < P.V; v0 += L.piece) {
     const int64_t cnt = P.V - v0 < L.piece ? P.V - v0 : L.piece;
@@ -1142,7 +1152,16 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
       G.mt = (int32_t)(L.Np / 4);
       hipLaunchKernelGGL(dz_kept_kernel, dim3((unsigned)(G.mt + loss), (unsigned)cdiv(cp, 1024)), b256, 0, st, P, G);
     } else {
-      hipLaunchKernelGGL((dz_kernel<DT, TS>), dim3((unsigned)(G.mt * G.nt + loss)), dim3(TS::TPB), 0, st, P, G);
+      auto dz = [&](auto terms) {
+        constexpr bool TERMS = decltype(terms)::value;
+        hipLaunchKernelGGL((dz_kernel<DT, TS, TERMS>), dim3((unsigned)(G.mt * G.nt + loss)), dim3(TS::TPB), 0, st, P, G);
+      };
+      if constexpr (DT == SV_BF16 && TS::BM > PAIR) {
+        if (P.terms > 1) dz(std::true_type());
+        else dz(std::false_type());
+      } else {
+        dz(std::false_type());
+      }
     }
     if (kd) hipLaunchKernelGGL((fix_kernel<DT>), dim3((unsigned)cdiv((int64_t)P.N * TOP, 256)), b256, 0, st, P, G);
     if (P.gh) {
@@ -1150,8 +1169,11 @@ template <int DT, class T, class TS = T> int enqueue(const Head &P, const Plan &
       X.y_ld = G.y_ld;
       X.M = (int32_t)cnt;
       X.nk = (int32_t)cdiv(cnt * E, STEP);
-      X.first = v0 == 0;
-      hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)L.groups), dim3(T::TPB), 0, st, P, X);
+      for (int k = 0; k < P.terms; ++k) {
+        X.x = P.dz + k * L.Np * L.dz_ld;
+        X.first = v0 == 0 && k == 0;
+        hipLaunchKernelGGL((dx_kernel<DT, T>), dim3((unsigned)L.groups), dim3(T::TPB), 0, st, P, X);
+      }
     }
     if (P.gw) {
       Prod W = {};
@@ -1208,7 +1230,7 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.H = s.H;
   P.V = s.V;
   P.T = kd ? TOP : 1;
-  P.grads = s.grads;
+  P.grads = s.grads & (SV_GRAD_HIDDEN | SV_GRAD_WEIGHT);
   P.ignore = s.ignore_index;
   P.inv_t = 1.f / s.temperature;
   P.Kp = L.Kp;
@@ -1216,6 +1238,7 @@ int run(const sv_head_shape_t &s, bool kd, Head P, const void *hidden, const flo
   P.dz_ld = L.dz_ld;
   P.keep = L.keep;
   P.split = s.dtype == SV_BF16 && L.bm == PAIR;
+  P.terms = L.terms;
   P.Np = L.Np;
   P.hidden = (const char *)hidden;
   P.h_ld = (s.hidden_stride ? s.hidden_stride : s.H) * (int64_t)he;

@@ -108,6 +108,7 @@ struct Plan {
   int64_t xw_ld, dzw_ld;                 // the same for dW's operands, rows of 16-byte blocks
   int bm, bn;                            // tile of the products
   bool keep;                             // the forward product's logits stay in dz (fp32, one piece)
+  int terms;                             // bf16 terms of dz in rows of their own (beyond bm = 32, whose tiles hold two)
   bool narrow;                           // tiles of 64 columns against the weight's rows
   // the hidden gradient: chunks of a piece, steps of one; workgroups, tiles each may touch
   int chunks, full, groups, slots;
@@ -119,7 +120,7 @@ inline bool head_shape_ok(const sv_head_shape_t *s, bool kd) {
   if (s->N < 0 || s->N > SV_HEAD_MAX_N || s->H < 1 || s->H > SV_HEAD_MAX_H || s->V < 1 || s->V > SV_HEAD_MAX_V)
     return false;
   if (!real_dtype(s->dtype) || (s->hidden_dtype != s->dtype && s->hidden_dtype != SV_I8)) return false;
-  if (s->grads & ~(SV_GRAD_HIDDEN | SV_GRAD_WEIGHT)) return false;
+  if (s->grads & ~(SV_GRAD_HIDDEN | SV_GRAD_WEIGHT | SV_GRAD_TWO_TERMS) || s->grads == SV_GRAD_TWO_TERMS) return false;
   if ((s->hidden_stride && s->hidden_stride < s->H) || (s->weight_stride && s->weight_stride < s->H)) return false;
   if (kd) {
     if (s->temperature != 1.f) return false;
@@ -150,7 +151,8 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   // 4096 x 151936 in bf16, with the weight counted too: 13.2 ms with 256 MB, 12.8 with
   // 640, 12.6 with 1280, for fewer passes over the sums of dx and fewer last rounds of
   // tiles), but the logits in fp32 would be 2.5 GB.
-  int64_t per = (s->grads ? 2 * p.Np * e : 0) + (direct ? 0 : p.Kp * e);
+  p.terms = (s->grads & SV_GRAD_TWO_TERMS) && s->dtype == SV_BF16 && p.bm > 32 ? 2 : 1;
+  int64_t per = (s->grads ? 2 * p.terms * p.Np * e : 0) + (direct ? 0 : p.Kp * e);
   if (per < 16) per = 16;
   int64_t most = PIECE / per / 256 * 256;
   if (most < 256) most = 256;
@@ -192,9 +194,9 @@ inline Plan plan_for(const sv_head_shape_t *s, bool kd, bool direct) {
   p.xs = take((size_t)p.Np * p.x_ld);
   p.xw_ld = spread(p.Kp * 16);
   p.dzw_ld = spread(p.piece * 16);
-  p.xw = take(gw ? (size_t)(p.Np * e / 16) * p.xw_ld : 0);
-  p.dz = take(gh || p.keep ? (size_t)p.Np * p.dz_ld : 0);
-  p.dzw = take(gw ? (size_t)(p.Np * e / 16) * p.dzw_ld : 0);
+  p.xw = take(gw ? (size_t)(p.terms * p.Np * e / 16) * p.xw_ld : 0);
+  p.dz = take(gh || p.keep ? (size_t)(p.terms * p.Np) * p.dz_ld : 0);
+  p.dzw = take(gw ? (size_t)(p.terms * p.Np * e / 16) * p.dzw_ld : 0);
   p.wt = take(direct ? 0 : (size_t)p.piece * p.x_ld);
   p.acc = take(gh ? (size_t)p.groups * p.slots * p.bm * p.bn * 4 : 0);
   p.total = o;

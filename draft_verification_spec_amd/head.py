@@ -14,7 +14,7 @@ import ctypes
 from collections import namedtuple
 
 SV_I8 = 2
-GRAD_HIDDEN, GRAD_WEIGHT = 1, 2
+GRAD_HIDDEN, GRAD_WEIGHT, GRAD_TWO_TERMS = 1, 2, 4
 HEAD_BAD_TARGET, HEAD_NAN, HEAD_POSINF, HEAD_EMPTY, HEAD_BAD_WEIGHT = 1, 2, 4, 8, 16
 MAX_H, MAX_N, MAX_V = 131072, 1048576, 16777216
 
@@ -248,7 +248,7 @@ def _float(t, dev, what, shape):
     return t.to(dtype=torch.float32).contiguous()
 
 
-def _loss(fn, result, hidden, weight, grad, temperature, workspace, stream, inputs, **kw):
+def _loss(fn, result, hidden, weight, grad, two_terms, temperature, workspace, stream, inputs, **kw):
     import torch
     if weight.dim() != 2:
         raise ValueError("weight must be [V, H]")
@@ -264,6 +264,8 @@ def _loss(fn, result, hidden, weight, grad, temperature, workspace, stream, inpu
     grads = {True: GRAD_HIDDEN | GRAD_WEIGHT, False: 0, "hidden": GRAD_HIDDEN, "weight": GRAD_WEIGHT}.get(grad)
     if grads is None:
         raise ValueError('grad must be True, False, "hidden" or "weight"')
+    if grads and two_terms:
+        grads |= GRAD_TWO_TERMS
     N = x.shape[0]
     _fits(N, V, H, kw.get("S", 0), kw.get("group", 0))
     here, st = _on(dev, stream)
@@ -292,7 +294,7 @@ def _loss(fn, result, hidden, weight, grad, temperature, workspace, stream, inpu
 
 
 def head_ce(hidden, weight, targets, row_weight=None, *, temperature: float = 1.0, ignore_index: int = -1,
-            grad=True, workspace=None, stream=None) -> HeadCEResult:
+            grad=True, two_terms: bool = False, workspace=None, stream=None) -> HeadCEResult:
     """Softmax cross entropy of hidden rows under a vocabulary head, from pieces
     of the vocabulary: no logits are kept.
 
@@ -305,26 +307,31 @@ def head_ce(hidden, weight, targets, row_weight=None, *, temperature: float = 1.
     grad: True for the gradients of hidden rows and weight, "hidden" or "weight"
     for one of them, False for none.  Returns loss [1] float32 = sum of row_weight
     * nll, nll and lse [N] float32, status [N] (HEAD_* bits; such a row has NaN
-    results and adds nothing), and the gradients in the weight's dtype."""
+    results and adds nothing), and the gradients in the weight's dtype.
+
+    two_terms: for bfloat16 the logits' gradient, an operand of both gradients'
+    products, in two bfloat16 terms instead of one: the gradients are then off by
+    their own rounding alone (0.0017 of the norm, else up to 0.0028), for a second
+    product of each.  Up to 32 rows, and in float32, that is so anyway."""
     if not -(1 << 31) <= int(ignore_index) < (1 << 31):
         raise ValueError("ignore_index must fit in 32 bits")
 
     def inputs(N, dev):
         return (_int32(targets, dev, "targets", (N,), int(ignore_index)),
                 None if row_weight is None else _float(row_weight, dev, "row_weight", (N,)))
-    return _loss("sv_head_ce", HeadCEResult, hidden, weight, grad, temperature, workspace, stream, inputs,
+    return _loss("sv_head_ce", HeadCEResult, hidden, weight, grad, two_terms, temperature, workspace, stream, inputs,
                  ignore_index=int(ignore_index))
 
 
 def head_kd(hidden, weight, topk_val, topk_idx, row_sample, rewards, group: int, *, w_max: float = float("inf"),
-            grad=True, workspace=None, stream=None) -> HeadKDResult:
+            grad=True, two_terms: bool = False, workspace=None, stream=None) -> HeadKDResult:
     """kd's reward-weighted distillation loss over the stored top-32, from hidden
     rows and head instead of drafter logits: no logits are kept.  hidden, weight,
-    grad as in head_ce; topk_val, topk_idx [N, 32], row_sample [N], rewards [S],
+    grad, two_terms as in head_ce; topk_val, topk_idx [N, 32], row_sample [N], rewards [S],
     group and w_max as in kd.  Returns loss [1] float32, kl and weight [N] float32,
     status [N] (KD_* bits) and the gradients in the weight's dtype."""
     def inputs(N, dev):
         return (_float(topk_val, dev, "topk_val", (N, 32)), _int32(topk_idx, dev, "topk_idx", (N, 32)),
                 _int32(row_sample, dev, "row_sample", (N,)), _float(rewards, dev, "rewards", (rewards.numel(),)))
-    return _loss("sv_head_kd", HeadKDResult, hidden, weight, grad, 1.0, workspace, stream, inputs,
+    return _loss("sv_head_kd", HeadKDResult, hidden, weight, grad, two_terms, 1.0, workspace, stream, inputs,
                  S=rewards.numel(), group=int(group), w_max=float(w_max))

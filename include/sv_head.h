@@ -104,12 +104,16 @@ int sv_head_logits(const sv_logits_shape_t *shape, const void *hidden, const flo
  *   the stored 32, u_n = the clipped group-normalised reward.
  * Gradients of both: dx[n,k] = (1/T) sum_v dz[n,v] w[v,k],
  *                    dw[v,k] = (1/T) sum_n dz[n,v] x[n,k].
- * Products of bf16 operands are summed in fp32; for them dz is rounded to bf16
- * (it is an operand of the gradients' products; up to 32 rows in two bf16 terms),
- * everything else is fp32 or fp64.
+ * Products of bf16 operands are summed in fp32; for them dz is rounded to bf16, as
+ * it is an operand of the gradients' products (their error: 0.0020 to 0.0028 of the
+ * norm, where the rounding of the results alone is 0.0015 to 0.0017).  Up to 32
+ * rows, and with SV_GRAD_TWO_TERMS at any number, it is the sum of two bf16 numbers
+ * (0.0015 to 0.0017; a second product of each gradient beyond 32 rows).  Everything
+ * else is fp32 or fp64.
  */
 #define SV_GRAD_HIDDEN 1
 #define SV_GRAD_WEIGHT 2
+#define SV_GRAD_TWO_TERMS 4   /* with one of the others; changes nothing for fp32 */
 
 /* status bits of sv_head_ce, per row (sv_head_kd: the SV_KD_* bits of sv_kd.h) */
 #define SV_HEAD_BAD_TARGET 1   /* the target is neither ignore_index nor in [0, V) */

@@ -353,3 +353,87 @@ def test_float32_gradients_are_near(sv, op, n, h, v, kind):
     share = float((torch.exp(ref["z"] - ref["lse"][:, None]) * u[:, None]).norm() / ref["dz"].norm())
     for name, got, want in (("hidden", r.grad_hidden, ref["dz"] @ w), ("weight", r.grad_weight, ref["dz"].T @ x)):
         assert off(got, want) <= 2.0 ** -20 * max(share, 1.0), (name, off(got, want), share)
+
+
+#: more than 32 rows: one step of rows, ragged ones, each tile, dW's tiles, several pieces
+TWO_TERMS = [(33, 72, 501), (40, 1024, 20000), (64, 256, 3001), (65, 100, 1000), (150, 520, 9001), (300, 192, 21900),
+             (1100, 64, 7300), (2048, 128, 151936), (50, 1001, 240000)]
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("kind", ["same", "i8"])
+@pytest.mark.parametrize("n,h,v", TWO_TERMS)
+def test_two_terms(sv, op, n, h, v, kind):
+    """dz in two terms at more rows: the gradients are off by their own rounding, the
+    rest is the call's without; each gradient alone has the same bits."""
+    log(f"two terms asked for {op} n={n} h={h} v={v} {kind}")
+    call, ref, x, w, _ = near_case(sv, op, n, h, v, BF, kind, n + h)
+    one, r = call(), call(two_terms=True)
+    check_two_terms(r, ref, x, w)
+    for name in r._fields[:4]:
+        assert torch.equal(getattr(r, name), getattr(one, name)), name
+    assert torch.equal(call(two_terms=True, grad="hidden").grad_hidden, r.grad_hidden)
+    assert torch.equal(call(two_terms=True, grad="weight").grad_weight, r.grad_weight)
+    assert torch.equal(call(two_terms=True, grad=False)[0], r[0])
+
+
+@pytest.mark.parametrize("n", [150, 300, 1100])
+def test_two_terms_with_rows_left_out(sv, n):
+    """A front part of the rows that ends anywhere in a tile, and rows with data errors."""
+    hidden, x, w, t, u = ce_case(sv, n, 136, 9001, BF, "same", 1.0, n)
+    t[n // 7::3] = -1
+    t[n // 3::2] = -1
+    hidden[5, 3], t[5] = float("nan"), 4
+    r = sv.head_ce(hidden, w, t, u, two_terms=True)
+    assert int(r.status[5]) == sv.HEAD_NAN and int((r.status != 0).sum()) == 1
+    used = (t >= 0) & (r.status == 0)
+    ud = torch.where(used, u.double(), torch.zeros_like(u).double())
+    x = torch.where(used[:, None], x, torch.zeros_like(x))
+    pt = torch.zeros(n, 9001, dtype=torch.double, device="cuda")
+    pt[used, t[used]] = 1
+    check_two_terms(r, reference(x, w.double(), pt, ud, 1.0), x, w.double())
+    assert not r.grad_hidden[~used].any()
+
+
+@pytest.mark.parametrize("dtype,n", [(F, 100), (F, 20), (BF, 20)])
+def test_two_terms_where_they_are_so_anyway(sv, dtype, n):
+    """fp32, and up to 32 rows: the same bits with and without."""
+    hidden, _, w, t, u = ce_case(sv, n, 128, 900, dtype, "same", 1.0, n)
+    assert all(torch.equal(a, b) for a, b in zip(sv.head_ce(hidden, w, t, u), sv.head_ce(hidden, w, t, u, two_terms=True)))
+
+
+def test_two_terms_guards_and_replays(sv):
+    """A workspace of exactly the stated size, nothing behind it or the gradients
+    written; a captured call replayed on other inputs."""
+    import ctypes
+    lib = sv.load_library()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for n, h, v in ((40, 100, 900), (300, 500, 70000)):
+        log(f"two terms, guards n={n} h={h} v={v}")
+        hidden, _, w, t, u = ce_case(sv, n, h, v, BF, "same", 1.0, n)
+        want = sv.head_ce(hidden, w, t, u, two_terms=True)
+        t = t.int()
+        shape = sv.sv_head_shape_t(n, h, v, 1, 1, 7, 0, 0, 1.0, -1, 0, 0, float("inf"))
+        need = lib.sv_head_ce_workspace_bytes(ctypes.byref(shape))
+        ws = torch.full((need + 65536,), 0xff, dtype=torch.uint8, device="cuda")
+        res, loss = torch.empty(n, device="cuda"), torch.empty(1, device="cuda")
+        gh, gw = (torch.full((k * h + 16,), 5.0, dtype=BF, device="cuda") for k in (n, v))
+        assert lib.sv_head_ce(ctypes.byref(shape), p(hidden), None, p(w), p(t), p(u), p(res), None, None, p(loss), p(gh), p(gw),
+                              p(ws), need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+        assert torch.equal(gh[:n * h].view(n, h), want.grad_hidden) and torch.equal(gw[:v * h].view(v, h), want.grad_weight)
+        assert (gh[n * h:] == 5).all() and (gw[v * h:] == 5).all() and (ws[need:] == 0xff).all()
+    held = ce_case(sv, 150, 128, 3000, BF, "same", 1.0, 1)
+    call = lambda c: list(sv.head_ce(c[0], c[2], c[3], c[4], two_terms=True))  # noqa: E731
+    call(held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(held)
+    for seed in (2, 3, 4):
+        new = ce_case(sv, 150, 128, 3000, BF, "same", 1.0, seed)
+        for a, b in zip(held, new):
+            a.copy_(b)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, call(new))), seed

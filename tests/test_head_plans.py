@@ -96,6 +96,8 @@ static int holds(const sv_head_shape_t &s, bool kd, bool direct) {
     NEED(cdiv(M, T.bm) * nt * T.frags < 0x7fffffffLL);
   }
   // sections
+  const int terms = (s.grads & SV_GRAD_TWO_TERMS) && bf && p.bm > 32 ? 2 : 1;
+  NEED(p.terms == terms);
   int64_t columns = 0;
   const int64_t part = direct ? s.V : p.piece, most = launch_columns(cdiv(s.N, S.bm), S.bn, S.threads);
   NEED(most >= 256 && most % 256 == 0);
@@ -108,8 +110,8 @@ static int holds(const sv_head_shape_t &s, bool kd, bool direct) {
     }
   NEED((int64_t)(p.xs - p.part) >= columns * s.N * 8);
   NEED((int64_t)(p.xw - p.xs) >= p.Np * p.x_ld);
-  if (gw) NEED((int64_t)(p.dz - p.xw) >= p.Np * e / 16 * p.xw_ld && (int64_t)(p.wt - p.dzw) >= p.Np * e / 16 * p.dzw_ld);
-  if (gh || p.keep) NEED((int64_t)(p.dzw - p.dz) >= p.Np * p.dz_ld);
+  if (gw) NEED((int64_t)(p.dz - p.xw) >= terms * p.Np * e / 16 * p.xw_ld && (int64_t)(p.wt - p.dzw) >= terms * p.Np * e / 16 * p.dzw_ld);
+  if (gh || p.keep) NEED((int64_t)(p.dzw - p.dz) >= terms * p.Np * p.dz_ld);
   if (!direct) NEED((int64_t)(p.acc - p.wt) >= p.piece * p.x_ld);
   if (gh) NEED((int64_t)(p.total - p.acc) >= (int64_t)p.groups * p.slots * T.bm * T.bn / (both ? 2 : 1) * 4);
   // launches over a piece
@@ -124,8 +126,9 @@ int main() {
   const int Ns[] = {1, 5, 24, 32, 33, 64, 65, 100, 128, 129, 191, 250, 256, 257, 520, 750, 1000, 1025, 2772, 4096, 20000, 1 << 20};
   const int Hs[] = {1, 7, 64, 72, 100, 192, 512, 1001, 1024, 2048, 4096, 8192, 131072};
   const int Vs[] = {1, 40, 255, 257, 1000, 4343, 20000, 32768, 33000, 65535, 65536, 100000, 151936, 262144, 600000, 1 << 24};
+  const int Gs[] = {0, 1, 2, 3, 5, 7};
   long long plans = 0;
-  for (int N : Ns) for (int H : Hs) for (int V : Vs) for (int dt = 0; dt < 2; ++dt) for (int g = 0; g < 4; ++g)
+  for (int N : Ns) for (int H : Hs) for (int V : Vs) for (int dt = 0; dt < 2; ++dt) for (int g : Gs)
     for (int kd = 0; kd < 2; ++kd) {
       if ((double)N * H * V > 4e15 && (g == 1 || kd)) continue;
       sv_head_shape_t s = {N, H, V, dt, dt, g, 0, 0, 1.f, -1, 4, 2, 1.f};
