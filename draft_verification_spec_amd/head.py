@@ -101,11 +101,11 @@ def _on(dev, stream):
     return both, stream
 
 
-def _fits(*sizes):
-    """Sizes that the C structures hold; ctypes would keep the low 32 bits of others."""
-    for n in sizes:
-        if not -(1 << 31) <= n < 1 << 31:
-            _check(-2)                                # SV_ERR_SHAPE
+def _fits(size):
+    """A size (or several joined by |, none negative) that the C structures hold; ctypes
+    would keep the low 32 bits of another."""
+    if not -0x80000000 <= size < 0x80000000:
+        _check(-2)                                    # SV_ERR_SHAPE
 
 
 def _rows(t, H, what):
@@ -210,7 +210,7 @@ def head_logits(hidden, weight: Act8, *, out_dtype=None, workspace=None, stream=
     hc = SV_I8 if xs is not None else _code(x.dtype, "hidden rows")
     if weight.codes.device != dev:
         raise ValueError("hidden and weight must be on one device")
-    _fits(V, H, x.numel() // (H or 1))
+    _fits(V | H | x.numel() // (H or 1))
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "hidden")
@@ -267,7 +267,8 @@ def _loss(fn, result, hidden, weight, grad, two_terms, temperature, workspace, s
     if grads and two_terms:
         grads |= GRAD_TWO_TERMS
     N = x.shape[0]
-    _fits(N, V, H, kw.get("S", 0), kw.get("group", 0))
+    _fits(N | V | H | kw.get("S", 0))
+    _fits(kw.get("group", 0))
     here, st = _on(dev, stream)
     with here:
         r, ld = _rows(x, H, "hidden")
