@@ -69,8 +69,8 @@ struct LogitsP {
   int N, V, mt, nt, nk, band;
 };
 
-// One tile of logits.  The int32 sums are exact; the two scales are joined first
-// and the product with them rounds once (twice with a bf16 output).  1024 rows of 4096 x
+// One tile of logits.  The int32 sums are exact; three fp32 roundings follow, of the sum
+// (beyond 2^24), of the two scales' product and of the product of both, and the output's.  1024 rows of 4096 x
 // 128256 456 us, 2.36 POP/s (matrix instructions); 32 rows of 4096 x 151936 114 us, 5.5
 // TB/s, and one of 1024 x 32000 6.4 us, 5.1 TB/s (reading the head).
 template <class T, int OT> __global__ __launch_bounds__(T::TPB) void logits_kernel(LogitsP P) {

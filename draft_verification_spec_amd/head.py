@@ -141,7 +141,8 @@ def act8_pack(x, *, stream=None) -> Act8:
     """Rows [..., H] (float32 or bfloat16) in 8 bits: scale = max|x| / 127 of the
     row, codes = x / scale rounded to even.  A row of zeros has scale 0, a row
     with a NaN or an infinity scale NaN.  The rows of codes lie 128 bytes apart
-    or a multiple, so that head_logits reads them in place."""
+    or a multiple, so that head_logits reads a head in place (hidden rows it copies,
+    as it does those that it packs itself)."""
     import torch
     dt = _code(x.dtype, "rows")
     if x.dim() < 1 or not 1 <= x.shape[-1] <= MAX_H:

@@ -53,7 +53,7 @@ extern "C" {
 /* ---------------------------------------------------------------- 8-bit rows
  *   scale[n] = fl(max_k |x[n,k]| / 127)
  *   codes[n,k] = clamp(round_to_even(x[n,k] / scale[n]), -127, 127), exactly
- *                rounded; 0 where scale[n] is 0
+ *                rounded also where scale[n] is subnormal; 0 where it is 0
  *   unpacked y[n,k] = codes[n,k] * scale[n]
  * A row holding a NaN or an infinity gets scale NaN and codes 0 (unpacked: NaN).
  * x [N, H] (SV_F32 or SV_BF16) with row stride x_stride elements, codes [N, H]
@@ -68,8 +68,8 @@ int sv_act8_unpack(int32_t N, int32_t H, const int8_t *codes, int64_t codes_stri
 
 /* ------------------------------------------------------------ 8-bit head logits
  *   logits[n,v] = scale_x[n] * scale_w[v] * sum_k cx[n,k] cw[v,k]
- * The sum is exact (int32); its product with the scales is rounded once more, and
- * to bf16 where the logits are bf16.  cx is either given (hidden_dtype SV_I8,
+ * The sum is exact (int32).  It, the product of the two scales and the product of
+ * both are each rounded to fp32 once, the last to bf16 as well where the logits are bf16.  cx is either given (hidden_dtype SV_I8,
  * with hidden_scale) or formed from fp32 or bf16 rows as sv_act8_pack does.
  */
 typedef struct {
