@@ -1,0 +1,88 @@
+// sv_logprobs_host.h -- host-side argument checks and plans of the log-probability
+// operators, in plain C++ with no HIP (a CPU build with sanitizers drives it over valid
+// and invalid shapes).
+#pragma once
+
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+#include "sv_head_host.h"
+#include "sv_logprobs.h"
+
+namespace sv_logprobs_host {
+
+using sv_head_host::cdiv;
+using sv_head_host::esize;
+using sv_head_host::real_dtype;
+
+constexpr int VECS = 4;                  // 16-byte vectors of a thread at a time
+constexpr int LIST = 32;                 // alternatives that a list holds
+constexpr int64_t MAX_GROUPS = sv_head_host::max_groups(1024);
+
+// A row's share of the launch: waves of a workgroup, workgroups of a row.
+struct Plan {
+  int waves, parts;
+  int64_t batch, batches;                // entries of a workgroup's step, steps of a row
+  size_t stats, keys, total;             // workspace sections (parts > 1)
+};
+
+inline Plan plan_for(const sv_logprobs_shape_t *s) {
+  Plan p;
+  const int64_t w = 16 / esize(s->dtype);
+  p.waves = s->N >= 1024 ? 4 : 16;
+  p.batch = (int64_t)p.waves * 64 * VECS * w;
+  p.batches = cdiv(s->V, p.batch);
+  p.parts = 1;
+  if (s->N < 128 && p.batches > 4) {
+    const int64_t most = cdiv(256, s->N < 1 ? 1 : s->N), by = cdiv(p.batches, 2);
+    p.parts = (int)(most < by ? most : by);
+    if (p.parts > 64) p.parts = 64;
+  }
+  const size_t n = p.parts > 1 ? (size_t)s->N * p.parts : 0;
+  p.stats = 0;
+  p.keys = (n * 24 + 255) & ~(size_t)255;
+  p.total = p.keys + (s->top ? n * LIST * 8 : 0);
+  return p;
+}
+
+inline bool temperature_ok(float t) { return t > 0.f && t < INFINITY && 1.44269504f / t < INFINITY; }
+
+inline bool shape_ok(const sv_logprobs_shape_t *s) {
+  return s->N >= 0 && s->N <= SV_HEAD_MAX_N && s->V >= 1 && s->V <= SV_HEAD_MAX_V && real_dtype(s->dtype) &&
+         s->top >= 0 && s->top <= SV_LOGPROBS_MAX_TOP && (!s->row_stride || s->row_stride >= s->V);
+}
+
+inline int check(const sv_logprobs_shape_t *s, const void *logits, const void *tokens, const void *logp,
+                 const void *top_logp, const void *top_idx, const void *ws, size_t wsb, bool *nothing) {
+  *nothing = false;
+  if (!s) return SV_ERR_NULL;
+  if (!real_dtype(s->dtype)) return SV_ERR_DTYPE;
+  if (!temperature_ok(s->temperature)) return SV_ERR_TEMPERATURE;
+  if (!shape_ok(s)) return SV_ERR_SHAPE;
+  if (s->N == 0) { *nothing = true; return SV_OK; }
+  if (!logits || !tokens || !logp || (s->top && (!top_logp || !top_idx))) return SV_ERR_NULL;
+  const size_t need = plan_for(s).total;
+  if (need && (!ws || wsb < need || ((uintptr_t)ws & 255))) return SV_ERR_WORKSPACE;
+  return SV_OK;
+}
+
+inline int check_grad(const sv_logprobs_grad_shape_t *s, const void *logits, const void *tokens, const void *norm,
+                      const void *entropy, const void *grad_logp, const void *grad_entropy, const void *grad,
+                      bool *nothing) {
+  *nothing = false;
+  if (!s) return SV_ERR_NULL;
+  if (!real_dtype(s->dtype) || !real_dtype(s->grad_dtype)) return SV_ERR_DTYPE;
+  if (!temperature_ok(s->temperature)) return SV_ERR_TEMPERATURE;
+  if (s->N < 0 || s->N > SV_HEAD_MAX_N || s->V < 1 || s->V > SV_HEAD_MAX_V || (s->row_stride && s->row_stride < s->V) ||
+      (s->grad_stride && s->grad_stride < s->V))
+    return SV_ERR_SHAPE;
+  if (s->N == 0) { *nothing = true; return SV_OK; }
+  if (!logits || !tokens || !norm || !grad_logp || !grad || (grad_entropy && !entropy)) return SV_ERR_NULL;
+  const int64_t rs = s->row_stride ? s->row_stride : s->V, gs = s->grad_stride ? s->grad_stride : s->V;
+  if (logits == grad && (rs != gs || s->dtype != s->grad_dtype)) return SV_ERR_SHAPE;
+  return SV_OK;
+}
+
+}  // namespace sv_logprobs_host
