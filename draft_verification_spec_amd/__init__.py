@@ -1,6 +1,6 @@
 """Python binding of the library's C ABI: spec_verify (include/spec_verify.h),
-sv_kd (include/sv_kd.h), the vocabulary-head operators (include/sv_head.h, in
-head.py) and those on tokens' log-probabilities (include/sv_logprobs.h, in score.py).
+sv_kd (include/sv_kd.h), the vocabulary-head operators (include/sv_head.h and
+include/sv_mx4.h, in head.py) and those on tokens' log-probabilities (include/sv_logprobs.h, in score.py).
 
 Argument marshalling only: every step of the verification runs in the HIP
 library libspec_verify.so built next to this file.  PyTorch supplies device
@@ -17,8 +17,9 @@ from collections import namedtuple
 from typing import Optional
 
 from .head import (Act8, GRAD_HIDDEN, GRAD_TWO_TERMS, GRAD_WEIGHT, HEAD_BAD_TARGET, HEAD_BAD_WEIGHT,  # noqa: F401
-                   HEAD_EMPTY, HEAD_NAN, HEAD_POSINF, HeadCEResult, HeadKDResult, SV_I8, act8_pack, act8_unpack,
-                   bind as _bind_head, head_ce, head_kd, head_logits, sv_head_shape_t, sv_logits_shape_t)
+                   HEAD_EMPTY, HEAD_NAN, HEAD_POSINF, HeadCEResult, HeadKDResult, Mx4, SV_I8, SV_MX4, act8_pack,
+                   act8_unpack, bind as _bind_head, head_ce, head_kd, head_logits, mx4_pack, mx4_unpack,
+                   sv_head_shape_t, sv_logits4_shape_t, sv_logits_shape_t)
 from .score import (LogprobsResult, bind as _bind_logprobs, logprobs, logprobs_grad, sv_logprobs_grad_shape_t,  # noqa: F401
                     sv_logprobs_shape_t)
 

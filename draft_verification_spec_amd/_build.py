@@ -8,7 +8,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "spec_verify.hip")
 SRCS = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("sv_kd.hip", "sv_head.hip", "sv_logits8.hip",
-                                                            "sv_logprobs.hip")]
+                                                            "sv_mx4.hip", "sv_logprobs.hip")]
 LIB = os.path.join(HERE, "libspec_verify.so")
 HEADER = os.path.join(ROOT, "include", "spec_verify.h")
 # the benchmark's stream-read reference (measurement only; not part of the library)

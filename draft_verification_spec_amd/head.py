@@ -1,6 +1,6 @@
-"""Vocabulary-head operators (include/sv_head.h) on torch tensors: 8-bit hidden
-rows, logits of a head held in 8-bit integers, and the cross-entropy and
-distillation losses from hidden rows.
+"""Vocabulary-head operators (include/sv_head.h, include/sv_mx4.h) on torch tensors: rows
+in 8 bits and in microscaled 4 bits, logits of a head held in either, and the
+cross-entropy and distillation losses from hidden rows.
 
 Argument marshalling only, as in the package's front end: every step runs in the
 HIP library.  Scratch memory comes from torch's allocator, one piece per call on
@@ -13,7 +13,8 @@ import contextlib
 import ctypes
 from collections import namedtuple
 
-SV_I8 = 2
+SV_I8, SV_MX4 = 2, 3
+MX4_BLOCK = 32
 GRAD_HIDDEN, GRAD_WEIGHT, GRAD_TWO_TERMS = 1, 2, 4
 HEAD_BAD_TARGET, HEAD_NAN, HEAD_POSINF, HEAD_EMPTY, HEAD_BAD_WEIGHT = 1, 2, 4, 8, 16
 MAX_H, MAX_N, MAX_V = 131072, 1048576, 16777216
@@ -25,6 +26,12 @@ class sv_logits_shape_t(ctypes.Structure):
                 ("out_stride", ctypes.c_int64)]
 
 
+class sv_logits4_shape_t(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("V", ctypes.c_int32), ("hidden_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("hidden_stride", ctypes.c_int64), ("hidden_scale_stride", ctypes.c_int64),
+                ("weight_stride", ctypes.c_int64), ("weight_scale_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
 class sv_head_shape_t(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("hidden_dtype", ctypes.c_int32), ("grads", ctypes.c_int32), ("hidden_stride", ctypes.c_int64),
@@ -34,6 +41,10 @@ class sv_head_shape_t(ctypes.Structure):
 
 #: hidden rows (or a head's rows) in 8 bits: codes int8 [..., H], scale float32 [...]
 Act8 = namedtuple("Act8", "codes scale")
+#: rows [..., width] in 4 bits, 32 elements to a power-of-two scale (the OCP microscaling format
+#: MXFP4): codes uint8 [..., (width + 1) // 2], the even element in the low half of a byte;
+#: scale uint8 [..., (width + 31) // 32], e for 2 ** (e - 127), 255 for NaN
+Mx4 = namedtuple("Mx4", "codes scale width")
 HeadCEResult = namedtuple("HeadCEResult", "loss nll lse status grad_hidden grad_weight")
 HeadKDResult = namedtuple("HeadKDResult", "loss kl weight status grad_hidden grad_weight")
 
@@ -42,11 +53,16 @@ def bind(lib):
     """Declare the operators' C entry points on a loaded library."""
     P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     L, H = ctypes.POINTER(sv_logits_shape_t), ctypes.POINTER(sv_head_shape_t)
+    L4 = ctypes.POINTER(sv_logits4_shape_t)
     for name, args, res in (
             ("sv_act8_pack", [i32, i32, i32, P, i64, P, i64, P, P], ctypes.c_int),
             ("sv_act8_unpack", [i32, i32, P, i64, P, i32, P, P], ctypes.c_int),
             ("sv_head_logits_workspace_bytes", [L], size),
             ("sv_head_logits", [L, P, P, P, P, P, P, size, P], ctypes.c_int),
+            ("sv_mx4_pack", [i32, i32, i32, P, i64, P, i64, P, i64, P], ctypes.c_int),
+            ("sv_mx4_unpack", [i32, i32, P, i64, P, i64, i32, P, P], ctypes.c_int),
+            ("sv_head_logits4_workspace_bytes", [L4], size),
+            ("sv_head_logits4", [L4, P, P, P, P, P, P, size, P], ctypes.c_int),
             ("sv_head_ce_workspace_bytes", [H], size),
             ("sv_head_kd_workspace_bytes", [H], size),
             ("sv_head_ce", [H] + [P] * 12 + [size, P], ctypes.c_int),
@@ -184,6 +200,111 @@ def act8_unpack(a: Act8, dtype=None, *, stream=None):
     return y
 
 
+def _padded(lead, n, unit, dtype, dev):
+    """Memory for rows [..., n] that lie a multiple of `unit` elements apart."""
+    import torch
+    np = -(-n // unit) * unit
+    steps, k = [1], np
+    for d in reversed(lead):
+        steps.append(k)
+        k *= max(d, 1)
+    return torch.empty_strided((*lead, n), steps[::-1], dtype=dtype, device=dev), np
+
+
+def mx4_pack(x, *, stream=None) -> Mx4:
+    """Rows [..., H] (float32 or bfloat16) in microscaled 4 bits: to each 32 elements the scale
+    2 ** (floor(log2(max|x|)) - 2), and x / scale rounded to the nearest of 0, 0.5, 1, 1.5, 2,
+    3, 4, 6 and their negatives, ties to even, the largest magnitudes to 6.  A block with a
+    NaN or an infinity stands for NaN.  Rows of codes lie 128 bytes apart or a multiple, rows
+    of scales 16, so that head_logits reads a head in place."""
+    import torch
+    dt = _code(x.dtype, "rows")
+    if x.dim() < 1 or not 1 <= x.shape[-1] <= MAX_H:
+        raise ValueError(f"rows must be [..., H] with H of 1 .. {MAX_H}")
+    lead, H, dev = x.shape[:-1], x.shape[-1], x.device
+    _fits(x.numel() // H)
+    here, st = _on(dev, stream)
+    with here:
+        r, ld = _rows(x, H, "rows")
+        codes, cld = _padded(lead, (H + 1) // 2, 128, torch.uint8, dev)
+        scale, sld = _padded(lead, -(-H // MX4_BLOCK), 16, torch.uint8, dev)
+        _check(_lib().sv_mx4_pack(r.shape[0], H, dt, r.data_ptr(), ld, codes.data_ptr(), cld, scale.data_ptr(), sld, st))
+    return Mx4(codes, scale, H)
+
+
+def _mx4(a, what):
+    """(width, leading shape, device) of an Mx4 whose parts belong together."""
+    import torch
+    codes, scale, H = a
+    if codes.dtype is not torch.uint8 or scale.dtype is not torch.uint8:
+        raise TypeError(f"{what} codes and scales must be uint8")
+    H = int(H)
+    if codes.dim() < 1 or not 1 <= H <= MAX_H or codes.shape[-1] != (H + 1) // 2:
+        raise ValueError(f"{what} codes must be [..., (width + 1) // 2] with a width of 1 .. {MAX_H}")
+    lead = codes.shape[:-1]
+    if scale.shape != (*lead, -(-H // MX4_BLOCK)) or scale.device != codes.device:
+        raise ValueError(f"{what} scales must be one byte per {MX4_BLOCK} elements of a row on the codes' device")
+    return H, lead, codes.device
+
+
+def mx4_unpack(a: Mx4, dtype=None, *, stream=None):
+    """The rows [..., width] that 4-bit codes and their scales stand for, in dtype (bfloat16
+    unless given)."""
+    import torch
+    if not isinstance(a, Mx4):
+        raise TypeError("rows must be an Mx4")
+    dtype = torch.bfloat16 if dtype is None else dtype
+    dt = _code(dtype, "dtype")
+    H, lead, dev = _mx4(a, "rows'")
+    _fits(a.codes.numel() // ((H + 1) // 2))
+    here, st = _on(dev, stream)
+    with here:
+        c, cld = _rows(a.codes, (H + 1) // 2, "codes")
+        s, sld = _rows(a.scale, -(-H // MX4_BLOCK), "scales")
+        y = torch.empty((*lead, H), dtype=dtype, device=dev)
+        _check(_lib().sv_mx4_unpack(c.shape[0], H, c.data_ptr(), cld, s.data_ptr(), sld, dt, y.data_ptr(), st))
+    return y
+
+
+def _logits4(hidden, weight, out_dtype, workspace, stream):
+    import torch
+    H, lead, dev = _mx4(weight, "weight")
+    if len(lead) != 1:
+        raise TypeError("weight must be an Mx4 with codes [V, (H + 1) // 2]")
+    V = lead[0]
+    if isinstance(hidden, Mx4):
+        h, rows, hdev = _mx4(hidden, "hidden")
+        if h != H:
+            raise ValueError(f"hidden must be [..., {H}]")
+        hc = SV_MX4
+    else:
+        rows, hdev, hc = hidden.shape[:-1], hidden.device, _code(hidden.dtype, "hidden rows")
+    odt = torch.bfloat16 if out_dtype is None else out_dtype
+    oc = _code(odt, "out_dtype")
+    if hdev != dev:
+        raise ValueError("hidden and weight must be on one device")
+    _fits(V | (hidden.codes.numel() // ((H + 1) // 2) if hc == SV_MX4 else hidden.numel() // H))
+    here, st = _on(dev, stream)
+    with here:
+        xs, xsld = None, 0
+        if hc == SV_MX4:
+            x, ld = _rows(hidden.codes, (H + 1) // 2, "hidden codes")
+            xs, xsld = _rows(hidden.scale, -(-H // MX4_BLOCK), "hidden scales")
+        else:
+            x, ld = _rows(hidden, H, "hidden")
+        w, wld = _rows(weight.codes, (H + 1) // 2, "weight codes")
+        ws, wsld = _rows(weight.scale, -(-H // MX4_BLOCK), "weight scales")
+        out = torch.empty((*rows, V), dtype=odt, device=dev)
+        shape = sv_logits4_shape_t(x.shape[0], H, V, hc, oc, ld, xsld, wld, wsld, 0)
+        lib = _lib()
+        n = lib.sv_head_logits4_workspace_bytes(ctypes.byref(shape))
+        buf = _scratch(workspace, n, dev) if n or workspace is not None else None
+        _check(lib.sv_head_logits4(ctypes.byref(shape), x.data_ptr(), None if xs is None else xs.data_ptr(), w.data_ptr(),
+                                   ws.data_ptr(), out.data_ptr(), None if buf is None else buf.data_ptr(),
+                                   0 if buf is None else buf.numel(), st))
+    return out
+
+
 def _hidden(hidden, H, what="hidden"):
     """(rows tensor, its scales or None, device) of hidden rows or an Act8."""
     import torch
@@ -194,14 +315,20 @@ def _hidden(hidden, H, what="hidden"):
     return hidden, None, hidden.device
 
 
-def head_logits(hidden, weight: Act8, *, out_dtype=None, workspace=None, stream=None):
+def head_logits(hidden, weight, *, out_dtype=None, workspace=None, stream=None):
     """Logits [..., V] of hidden rows [..., H] under a head in 8-bit integers, as
     verify takes them: the int32 products of the codes times both scales.
     hidden: float32 or bfloat16 rows, put into 8 bits row by row on the way, or an
     Act8.  weight: Act8 with codes [V, H] (act8_pack of the head, once).
+    Or, for a drafter, under a head in microscaled 4 bits: weight is the Mx4 of rows [V, H]
+    (mx4_pack of the head, once), hidden rows are put into 4 bits on the way or given as an
+    Mx4, and the products of what the codes stand for are summed in fp32.
     out_dtype: bfloat16 unless given, or float32.  workspace: uint8 scratch of at
-    least sv_head_logits_workspace_bytes, 256-byte aligned."""
+    least sv_head_logits_workspace_bytes (4 bits: sv_head_logits4_workspace_bytes),
+    256-byte aligned."""
     import torch
+    if isinstance(weight, Mx4):
+        return _logits4(hidden, weight, out_dtype, workspace, stream)
     if not isinstance(weight, Act8) or weight.codes.dim() != 2 or weight.codes.dtype != torch.int8:
         raise TypeError("weight must be an Act8 with int8 codes [V, H]")
     V, H = weight.codes.shape
