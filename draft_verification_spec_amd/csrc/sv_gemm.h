@@ -190,6 +190,13 @@ template <int DT, int R, int F, int NW, Lie LIE> struct Side {
       pos = pos + STEP == end ? end - nk * STEP : pos + STEP;
     }
   }
+  // rows: the next step's load j alone, and the step after it
+  __device__ __forceinline__ void issue_one(char *buf, int j) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(buf + (wid + j * NW) * 1024), 16, off[j], pos, 0, 0);
+  }
+  __device__ __forceinline__ void next(int nk) { pos = pos + STEP == end ? end - nk * STEP : pos + STEP; }
+  // rows: from here on loads read nothing and put zeros
+  __device__ __forceinline__ void stop() { rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, 0, 0x00020000); }
   static constexpr int READS = LIE == COLS ? KL : F;
   // what the wave's fragments g0 .. g0 + F - 1 (of 16 indices) of half step h hold,
   // for columns in the order of k

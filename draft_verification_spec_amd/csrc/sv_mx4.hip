@@ -416,151 +416,223 @@ template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * 
 }
 
 // The weight's scales as the lanes of the tiled product take them: lane l of 16 rows and 16
-// blocks has row l & 15 and blocks 4 k + (l >> 4), k = 0 .. 3, in one word.  0 past the rows'
-// end (codes of the hidden rows are 0 there; what lies in memory might stand for NaN).
+// blocks has row l & 15 and blocks 4 k + (l >> 4), k = 0 .. 3, in one word.  A thread takes
+// the 16 scales of a row: it turns four words of four blocks into four of every fourth.  0
+// past the rows' end (codes of the hidden rows are 0 there; what lies in memory might stand
+// for NaN).
 __global__ __launch_bounds__(256) void scales_kernel(const uint8_t *s, int64_t ld, int64_t V, int nb, int groups,
-                                                     int64_t words, uint32_t *o) {
+                                                     int64_t items, uint32_t *o) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= words) return;
-  const int lane = threadIdx.x & 63;
-  const int64_t at = i >> 6, tile = at / groups, row = tile * 16 + (lane & 15);
-  const int b = (int)(at - tile * groups) * 16 + (lane >> 4);
-  uint32_t w = 0;
+  if (i >= items) return;
+  const int64_t at = i >> 4, tile = at / groups, row = tile * 16 + (threadIdx.x & 15);
+  const int b = (int)(at - tile * groups) * 16;
+  u32x4 v = 0;
   if (row < V) {
+    const uint8_t *p = s + row * ld + b;
+    if (b + 16 <= nb) {
+      v = *(const u32x4_any *)p;
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (b + 4 * k < nb) w |= (uint32_t)s[row * ld + b + 4 * k] << (8 * k);
+      for (int k = 0; k < 16; ++k)
+        if (b + k < nb) v[k / 4] |= (uint32_t)p[k] << (k % 4 * 8);
+    }
   }
-  o[i] = w;
+  o += at * 64 + (threadIdx.x & 15);
+  const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x05010400), hi = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
+  const uint32_t lo2 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602), hi2 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
+  o[0] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+  o[16] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+  o[32] = __builtin_amdgcn_perm(hi2, lo2, 0x05040100);
+  o[48] = __builtin_amdgcn_perm(hi2, lo2, 0x07060302);
 }
 
-// Many rows: tiles of both operands through LDS, two buffers each, as in sv_gemm.h; a pair of
-// steps at a time, whose four scales of a row are a word.
-template <class T>
-__device__ __forceinline__ void product(f32x4 (&acc)[T::FM][T::FN], char *lds, const Part &X, const Part &Y, int pairs,
-                                        const uint32_t *xs, const uint32_t *ws) {
+#ifdef __HIP_DEVICE_COMPILE__
+// Four products of one hidden fragment, scales in byte K of their words.  The compiler gives
+// the builtin's result registers of its own, and with all of them taken moves sums about
+// (five moves to two products; 1024 rows of 4096 x 151936 457 us), so the sums are tied
+// here.  s_nop: what the compiler may write to a source right before.
+#define SV_MUL4(SEL)                                                                                 \
+  asm volatile("s_nop 1\n\t"                                                                         \
+               "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %4, %8, %0, %9, %13 " SEL " cbsz:4 blgp:4\n\t"  \
+               "v_mfma_scale_f32_16x16x128_f8f6f4 %1, %5, %8, %1, %10, %13 " SEL " cbsz:4 blgp:4\n\t" \
+               "v_mfma_scale_f32_16x16x128_f8f6f4 %2, %6, %8, %2, %11, %13 " SEL " cbsz:4 blgp:4\n\t" \
+               "v_mfma_scale_f32_16x16x128_f8f6f4 %3, %7, %8, %3, %12, %13 " SEL " cbsz:4 blgp:4"      \
+               : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                      \
+               : "v"(y[0]), "v"(y[1]), "v"(y[2]), "v"(y[3]), "v"(x), "v"(sy[0]), "v"(sy[1]), "v"(sy[2]), "v"(sy[3]), "v"(sx))
+template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, const uint32_t *sy, u32x4 x, uint32_t sx) {
+  if constexpr (K == 0) SV_MUL4("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+  else if constexpr (K == 1) SV_MUL4("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+  else if constexpr (K == 2) SV_MUL4("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+  else SV_MUL4("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+}
+#undef SV_MUL4
+#endif
+
+// Many rows: tiles of both operands through LDS, two buffers each, laid as in sv_gemm.h; a
+// pair of steps at a time, whose four scales of a row are a word.  A wave holds one set of
+// fragments of the hidden rows and two of the weight's: a hidden fragment of the next half
+// step is read into the registers of this one's as soon as its products are issued.  The one
+// barrier of a step stands in its middle: by then every wave has read all of the step's
+// buffers, which later loads may overwrite, and the next step's tiles have landed.
+//
+// A workgroup takes one tile after another, and its loads run on into the next: a tile's
+// results leave while the next one's first steps come in (1024 rows of 4096 x 151936 398 us
+// with a workgroup a tile).  Rows a power of two apart lie on few memory channels at any one
+// step, so neighbouring tiles of the vocabulary begin at different pairs.
+template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel(LogitsP P) {
+  __shared__ __align__(16) char lds[2 * (T::XBUF + T::YBUF)];
 #ifdef __HIP_DEVICE_COMPILE__
   typedef Side<SV_I8, T::BM, T::FM, T::NW, ROWS> SX;
   typedef Side<SV_I8, T::BN, T::FN, T::NW, ROWS> SY;
+  static_assert(T::FN % 4 == 0 && T::FN <= T::FM, "products in fours, weight reads beside hidden ones");
+  constexpr int LD = SX::NL + SY::NL, PER = (LD + T::FM - 1) / T::FM;   // loads of a step, beside a fragment's products
+  constexpr int STORES = T::FM * T::FN / (OT == SV_BF16 ? 2 : 1);       // of a wave's whole tile
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int gx = wid / T::WN * T::FM, gy = wid % T::WN * T::FN, nk = 2 * pairs;
+  const int wm = wid / T::WN, wn = wid % T::WN, gx = wm * T::FM, gy = wn * T::FN;
+  const int total = P.mt * P.nt, pairs = P.groups, nk = 2 * pairs;
   SX sx;
   SY sy;
-  sx.start(X, 0, nk, 0);
-  sy.start(Y, 0, nk, 0);
-  char *const yl = lds + 2 * T::XBUF;
-  xs += (int64_t)gx * pairs * 64;
-  ws += (int64_t)gy * pairs * 64;
-  u32x4 x0[T::FM], y0[T::FN], x1[T::FM], y1[T::FN];
+  const uint32_t *xs, *ws;
+  int m0, n0, from;
+  // the loads' tile
+  auto start = [&](int id) {
+    int im, in;
+    tile_at(run_of_xcd(id, total), P.mt, P.nt, P.band, im, in);
+    m0 = im * T::BM;
+    n0 = in * T::BN;
+    from = in % pairs;
+    const Part X = {(const char *)P.xc + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, (int64_t)pairs * 256};
+    const Part Y = {(const char *)P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
+    sx.start(X, 0, nk, 2 * from);
+    sy.start(Y, 0, nk, 2 * from);
+    xs = (const uint32_t *)P.xs + (int64_t)(m0 / 16 + gx) * pairs * 64 + lane;
+    ws = (const uint32_t *)P.ws + (int64_t)(n0 / 16 + gy) * pairs * 64 + lane;
+  };
+  u32x4 x[T::FM], y0[T::FN], y1[T::FN];
   uint32_t sa[T::FM], sb[T::FN], sa2[T::FM], sb2[T::FN];
-  auto scales = [&](uint32_t (&a)[T::FM], uint32_t (&b)[T::FN], int p) {
-#pragma unroll
-    for (int f = 0; f < T::FM; ++f) a[f] = xs[((int64_t)f * pairs + p) * 64 + lane];
-#pragma unroll
-    for (int f = 0; f < T::FN; ++f) b[f] = ws[((int64_t)f * pairs + p) * 64 + lane];
-  };
-  auto read = [&](u32x4 (&x)[T::FM], u32x4 (&y)[T::FN], int b, int h) {
-    SX::read(x, lds + b * T::XBUF, gx, h);
-    SY::read(y, yl + b * T::YBUF, gy, h);
-  };
+  f32x4 acc[T::FM][T::FN];
+  clear<SV_BF16, T>(acc);
+  // this wave's first fragments in a buffer at half step 0 and 1
+  const int o0 = (lane & 15) * STEP + (((lane >> 4) ^ (lane & 7)) << 4), o1 = o0 ^ 64;
+  char *const x0b = lds, *const x1b = lds + T::XBUF, *const y0b = lds + 2 * T::XBUF, *const y1b = y0b + T::YBUF;
+  const int fx = gx * 16 * STEP, fy = gy * 16 * STEP;
+  // This wave's LDS reads are done and its loads have landed, and so are all others'.  The
+  // results of the tile before, which it may have stored since, need not have.
+  bool stored = false;
   auto landed = [&]() {
     asm volatile("" ::: "memory");
-    wait_loads<0, 1>(0);
+    constexpr int S = STORES < 63 ? STORES : 63;
+    if (stored) __builtin_amdgcn_s_waitcnt(0x0070 | (S & 15) | (S >> 4) << 14);
+    else wait_loads<0, 1>(0);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  auto half = [&](auto K, u32x4 (&x)[T::FM], u32x4 (&y)[T::FN]) {
-    constexpr int k = decltype(K)::value;
+  // Products of half step K of a pair; beside them the reads of the next half's fragments from
+  // xb and yb, a later step's loads into xl and yl, and a pair's scales.
+  auto half = [&](auto K, u32x4 (&y)[T::FN], u32x4 (&yn)[T::FN], const char *xb, const char *yb, auto loads, char *xl,
+                  char *yl, auto scales) {
 #pragma unroll
-    for (int f = 0; f < T::FM; ++f)
+    for (int f = 0; f < T::FM; ++f) {
 #pragma unroll
-      for (int g = 0; g < T::FN; ++g) mul<k, k>(acc[f][g], y[g], sb[g], x[f], sa[f]);
+      for (int g = 0; g < T::FN; g += 4) mul4<decltype(K)::value>(&acc[f][g], &y[g], &sb[g], x[f], sa[f]);
+      x[f] = *(const u32x4 *)(xb + f * 16 * STEP);
+      if (f < T::FN) yn[f] = *(const u32x4 *)(yb + f * 16 * STEP);
+      if constexpr (decltype(loads)::value) {
+#pragma unroll
+        for (int j = f * PER; j < (f + 1) * PER && j < LD; ++j) {
+          if (j < SX::NL) sx.issue_one(xl, j);
+          else sy.issue_one(yl, j - SX::NL);
+        }
+      }
+      if constexpr (decltype(scales)::value) {
+        sa2[f] = xs[(f * pairs + from) * 64];
+        if (f < T::FN) sb2[f] = ws[(f * pairs + from) * 64];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (decltype(loads)::value) {
+      sx.next(nk);
+      sy.next(nk);
+    }
   };
-  scales(sa, sb, 0);
-  sx.issue(lds, false, nk);
-  sy.issue(yl, false, nk);
-  sx.issue(lds + T::XBUF, false, nk);
-  sy.issue(yl + T::YBUF, false, nk);
+  typedef std::true_type Yes;
+  typedef std::false_type No;
+  int id = blockIdx.x;
+  start(id);
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) sa[f] = xs[(f * pairs + from) * 64];
+#pragma unroll
+  for (int f = 0; f < T::FN; ++f) sb[f] = ws[(f * pairs + from) * 64];
+  sx.issue(x0b, true, nk);
+  sy.issue(y0b, true, nk);
+  sx.issue(x1b, true, nk);
+  sy.issue(y1b, true, nk);
   landed();
-  read(x0, y0, 0, 0);
-  constexpr int MM = T::FM * T::FN, RD = T::FM + T::FN, LD = SX::NL + SY::NL;
-  auto pair = [&](int p, auto more) {
-    constexpr bool M = decltype(more)::value;            // another pair follows
-    // step 2 p: buffer 0
-    read(x1, y1, 0, 1);
-    half(std::integral_constant<int, 0>(), x0, y0);
-    mix<MM, RD, 0>();
-    landed();
-    if constexpr (M) {
-      sx.issue(lds, true, nk);
-      sy.issue(yl, true, nk);
-      scales(sa2, sb2, p + 1);
-    }
-    read(x0, y0, 1, 0);
-    half(std::integral_constant<int, 1>(), x1, y1);
-    mix<MM, RD, M ? LD + RD : 0>();
-    __builtin_amdgcn_sched_barrier(0);
-    // step 2 p + 1: buffer 1
-    read(x1, y1, 1, 1);
-    half(std::integral_constant<int, 2>(), x0, y0);
-    mix<MM, RD, 0>();
-    landed();
-    if constexpr (M) {
-      sx.issue(lds + T::XBUF, true, nk);
-      sy.issue(yl + T::YBUF, true, nk);
-      read(x0, y0, 0, 0);
-    }
-    half(std::integral_constant<int, 3>(), x1, y1);
-    if constexpr (M) {
-      mix<MM, RD, LD>();
+#pragma unroll
+  for (int f = 0; f < T::FM; ++f) x[f] = *(const u32x4 *)(x0b + fx + o0 + f * 16 * STEP);
+#pragma unroll
+  for (int f = 0; f < T::FN; ++f) y0[f] = *(const u32x4 *)(y0b + fy + o0 + f * 16 * STEP);
+  const Beside beside;
+  for (;;) {
+    const int m1 = m0, n1 = n0;          // this tile, when the loads are at the next
+    for (int p = 0; p < pairs; ++p) {
+      const bool last = p + 1 == pairs;
+      from = from + 1 == pairs ? 0 : from + 1;
+      if (last) {
+        id += gridDim.x;
+        if (id < total) {
+          start(id);
+        } else {                         // loads read nothing, and what is read of LDS is not used
+          sx.stop();
+          sy.stop();
+        }
+      }
+      half(std::integral_constant<int, 0>(), y0, y1, x0b + fx + o1, y0b + fy + o1, No(), nullptr, nullptr, No());
+      landed();
+      stored = false;
+      half(std::integral_constant<int, 1>(), y1, y0, x1b + fx + o0, y1b + fy + o0, Yes(), x0b, y0b, Yes());
+      half(std::integral_constant<int, 2>(), y0, y1, x1b + fx + o1, y1b + fy + o1, No(), nullptr, nullptr, No());
+      landed();
+      half(std::integral_constant<int, 3>(), y1, y0, x0b + fx + o0, y0b + fy + o0, Yes(), x1b, y1b, No());
+      // the last products' results, before an instruction of the compiler's own reads them
+      // (within the loop: it may move sums right behind it)
+      if (last) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
       for (int f = 0; f < T::FM; ++f) sa[f] = sa2[f];
 #pragma unroll
       for (int f = 0; f < T::FN; ++f) sb[f] = sb2[f];
     }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  int p = 0;
-  for (; p + 1 < pairs; ++p) pair(p, std::true_type());
-  pair(p, std::false_type());
-#endif
-}
-
-template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel(LogitsP P) {
-  __shared__ __align__(16) char lds[2 * (T::XBUF + T::YBUF)];
-  int im, in;
-  tile_at(run_of_xcd(blockIdx.x, P.mt * P.nt), P.mt, P.nt, P.band, im, in);
-  const int m0 = im * T::BM, n0 = in * T::BN;
-  f32x4 acc[T::FM][T::FN];
-  clear<SV_BF16, T>(acc);
-  const Part X = {(const char *)P.xc + (int64_t)m0 * P.x_ld, P.x_ld, P.N - m0 < T::BM ? P.N - m0 : T::BM, P.x_ld};
-  const Part Y = {(const char *)P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
-  product<T>(acc, lds, X, Y, P.groups, (const uint32_t *)P.xs + (int64_t)(m0 / 16) * P.groups * 64,
-             (const uint32_t *)P.ws + (int64_t)(n0 / 16) * P.groups * 64);
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, wm = wid / T::WN, wn = wid % T::WN;
-  const Beside beside;
+    stored = m1 + T::BM <= P.N && n1 + T::BN <= P.V;
 #pragma unroll
-  for (int f = 0; f < T::FM; ++f) {
-    const int m = m0 + (wm * T::FM + f) * 16 + (lane & 15);
-    if (m >= P.N) continue;
-    const int64_t row = (int64_t)m * P.out_ld;
+    for (int f = 0; f < T::FM; ++f) {
+      const int m = m1 + (gx + f) * 16 + (lane & 15);
+      if (stored || m < P.N) {
+        const int64_t row = (int64_t)m * P.out_ld;
 #pragma unroll
-    for (int g = 0; g < T::FN; g += OT == SV_BF16 ? 2 : 1) {
-      const int n = n0 + (wn * T::FN + g) * 16;
-      if constexpr (OT == SV_BF16) {
-        float u[4], v[4];
+        for (int g = 0; g < T::FN; g += OT == SV_BF16 ? 2 : 1) {
+          const int n = n1 + (gy + g) * 16;
+          if constexpr (OT == SV_BF16) {
+            float u[4], v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i] = acc[f][g][i];
-          v[i] = acc[f][g + 1][i];
+            for (int i = 0; i < 4; ++i) {
+              u[i] = acc[f][g][i];
+              v[i] = acc[f][g + 1][i];
+            }
+            const u32x4 r = Beside::eight(u, v);
+            if (stored) *(u32x4_any *)(P.out + (row + n + beside.at) * 2) = r;
+            else store8(P.out, row, n + beside.at, P.V, r);
+          } else {
+            const int c = n + (lane >> 4) * 4;
+            store4<SV_F32>(P.out, row + c, stored ? 4 : P.V - c, acc[f][g]);
+          }
         }
-        store8(P.out, row, n + beside.at, P.V, Beside::eight(u, v));
-      } else {
-        const int c = n + (lane >> 4) * 4;
-        store4<SV_F32>(P.out, row + c, P.V - c, acc[f][g]);
       }
     }
+    if (id >= total) break;
+    clear<SV_BF16, T>(acc);
   }
+  __builtin_amdgcn_s_waitcnt(0x0070);    // no load is left that writes to LDS
+#endif
 }
 
 template <int FM, int SRC, int OT> void launch_held(const LogitsP &P, int64_t lds, hipStream_t st) {
@@ -593,7 +665,8 @@ template <class T> void launch_tiles(LogitsP P, int ot, hipStream_t st) {
   P.mt = (int)cdiv(P.N, T::BM);
   P.nt = (int)cdiv(P.V, T::BN);
   P.band = 8;
-  const dim3 grid((unsigned)((int64_t)P.mt * P.nt)), block(T::TPB);
+  const int64_t tiles = (int64_t)P.mt * P.nt, most = sv_mx4_host::CUS * (T::BM == 256 ? 1 : 2);   // as LDS holds
+  const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(T::TPB);
   if (ot == SV_BF16) hipLaunchKernelGGL((tile_kernel<T, SV_BF16>), grid, block, 0, st, P);
   else hipLaunchKernelGGL((tile_kernel<T, SV_F32>), grid, block, 0, st, P);
 }
@@ -690,7 +763,7 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
   {
     Rows R = P.x;
     R.lanes = (int32_t)(L.Kp / 4);
-    Out O = {ws + L.codes, ws + L.scales, L.Kp, 0, s.N, 0, L.groups};
+    Out O = {ws + L.codes, ws + L.scales, L.x_ld, 0, s.N, 0, L.groups};
     const int64_t most = sv_head_host::max_groups(256) * 1024 / R.lanes / 16 * 16;
     for (int64_t n = 0; n < s.N; n += most) {
       const int64_t rows = s.N - n < most ? s.N - n : most;
@@ -701,7 +774,7 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
       O.scale += rows * L.groups * 16;
     }
   }
-  P.x_ld = L.Kp;
+  P.x_ld = L.x_ld;
   P.groups = (int32_t)L.groups;
   const bool direct = codes_direct(P.w_ld, (uintptr_t)weight_codes);
   const int64_t w_ld = P.w_ld, s_ld = P.s_ld, step = direct ? L.scaled : L.piece;
@@ -714,13 +787,14 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
       // bytes does (aligned, so it lies in that byte's memory)
       P.w_bytes = up(code_bytes(s.H), 4);
     } else {
-      copy_rows(weight_codes + v0 * w_ld, w_ld, code_bytes(s.H), (char *)ws + L.weight, L.Kp, L.Kp, P.V, st);
+      copy_rows(weight_codes + v0 * w_ld, w_ld, code_bytes(s.H), (char *)ws + L.weight, L.x_ld, L.Kp, P.V, st);
       P.w = ws + L.weight;
-      P.w_ld = P.w_bytes = L.Kp;
+      P.w_ld = L.x_ld;
+      P.w_bytes = L.Kp;
     }
-    const int64_t words = up(P.V, 256) * L.groups * 4;
-    hipLaunchKernelGGL(scales_kernel, dim3((unsigned)cdiv(words, 256)), dim3(256), 0, st, weight_scale + v0 * s_ld, s_ld,
-                       (int64_t)P.V, (int)blocks(s.H), (int)L.groups, words, (uint32_t *)(ws + L.wscale));
+    const int64_t items = up(P.V, 256) * L.groups;
+    hipLaunchKernelGGL(scales_kernel, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, st, weight_scale + v0 * s_ld, s_ld,
+                       (int64_t)P.V, (int)blocks(s.H), (int)L.groups, items, (uint32_t *)(ws + L.wscale));
     P.ws = ws + L.wscale;
     P.out = (char *)logits + v0 * oe;
     if (L.large) launch_tiles<Tile<8, 8, 2, 2, 2, 2>>(P, s.out_dtype, st);

@@ -45,7 +45,7 @@ struct Plan {
   bool fused;                            // held: every workgroup forms the hidden rows' codes itself
   int64_t nks;                           // held: 128-element steps of k
   int64_t image, x_scales;               // bytes of the hidden rows' codes and scales, as staged
-  int64_t Kp;                            // tiles: bytes of a staged code row
+  int64_t Kp, x_ld;                      // tiles: bytes of a staged code row, and between two
   int64_t groups;                        // tiles: 16-block groups of scales
   bool large;                            // tiles of 256 x 256
   // tiles: vocabulary entries per product where the weight is copied, and where only its
@@ -97,17 +97,18 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
     p.total = o;
     return p;
   }
-  p.image = N * p.Kp;
+  p.x_ld = sv_head_host::spread(p.Kp);
+  p.image = N * p.x_ld;
   p.x_scales = up(N, 256) * p.groups * 16;
   // a copied piece of about 128 MB: it stays in the 256 MB Infinity Cache between its copy and its product
-  p.piece = up(((int64_t)128 << 20) / p.Kp, 256);
+  p.piece = up(((int64_t)128 << 20) / p.x_ld, 256);
   if (p.piece > up(s->V, 256)) p.piece = up(s->V, 256);
   // staged scales of a piece: 256 MB at most, and a launch's worth
   p.scaled = ((int64_t)256 << 20) / (p.groups * 16) / 256 * 256;
   if (p.scaled > up(s->V, 256)) p.scaled = up(s->V, 256);
   p.codes = take(p.image);
   p.scales = take(p.x_scales);
-  p.weight = take(p.piece * p.Kp);       // (an aligned stride may still meet an unaligned address)
+  p.weight = take(p.piece * p.x_ld);       // (an aligned stride may still meet an unaligned address)
   p.wscale = take((p.scaled > p.piece ? p.scaled : p.piece) * p.groups * 16);
   p.total = o;
   return p;

@@ -140,11 +140,11 @@ int main() {
     } else {
       NEED(p.Kp % SPAN == 0 && 2 * p.Kp >= H && p.groups * SPAN == p.Kp && p.groups * 16 * BLOCK >= H);
       NEED(p.piece % 256 == 0 && p.piece >= 256 && p.scaled % 256 == 0 && p.scaled >= 256);
-      NEED(p.scales - p.codes >= (size_t)N * p.Kp && p.weight - p.scales >= (size_t)(up(N, 256) * p.groups * 16));
-      NEED(p.wscale - p.weight >= (size_t)(p.piece * p.Kp));
+      NEED(p.x_ld >= p.Kp && p.x_ld % 16 == 0 && p.x_ld <= MAX_LD && p.scales - p.codes >= (size_t)N * p.x_ld && p.weight - p.scales >= (size_t)(up(N, 256) * p.groups * 16));
+      NEED(p.wscale - p.weight >= (size_t)(p.piece * p.x_ld));
       NEED(p.total - p.wscale >= (size_t)((p.piece > p.scaled ? p.piece : p.scaled) * p.groups * 16));
       // a launch of the scales' words, and a tile's offsets
-      NEED((p.piece > p.scaled ? p.piece : p.scaled) * p.groups * 4 < 0xffffffffLL && 255 * p.Kp < 0x7fffffffLL);
+      NEED((p.piece > p.scaled ? p.piece : p.scaled) * p.groups * 4 < 0xffffffffLL && 255 * p.x_ld < 0x7fffffffLL);
     }
     if (p.total && !nothing)
       NEED(check_logits(&s, mem, mem, mem, mem, mem, mem, p.total - 1, &nothing) == SV_ERR_WORKSPACE);
