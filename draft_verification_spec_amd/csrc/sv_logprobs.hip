@@ -1,12 +1,12 @@
 // sv_logprobs.hip -- log-probabilities of given tokens with the rows' entropies and
 // largest alternatives, and their gradient, for gfx950 (MI355X).
 //
-// One pass over the logits.  With the running maximum m of what a thread has read and d =
-// z - m, it keeps s = sum 2^(d c) and a = sum 2^(d c) d, c = log2(e) / T; a larger maximum
-// M scales both by f = 2^((m - M) c), a -> f (a + s (m - M)).  At the end ln s is the
-// normaliser's part beyond the maximum, and ln s - a / (s T) the entropy.  d is a
-// difference of two logits before anything is scaled, so rows of any magnitude, those
-// filled with the type's lowest value among them, keep their precision.
+// One pass over the logits.  With the running maximum m of what a thread has read, c =
+// log2(e) / T and y = (z - m) c, it keeps s = sum 2^y and a = sum 2^y y; a larger maximum M
+// scales both by f = 2^((m - M) c), a -> f (a + s (m - M) c).  At the end ln s is the
+// normaliser's part beyond the maximum, and ln s - ln 2 a / s the entropy.  Exponents are
+// exact to their own rounding whatever the logits' magnitude (rows filled with the type's
+// lowest value among them).
 //
 // Alternatives: a wave keeps the `top` best keys it has seen, a key holding value and
 // index so that larger is better and no two are equal.  A vector of logits costs one
@@ -49,7 +49,7 @@ struct LogprobsP {
   Key *keys;                             // [N][parts][LIST]
 };
 
-// s and a of the entries seen, relative to their maximum m
+// s = sum 2^y and a = sum 2^y y of the entries seen, y = (z - m) c with their maximum m
 struct Stat {
   float m;
   double s, a;
@@ -62,7 +62,7 @@ __device__ __forceinline__ Stat join(const Stat &x, const Stat &y, float c) {
   auto part = [&](const Stat &t, double &s, double &a) {
     const float d = t.m - r.m, f = t.m == r.m ? 1.f : __builtin_amdgcn_exp2f(d * c);
     s = f > 0.f ? t.s * (double)f : 0.0;
-    a = f > 0.f ? (t.m == r.m ? t.a : (t.a + t.s * (double)d) * (double)f) : 0.0;
+    a = f > 0.f ? (t.m == r.m ? t.a : (t.a + t.s * (double)(d * c)) * (double)f) : 0.0;
   };
   double s, a;
   part(x, r.s, r.a);
@@ -72,13 +72,17 @@ __device__ __forceinline__ Stat join(const Stat &x, const Stat &y, float c) {
   return r;
 }
 
+// Of all lanes: the common maximum first, then each lane's part scaled to it once, so that the
+// sums are plain ones (the lanes' order is fixed).
 __device__ __forceinline__ Stat wave_join(Stat v, float c) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const Stat w = {__shfl_xor(v.m, o), __shfl_xor(v.s, o), __shfl_xor(v.a, o)};
-    v = (threadIdx.x & o) ? join(w, v, c) : join(v, w, c);
-  }
-  return v;
+  Stat r;
+  r.m = wave_max_f(v.m);
+  const float d = v.m - r.m, f = v.m == r.m ? 1.f : __builtin_amdgcn_exp2f(d * c);
+  const bool some = f > 0.f;             // (NaN and empty lanes: none)
+  const double a = v.m == r.m ? v.a : v.a + v.s * (double)(d * c);
+  r.s = wave_sum_d(some ? v.s * (double)f : 0.0);
+  r.a = wave_sum_d(some ? a * (double)f : 0.0);
+  return r;
 }
 
 // The order of floats as that of unsigned integers; -0 as +0.  Never 0 for a number.
@@ -94,12 +98,13 @@ __device__ __forceinline__ float value_of(Key k) {
 
 // Keys of the 64 lanes in descending order (a bitonic sort: 21 exchanges).
 __device__ __forceinline__ Key sort_wave(Key k) {
-  const int lane = threadIdx.x & 63;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));         // (what depends on it is formed here, not held throughout)
 #pragma unroll
   for (int n = 2; n <= 64; n <<= 1)
 #pragma unroll
     for (int j = n >> 1; j; j >>= 1) {
-      const Key o = __shfl_xor(k, j);
+      const Key o = __shfl(k, lane ^ j);
       const bool larger = ((lane & j) == 0) == ((lane & n) == 0);
       k = (o > k) == larger ? o : k;
     }
@@ -125,6 +130,7 @@ struct Best {
   Key worst;                             // the top-th of them: better ones are taken
   float border;                          // its value
   int count;                             // keys in the buffer
+  bool sorted;                           // whether any are in the list
   Key *buffer;                           // LIST keys in LDS, the wave's own
 
   __device__ __forceinline__ void start(Key *b) {
@@ -132,6 +138,7 @@ struct Best {
     worst = key_of(NEG_INF, 0);          // an entry of -inf is none
     border = NEG_INF;
     count = 0;
+    sorted = false;
     buffer = b;
   }
   __device__ __forceinline__ void flush(int top) {
@@ -141,6 +148,7 @@ struct Best {
     __builtin_amdgcn_wave_barrier();
     list = sort_wave(k);
     count = 0;
+    sorted = true;
     const Key w = __shfl(list, top - 1);
     if (w > worst) {
       worst = w;
@@ -149,6 +157,7 @@ struct Best {
   }
   // one entry of each lane
   __device__ __forceinline__ void offer(float v, uint32_t index, int top) {
+    if (!__ballot(v >= border)) return;
     Key k = v >= border ? key_of(v, index) : 0;
     uint64_t who = __ballot(k > worst);
     while (who) {
@@ -165,16 +174,34 @@ struct Best {
   }
 };
 
-// The first border: the top-th largest of the lanes' maxima, so that at least `top` entries
-// reach it and few others do.
-__device__ __forceinline__ void first_border(Best &b, float most, int top) {
-  uint32_t at = 0;
-  const uint32_t u = most > NEG_INF ? order_of(most) : 0;
-#pragma unroll
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = at | 1u << bit;
-    if (__popcll(__ballot(u >= t)) >= top) at = t;
+// The first border: of 64 groups of lanes (WAVES lanes each) the top-th largest maximum, cut to
+// 16 bits, so that at least `top` entries reach it and few others do (of random rows 24 for 20,
+// 44 for 32).  groups: 64 words in LDS, and one for the result.
+template <int WAVES> __device__ __forceinline__ void first_border(Best &b, float most, int top, uint32_t *groups) {
+  static_assert(WAVES == 4 || WAVES == 16, "groups within a row of lanes");
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  uint32_t u = most > NEG_INF ? order_of(most) : 0;
+  auto with = [&](uint32_t v) { u = v > u ? v : u; };
+  with(dpp<0xb1, 0xf, 0xf>(u, u));       // lanes 1 and 2 apart
+  with(dpp<0x4e, 0xf, 0xf>(u, u));
+  if constexpr (WAVES == 16) {
+    with(dpp<0x124, 0xf, 0xf>(u, u));    // turned by 4 and 8
+    with(dpp<0x128, 0xf, 0xf>(u, u));
   }
+  if (lane % WAVES == 0) groups[wid * (64 / WAVES) + lane / WAVES] = u;
+  __syncthreads();
+  if (wid == 0) {
+    u = groups[lane];
+    uint32_t at = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t t = at | 1u << bit;
+      at = __popcll(__ballot(u >= t)) >= top ? t : at;
+    }
+    if (lane == 0) groups[64] = at;
+  }
+  __syncthreads();
+  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)groups[64]);
   if (at > order_of(NEG_INF)) {
     b.worst = ((Key)at << 32) - 1;
     b.border = value_of((Key)at << 32);
@@ -221,7 +248,7 @@ __device__ __forceinline__ void finish(const LogprobsP &P, int64_t n, const Stat
   const double T = (double)P.T, ls = log(t.s);
   if (lane == 0) {
     const float none = __builtin_nanf("");
-    const double logp = ((double)zt - (double)t.m) / T - ls, h = ls - t.a / t.s / T;
+    const double logp = ((double)zt - (double)t.m) / T - ls, h = ls - t.a / t.s * LN2;
     P.logp[n] = st ? none : (float)(logp < 0.0 ? logp : 0.0);
     if (P.entropy) P.entropy[n] = st ? none : (float)(h > 0.0 ? h : 0.0);
     if (P.lse) P.lse[n] = st ? none : (float)((double)t.m / T + ls);
@@ -253,10 +280,44 @@ __device__ __forceinline__ void left_out(const LogprobsP &P, int64_t n) {
   }
 }
 
-// The lists of WAVES waves into one, in wave 0's lanes: pairs, then pairs of pairs.
-template <int WAVES> __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[LIST]) {
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  if (lane < LIST) lists[wid][lane] = mine;
+// The waves' best keys into one list, in wave 0's lanes.  Few (the usual case): each goes to the
+// place that the number of larger ones gives it.  Many: sorted lists are joined in pairs, then
+// pairs of pairs.
+template <int WAVES>
+__device__ __forceinline__ Key join_best(Best &best, Key (*lists)[LIST], int32_t *counts, Key *all, int top) {
+  constexpr int FEW = 256;
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  if (best.sorted) {
+    best.flush(top);
+    if (lane < LIST) lists[wid][lane] = best.list;
+    best.count = __popcll(__ballot(lane < top && best.list != 0));
+  }
+  if (lane == 0) counts[wid] = best.count;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int c = counts[w];
+    before += w < wid ? c : 0;
+    total += c;
+  }
+  if (total <= FEW) {
+    if (lane < best.count) all[before + lane] = lists[wid][lane];
+    if (tid < LIST) all[FEW + tid] = 0;
+    __syncthreads();
+    if (tid < total) {
+      const Key k = all[tid];
+      int place = 0;
+      for (int j = 0; j < total; ++j) place += all[j] > k;
+      if (place < LIST) all[FEW + place] = k;
+    }
+    __syncthreads();
+    return all[FEW + lane % LIST];
+  }
+  if (!best.sorted) {
+    best.flush(top);
+    if (lane < LIST) lists[wid][lane] = best.list;
+  }
 #pragma unroll
   for (int n = 1; n < WAVES; n <<= 1) {
     __syncthreads();
@@ -269,29 +330,38 @@ template <int WAVES> __device__ __forceinline__ Key join_lists(Key mine, Key (*l
   return lists[0][lane % LIST];
 }
 
-template <int DT, int WAVES, bool TOP> __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(LogprobsP P) {
+template <int DT, int WAVES, bool TOP>
+__global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(LogprobsP P) {
   constexpr int W = Fmt<DT>::W;
-  __shared__ Key lists[TOP ? WAVES : 1][LIST];
+  __shared__ Key lists[TOP ? WAVES : 1][LIST], all[TOP ? 256 + LIST : 1];
+  __shared__ uint32_t groups[TOP ? 65 : 1];
+  __shared__ int32_t counts[TOP ? WAVES : 1];
   __shared__ Stat stats[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   const int64_t n = blockIdx.x / P.parts;
   const int part = (int)(blockIdx.x - n * P.parts);
-  const int token = P.tokens[n];
-  if (token == P.ignore) {
-    if (part == 0) left_out(P, n);
-    return;
-  }
   const char *row = P.z + n * P.z_ld;
-  const float c = LOG2E / P.T, least = -1e4f / c;
+  const float c = LOG2E / P.T;
   // steps of the row in equal runs
   const int64_t b0 = part * P.batches / P.parts, b1 = (part + 1) * P.batches / P.parts;
   const int64_t end = b1 * P.batch < P.V ? b1 * P.batch : P.V;
   int64_t at = b0 * P.batch + (int64_t)tid * W;
   Stat t = {NEG_INF, 0.0, 0.0};
+  // Whether the wave's entries ask for the careful way: masked ones (0 times -inf), or so large
+  // that a product's rounding is no small part of an exponent.
+  bool general = false;
   Best best;
-  if constexpr (TOP) best.start(lists[wid]);
   u32x4 r[VECS], next[VECS];
   load_step<DT, WAVES>(row, at, end, r);
+  // the first loads go out before the token is known
+  const int token = P.tokens[n];
+  if (token == P.ignore) {
+    if (part == 0) left_out(P, n);
+    return;
+  }
+  const bool bad = token < 0 || token >= P.V;
+  const float zt = wid == 0 && !bad ? load_elem<DT>(row, token) : 0.f;
+  if constexpr (TOP) best.start(lists[wid]);
   for (int64_t b = b0; b < b1; ++b, at += P.batch) {
     if (b + 1 < b1) load_step<DT, WAVES>(row, at + P.batch, end, next);
     float top[VECS], most = NEG_INF;
@@ -306,27 +376,73 @@ template <int DT, int WAVES, bool TOP> __global__ __launch_bounds__(64 * WAVES) 
     if (m != t.m) {                      // (NaN too)
       t = join(t, Stat{m, 0.0, 0.0}, c);
     }
-    const float ref = m == NEG_INF ? 0.f : m;
+    const float ref = m == NEG_INF ? 0.f : m, rc = ref * c;
+    // (each pass unpacks its entries again: held unpacked they would take 32 registers)
+#pragma unroll
+    for (int s = 0; s < VECS; ++s) asm volatile("" : "+v"(r[s]));
     float s1 = 0.f, a1 = 0.f;
-#pragma unroll
-    for (int s = 0; s < VECS; ++s)
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float d = __builtin_fmaxf(unpack<DT>(r[s], w) - ref, least), e = __builtin_amdgcn_exp2f(d * c);
-        s1 += e;
-        a1 = fmaf(e, d, a1);
-      }
-    t.s += (double)s1;
-    t.a += (double)a1;
-    if constexpr (TOP) {
-      if (b == b0) first_border(best, most, P.top);
+    general |= (b + 1) * P.batch > end;  // (what fills the last step is -inf)
+    if (!general) {
+      // one fused step an exponent; rc's rounding, the same for all, is taken out of the sums
 #pragma unroll
       for (int s = 0; s < VECS; ++s)
-        if (__ballot(b == b0 ? top[s] >= best.border : top[s] > best.border)) {
-          const uint32_t i = (uint32_t)(at + (int64_t)s * (64 * WAVES * W));
 #pragma unroll
-          for (int w = 0; w < W; ++w) best.offer(unpack<DT>(r[s], w), i + w, P.top);
+        for (int w = 0; w < W; ++w) {
+          const float y = fmaf(unpack<DT>(r[s], w), c, -rc), e = __builtin_amdgcn_exp2f(y);
+          s1 += e;
+          a1 = fmaf(e, y, a1);           // (NaN where an entry is -inf)
         }
+      const float lo = fmaf(ref, c, -rc);
+      if (__ballot(!(a1 == a1) || !(fabsf(rc) <= 65536.f))) {
+        general = true;
+      } else {
+        const double k = (double)__builtin_amdgcn_exp2f(-lo);
+        t.s += (double)s1 * k;
+        t.a += (double)fmaf(-lo, s1, a1) * k;
+      }
+    }
+    if (general) {
+#pragma unroll
+      for (int s = 0; s < VECS; ++s) asm volatile("" : "+v"(r[s]));
+      s1 = a1 = 0.f;
+#pragma unroll
+      for (int s = 0; s < VECS; ++s)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float y = __builtin_fmaxf((unpack<DT>(r[s], w) - ref) * c, -1e4f), e = __builtin_amdgcn_exp2f(y);
+          s1 += e;
+          a1 = fmaf(e, y, a1);
+        }
+      t.s += (double)s1;
+      t.a += (double)a1;
+    }
+    if constexpr (TOP) {
+      if (b == b0) first_border<WAVES>(best, most, P.top, groups);
+      // few lanes' vectors have an entry to take: each of those is spread over the lanes
+      uint64_t who[VECS], some = 0;
+#pragma unroll
+      for (int s = 0; s < VECS; ++s) some |= who[s] = __ballot(b == b0 ? top[s] >= best.border : top[s] > best.border);
+#pragma unroll 1
+      for (int s = 0; some && s < VECS; ++s) {
+        u32x4 v = r[0];
+        uint64_t w = who[0];
+#pragma unroll
+        for (int j = 1; j < VECS; ++j)
+          if (s == j) {
+            v = r[j];
+            w = who[j];
+          }
+        while (w) {
+          const int l = __builtin_ctzll(w);
+          w &= w - 1;
+          const uint32_t u0 = readlane(v[0], l), u1 = readlane(v[1], l), u2 = readlane(v[2], l), u3 = readlane(v[3], l);
+          const int q = DT == SV_BF16 ? lane >> 1 : lane;
+          uint32_t u = q & 2 ? (q & 1 ? u3 : u2) : (q & 1 ? u1 : u0);
+          if constexpr (DT == SV_BF16) u = lane & 1 ? u & 0xffff0000u : u << 16;
+          const int64_t i = at + (int64_t)s * (64 * WAVES * W) + (int64_t)(l - lane) * W;
+          best.offer(lane < W ? __uint_as_float(u) : NEG_INF, (uint32_t)i + lane, P.top);
+        }
+      }
     }
 #pragma unroll
     for (int s = 0; s < VECS; ++s) r[s] = next[s];
@@ -334,14 +450,12 @@ template <int DT, int WAVES, bool TOP> __global__ __launch_bounds__(64 * WAVES) 
   t = wave_join(t, c);
   Key k = 0;
   if constexpr (TOP) {
-    best.flush(P.top);
-    k = join_lists<WAVES>(best.list, lists);
+    k = join_best<WAVES>(best, lists, counts, all, P.top);
   }
   if (lane == 0) stats[wid] = t;
   __syncthreads();
   if (wid) return;
-  t = stats[0];
-  for (int w = 1; w < WAVES; ++w) t = join(t, stats[w], c);
+  t = wave_join(lane < WAVES ? stats[lane] : Stat{NEG_INF, 0.0, 0.0}, c);
   if (P.parts > 1) {
     double *o = P.stats + 3 * (int64_t)blockIdx.x;
     if (lane == 0) {
@@ -352,8 +466,7 @@ template <int DT, int WAVES, bool TOP> __global__ __launch_bounds__(64 * WAVES) 
     if (TOP && lane < LIST) P.keys[(int64_t)blockIdx.x * LIST + lane] = k;
     return;
   }
-  const bool bad = token < 0 || token >= P.V;
-  finish(P, n, t, k, bad ? 0.f : load_elem<DT>(row, token), bad);
+  finish(P, n, t, k, zt, bad);
 }
 
 // The parts of a row in order: one wave.
