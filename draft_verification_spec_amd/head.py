@@ -204,6 +204,8 @@ def _padded(lead, n, unit, dtype, dev):
     """Memory for rows [..., n] that lie a multiple of `unit` elements apart."""
     import torch
     np = -(-n // unit) * unit
+    if len(lead) == 1:
+        return torch.empty_strided((lead[0], n), (np, 1), dtype=dtype, device=dev), np
     steps, k = [1], np
     for d in reversed(lead):
         steps.append(k)
@@ -371,6 +373,8 @@ def _int32(t, dev, what, shape, ignore=-1):
 
 def _float(t, dev, what, shape):
     import torch
+    if t.dtype is torch.float32 and t.shape == shape and t.device == dev:
+        return t.contiguous()
     if not t.is_floating_point() or tuple(t.shape) != tuple(shape) or t.device != dev:
         raise ValueError(f"{what} must be floating {list(shape)} on the rows' device")
     return t.to(dtype=torch.float32).contiguous()

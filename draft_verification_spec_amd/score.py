@@ -78,21 +78,26 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
     with here:
         r, ld = _rows(logits, V, "logits")
         t = _int32(tokens, dev, "tokens", lead, ignore)
-        f = torch.empty((5, *lead), dtype=torch.float32, device=dev)
-        status = torch.empty(lead, dtype=torch.int32, device=dev)
-        tv = ti = None
-        if top:
-            tv = torch.empty((*lead, top), dtype=torch.float32, device=dev)
-            ti = torch.empty((*lead, top), dtype=torch.int32, device=dev)
-        shape = sv_logprobs_shape_t(r.shape[0], V, dt, top, ld, float(temperature), ignore)
-        lib, n = _lib(), 4 * r.shape[0]
+        # one piece of memory for all results (a tensor of its own costs the host three views)
+        n = r.shape[0]
+        k = n * top
+        f = torch.empty(6 * n + 2 * k, dtype=torch.float32, device=dev)
+        logp, entropy, lse, norm, status, tv, ti = f.split_with_sizes((n, n, n, 2 * n, n, k, k))
+        status, ti = status.view(torch.int32), ti.view(torch.int32)
+        shape = sv_logprobs_shape_t(n, V, dt, top, ld, float(temperature), ignore)
+        lib = _lib()
         need = lib.sv_logprobs_workspace_bytes(ctypes.byref(shape))
         buf = _scratch(workspace, need, dev) if need or workspace is not None else None
         p = f.data_ptr()
-        _check(lib.sv_logprobs(ctypes.byref(shape), r.data_ptr(), t.data_ptr(), p, p + n, p + 2 * n, p + 3 * n,
-                               status.data_ptr(), tv.data_ptr() if top else None, ti.data_ptr() if top else None,
+        at = p + 24 * n
+        _check(lib.sv_logprobs(ctypes.byref(shape), r.data_ptr(), t.data_ptr(), p, p + 4 * n, p + 8 * n, p + 12 * n,
+                               p + 20 * n, at if top else None, at + 4 * k if top else None,
                                None if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(), st))
-    return LogprobsResult(f[0], f[1], f[2], f[3:], status, tv, ti)
+    if len(lead) != 1:
+        logp, entropy, lse, status = logp.view(lead), entropy.view(lead), lse.view(lead), status.view(lead)
+    if not top:
+        return LogprobsResult(logp, entropy, lse, norm.view(2, *lead), status, None, None)
+    return LogprobsResult(logp, entropy, lse, norm.view(2, *lead), status, tv.view(*lead, top), ti.view(*lead, top))
 
 
 def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entropy=None, temperature: float = 1.0, *,
