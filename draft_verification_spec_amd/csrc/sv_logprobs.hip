@@ -280,6 +280,22 @@ __device__ __forceinline__ void left_out(const LogprobsP &P, int64_t n) {
   }
 }
 
+// The lists of WAVES waves into one, in all waves' lanes: pairs, then pairs of pairs.
+template <int WAVES> __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[LIST]) {
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  if (lane < LIST) lists[wid][lane] = mine;
+#pragma unroll 1
+  for (int n = 1; n < WAVES; n <<= 1) {
+    __syncthreads();
+    if (wid % (2 * n) == 0) {
+      const Key k = merge_lists(lists[wid + (lane >= LIST ? n : 0)][lane % LIST]);
+      if (lane < LIST) lists[wid][lane] = k;
+    }
+  }
+  __syncthreads();
+  return lists[0][lane % LIST];
+}
+
 // The waves' best keys into one list, in wave 0's lanes.  Few (the usual case): each goes to the
 // place that the number of larger ones gives it.  Many: sorted lists are joined in pairs, then
 // pairs of pairs.
@@ -314,20 +330,8 @@ __device__ __forceinline__ Key join_best(Best &best, Key (*lists)[LIST], int32_t
     __syncthreads();
     return all[FEW + lane % LIST];
   }
-  if (!best.sorted) {
-    best.flush(top);
-    if (lane < LIST) lists[wid][lane] = best.list;
-  }
-#pragma unroll
-  for (int n = 1; n < WAVES; n <<= 1) {
-    __syncthreads();
-    if (wid % (2 * n) == 0) {
-      const Key k = merge_lists(lists[wid + (lane >= LIST ? n : 0)][lane % LIST]);
-      if (lane < LIST) lists[wid][lane] = k;
-    }
-  }
-  __syncthreads();
-  return lists[0][lane % LIST];
+  if (!best.sorted) best.flush(top);
+  return join_lists<WAVES>(best.list, lists);
 }
 
 template <int DT, int WAVES, bool TOP>
@@ -469,27 +473,36 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(LogprobsP P) {
   finish(P, n, t, k, zt, bad);
 }
 
-// The parts of a row in order: one wave.
-template <int DT> __global__ __launch_bounds__(64) void join_kernel(LogprobsP P) {
-  const int lane = threadIdx.x;
+// The parts of a row, lane p part p's sums; of the lists, wave w joins every WAVES-th, then they
+// are joined in pairs.  One wave where there are none.
+template <int DT, int WAVES> __global__ __launch_bounds__(64 * WAVES) void join_kernel(LogprobsP P) {
+  __shared__ Key lists[WAVES][LIST];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int64_t n = blockIdx.x;
   const int token = P.tokens[n];
   if (token == P.ignore) return;
   const float c = LOG2E / P.T;
-  Stat t = {NEG_INF, 0.0, 0.0};
-  if (lane < P.parts) {
-    const double *o = P.stats + 3 * (n * P.parts + lane);
-    t = Stat{(float)o[0], o[1], o[2]};
-  }
-  t = wave_join(t, c);
-  Key k = 0;
-  if (P.top) {
-    const Key *keys = P.keys + n * P.parts * LIST;
-    k = lane < LIST ? keys[lane] : 0;
-    for (int p = 1; p < P.parts; ++p) k = merge_lists(lane < LIST ? k : keys[p * LIST + lane - LIST]);
-  }
   const bool bad = token < 0 || token >= P.V;
-  finish(P, n, t, k, bad ? 0.f : load_elem<DT>(P.z + n * P.z_ld, token), bad);
+  Stat t = {NEG_INF, 0.0, 0.0};
+  float zt = 0.f;
+  if (wid == 0) {
+    if (!bad) zt = load_elem<DT>(P.z + n * P.z_ld, token);
+    if (lane < P.parts) {
+      const double *o = P.stats + 3 * (n * P.parts + lane);
+      t = Stat{(float)o[0], o[1], o[2]};
+    }
+    t = wave_join(t, c);
+  }
+  Key k = 0;
+  if constexpr (WAVES > 1) {
+    const Key *keys = P.keys + n * P.parts * LIST;
+    for (int p = wid; p < P.parts; p += WAVES) {
+      const Key other = lane >= LIST ? keys[p * LIST + lane - LIST] : k;
+      k = p == wid ? __shfl(other, lane + LIST) : merge_lists(other);
+    }
+    k = join_lists<WAVES>(k, lists);
+  }
+  if (wid == 0) finish(P, n, t, k, zt, bad);
 }
 
 template <int DT> void launch(const LogprobsP &P, int waves, int64_t n, hipStream_t st) {
@@ -501,7 +514,10 @@ template <int DT> void launch(const LogprobsP &P, int waves, int64_t n, hipStrea
     if (P.top) hipLaunchKernelGGL((logprobs_kernel<DT, 16, true>), grid, block, 0, st, P);
     else hipLaunchKernelGGL((logprobs_kernel<DT, 16, false>), grid, block, 0, st, P);
   }
-  if (P.parts > 1) hipLaunchKernelGGL((join_kernel<DT>), dim3((unsigned)n), dim3(64), 0, st, P);
+  if (P.parts > 1) {
+    if (P.top) hipLaunchKernelGGL((join_kernel<DT, 16>), dim3((unsigned)n), dim3(1024), 0, st, P);
+    else hipLaunchKernelGGL((join_kernel<DT, 1>), dim3((unsigned)n), dim3(64), 0, st, P);
+  }
 }
 
 // ------------------------------------------------------------------- gradient

@@ -31,12 +31,19 @@ struct Plan {
 inline Plan plan_for(const sv_logprobs_shape_t *s) {
   Plan p;
   const int64_t w = 16 / esize(s->dtype);
-  p.waves = s->N >= 1024 ? 4 : 16;
+  // Few rows are cut into parts, joined in a launch of their own, where a row is more than
+  // three steps of 16 waves (that launch costs the host 3 us too): into many small ones without
+  // alternatives (one row of 151936 bf16 7.1 us, 16 uncut), into fewer with them, whose lists
+  // take longer to join (17 with waves in sixteens, 24 uncut; 32 rows 18 and 26).  From 128
+  // rows on (20.5 us and 29) uncut rows fill the chip, from 1024 on with four waves each.
+  const int64_t N = s->N < 1 ? 1 : s->N, step = 16 * 64 * VECS * w;
+  const bool cut = N < 128 && s->V > 3 * step;
+  p.waves = (cut && !s->top) || N >= 1024 ? 4 : 16;
   p.batch = (int64_t)p.waves * 64 * VECS * w;
   p.batches = cdiv(s->V, p.batch);
   p.parts = 1;
-  if (s->N < 128 && p.batches > 4) {
-    const int64_t most = cdiv(256, s->N < 1 ? 1 : s->N), by = cdiv(p.batches, 2);
+  if (cut && p.batches > 2) {
+    const int64_t most = p.waves == 4 ? cdiv(1024, N) : 256 / N, by = cdiv(p.batches, 2);
     p.parts = (int)(most < by ? most : by);
     if (p.parts > 64) p.parts = 64;
   }

@@ -26,6 +26,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------ rows to codes
+constexpr int64_t FEW = 8 * sv_mx4_host::CUS * 1024;     // items (lanes' shares) that take a thread each
+
 // Eight elements of a row: a lane's share.  Four lanes hold a block.
 template <int DT> __device__ __forceinline__ void load8(const char *row, int64_t k, int64_t H, float (&v)[8]) {
   if (k + 8 <= H) {
@@ -107,6 +109,12 @@ __device__ __forceinline__ int64_t held_scale(int64_t block, int64_t row, int64_
   return ((block / 16 * 4 + block % 4) * N + row) * 4 + block / 4 % 4;
 }
 
+// TILED: the scales of a row's 16 blocks are four words, blocks 4 k + q, k = 0 .. 3, in lane 16 q +
+// row % 16's; a lane's words of four times 16 rows lie together.
+__device__ __forceinline__ int64_t tiled_scale(int64_t row, int64_t group, int64_t lane, int64_t groups) {
+  return ((row / 64 * groups + group) * 64 + lane) * 4 + row / 16 % 4;
+}
+
 template <int FORM>
 __device__ __forceinline__ void put(const Out &o, int64_t row, int64_t g, uint32_t c, uint32_t e) {
   if constexpr (FORM == ROWS_OUT) {
@@ -121,7 +129,7 @@ __device__ __forceinline__ void put(const Out &o, int64_t row, int64_t g, uint32
   } else {
     const int64_t b = g / 4;
     *(uint32_t *)(o.codes + row * o.c_ld + 4 * g) = c;
-    if (g % 4 == 0) o.scale[((row / 16 * o.groups + b / 16) * 64 + b % 4 * 16 + row % 16) * 4 + b / 4 % 4] = (uint8_t)e;
+    if (g % 4 == 0) o.scale[tiled_scale(row, b / 16, b % 4 * 16 + row % 16, o.groups) * 4 + b / 4 % 4] = (uint8_t)e;
   }
 }
 
@@ -160,13 +168,14 @@ template <int SRC> __device__ __forceinline__ uint32_t take(const Rows &R, int64
   }
 }
 
-// Lanes over all rows' items, four a thread.  HBM bound.
-template <int SRC, int FORM> __global__ __launch_bounds__(256) void rows_kernel(Rows R, Out O) {
-  const int64_t first = (int64_t)blockIdx.x * 1024;
+// Lanes over all rows' items, PER a thread.  HBM bound: 151936 rows of 4096 bf16 265 us (1.58 GB),
+// one a thread 310; 4999 of 1111 fp32 8.1 us with one, 9.4 with four.
+template <int SRC, int FORM, int PER> __global__ __launch_bounds__(256) void rows_kernel(Rows R, Out O) {
+  const int64_t first = (int64_t)blockIdx.x * (256 * PER);
   const int64_t row0 = first / R.lanes;
   const int rest = (int)(first - row0 * R.lanes);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < PER; ++s) {
     const int64_t i = first + s * 256 + threadIdx.x;
     if (i >= R.items) return;            // (whole blocks: items are)
     const int at = rest + s * 256 + (int)threadIdx.x, r = at / R.lanes;
@@ -178,20 +187,27 @@ template <int SRC, int FORM> __global__ __launch_bounds__(256) void rows_kernel(
 
 template <int FORM> void launch_rows(int src, Rows R, Out O, int64_t rows, hipStream_t st) {
   R.items = rows * R.lanes;
-  const dim3 grid((unsigned)cdiv(R.items, 1024)), block(256);
-  if (src == SV_BF16) hipLaunchKernelGGL((rows_kernel<SV_BF16, FORM>), grid, block, 0, st, R, O);
-  else if (src == SV_F32) hipLaunchKernelGGL((rows_kernel<SV_F32, FORM>), grid, block, 0, st, R, O);
-  else if constexpr (FORM != ROWS_OUT) hipLaunchKernelGGL((rows_kernel<SV_MX4, FORM>), grid, block, 0, st, R, O);
+  const bool few = R.items < FEW;
+  const dim3 grid((unsigned)cdiv(R.items, few ? 256 : 1024)), block(256);
+  auto go = [&](auto S) {
+    constexpr int SRC = decltype(S)::value;
+    if (few) hipLaunchKernelGGL((rows_kernel<SRC, FORM, 1>), grid, block, 0, st, R, O);
+    else hipLaunchKernelGGL((rows_kernel<SRC, FORM, 4>), grid, block, 0, st, R, O);
+  };
+  if (src == SV_BF16) go(std::integral_constant<int, SV_BF16>());
+  else if (src == SV_F32) go(std::integral_constant<int, SV_F32>());
+  else if constexpr (FORM != ROWS_OUT) go(std::integral_constant<int, SV_MX4>());
 }
 
 // ------------------------------------------------------------------ codes to rows
-template <int DT> __global__ __launch_bounds__(256) void unpack_kernel(Rows R, char *y) {
-  const int64_t first = (int64_t)blockIdx.x * 1024;
+// HBM bound as well: 151936 rows of 4096 into bf16 300 us (1.58 GB).
+template <int DT, int PER> __global__ __launch_bounds__(256) void unpack_kernel(Rows R, char *y) {
+  const int64_t first = (int64_t)blockIdx.x * (256 * PER);
   const int64_t row0 = first / R.lanes;
   const int rest = (int)(first - row0 * R.lanes);
   constexpr int E = DT == SV_BF16 ? 2 : 4;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < PER; ++s) {
     const int64_t i = first + s * 256 + threadIdx.x;
     if (i >= R.items) return;
     const int at = rest + s * 256 + (int)threadIdx.x, r = at / R.lanes;
@@ -287,7 +303,7 @@ struct Chunk {
 // Few rows: each workgroup holds all of their codes in LDS, and each of its waves streams
 // 16 vocabulary rows at a time from memory to registers, a chunk ahead, with no barrier.
 // Bound by reading the head.
-template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void held_kernel(LogitsP P) {
+template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * WAVES, FM > 4 ? 2 : 4) void held_kernel(LogitsP P) {
   extern __shared__ __align__(16) uint8_t held[];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
   const int nc = (P.nks + 7) / 8, nb = (P.H + 31) / 32, bytes = (P.H + 1) / 2;
@@ -301,7 +317,7 @@ template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * 
     const int at = c * 512 + q * 16;
     if ((c + 1) * 512 <= bytes) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) t.w[k] = __builtin_nontemporal_load((const u32x4_any *)(w + at + k * 64));
+      for (int k = 0; k < 8; ++k) t.w[k] = *(const u32x4_any *)(w + at + k * 64);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -415,8 +431,7 @@ template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * 
   }
 }
 
-// The weight's scales as the lanes of the tiled product take them: lane l of 16 rows and 16
-// blocks has row l & 15 and blocks 4 k + (l >> 4), k = 0 .. 3, in one word.  A thread takes
+// The weight's scales as the lanes of the tiled product take them (tiled_scale).  A thread takes
 // the 16 scales of a row: it turns four words of four blocks into four of every fourth.  0
 // past the rows' end (codes of the hidden rows are 0 there; what lies in memory might stand
 // for NaN).
@@ -424,8 +439,9 @@ __global__ __launch_bounds__(256) void scales_kernel(const uint8_t *s, int64_t l
                                                      int64_t items, uint32_t *o) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= items) return;
-  const int64_t at = i >> 4, tile = at / groups, row = tile * 16 + (threadIdx.x & 15);
-  const int b = (int)(at - tile * groups) * 16;
+  // (neighbouring threads: rows of 64, which write together)
+  const int64_t at = i >> 6, tile = at / groups, group = at - tile * groups, row = tile * 64 + (threadIdx.x & 63);
+  const int b = (int)group * 16;
   u32x4 v = 0;
   if (row < V) {
     const uint8_t *p = s + row * ld + b;
@@ -437,13 +453,13 @@ __global__ __launch_bounds__(256) void scales_kernel(const uint8_t *s, int64_t l
         if (b + k < nb) v[k / 4] |= (uint32_t)p[k] << (k % 4 * 8);
     }
   }
-  o += at * 64 + (threadIdx.x & 15);
+  o += tiled_scale(row, group, row & 15, groups);
   const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x05010400), hi = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
   const uint32_t lo2 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602), hi2 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
   o[0] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
-  o[16] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-  o[32] = __builtin_amdgcn_perm(hi2, lo2, 0x05040100);
-  o[48] = __builtin_amdgcn_perm(hi2, lo2, 0x07060302);
+  o[64] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+  o[128] = __builtin_amdgcn_perm(hi2, lo2, 0x05040100);
+  o[192] = __builtin_amdgcn_perm(hi2, lo2, 0x07060302);
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
@@ -459,7 +475,7 @@ __global__ __launch_bounds__(256) void scales_kernel(const uint8_t *s, int64_t l
                "v_mfma_scale_f32_16x16x128_f8f6f4 %3, %7, %8, %3, %12, %13 " SEL " cbsz:4 blgp:4"      \
                : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                      \
                : "v"(y[0]), "v"(y[1]), "v"(y[2]), "v"(y[3]), "v"(x), "v"(sy[0]), "v"(sy[1]), "v"(sy[2]), "v"(sy[3]), "v"(sx))
-template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, const uint32_t *sy, u32x4 x, uint32_t sx) {
+template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, u32x4 sy, u32x4 x, uint32_t sx) {
   if constexpr (K == 0) SV_MUL4("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
   else if constexpr (K == 1) SV_MUL4("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
   else if constexpr (K == 2) SV_MUL4("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
@@ -484,7 +500,7 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
 #ifdef __HIP_DEVICE_COMPILE__
   typedef Side<SV_I8, T::BM, T::FM, T::NW, ROWS> SX;
   typedef Side<SV_I8, T::BN, T::FN, T::NW, ROWS> SY;
-  static_assert(T::FN % 4 == 0 && T::FN <= T::FM, "products in fours, weight reads beside hidden ones");
+  static_assert(T::FM % 4 == 0 && T::FN % 4 == 0 && T::FN <= T::FM, "products in fours, weight reads beside hidden ones");
   constexpr int LD = SX::NL + SY::NL, PER = (LD + T::FM - 1) / T::FM;   // loads of a step, beside a fragment's products
   constexpr int STORES = T::FM * T::FN / (OT == SV_BF16 ? 2 : 1);       // of a wave's whole tile
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -492,7 +508,7 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
   const int total = P.mt * P.nt, pairs = P.groups, nk = 2 * pairs;
   SX sx;
   SY sy;
-  const uint32_t *xs, *ws;
+  const u32x4 *xs, *ws;
   int m0, n0, from;
   // the loads' tile
   auto start = [&](int id) {
@@ -505,11 +521,11 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
     const Part Y = {(const char *)P.w + (int64_t)n0 * P.w_ld, P.w_ld, P.V - n0 < T::BN ? P.V - n0 : T::BN, P.w_bytes};
     sx.start(X, 0, nk, 2 * from);
     sy.start(Y, 0, nk, 2 * from);
-    xs = (const uint32_t *)P.xs + (int64_t)(m0 / 16 + gx) * pairs * 64 + lane;
-    ws = (const uint32_t *)P.ws + (int64_t)(n0 / 16 + gy) * pairs * 64 + lane;
+    xs = (const u32x4 *)P.xs + (int64_t)(m0 / 64 + gx / 4) * pairs * 64 + lane;
+    ws = (const u32x4 *)P.ws + (int64_t)(n0 / 64 + gy / 4) * pairs * 64 + lane;
   };
   u32x4 x[T::FM], y0[T::FN], y1[T::FN];
-  uint32_t sa[T::FM], sb[T::FN], sa2[T::FM], sb2[T::FN];
+  u32x4 sa[T::FM / 4], sb[T::FN / 4], sa2[T::FM / 4], sb2[T::FN / 4];   // a word a fragment
   f32x4 acc[T::FM][T::FN];
   clear<SV_BF16, T>(acc);
   // this wave's first fragments in a buffer at half step 0 and 1
@@ -534,7 +550,7 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
 #pragma unroll
     for (int f = 0; f < T::FM; ++f) {
 #pragma unroll
-      for (int g = 0; g < T::FN; g += 4) mul4<decltype(K)::value>(&acc[f][g], &y[g], &sb[g], x[f], sa[f]);
+      for (int g = 0; g < T::FN; g += 4) mul4<decltype(K)::value>(&acc[f][g], &y[g], sb[g / 4], x[f], sa[f / 4][f % 4]);
       x[f] = *(const u32x4 *)(xb + f * 16 * STEP);
       if (f < T::FN) yn[f] = *(const u32x4 *)(yb + f * 16 * STEP);
       if constexpr (decltype(loads)::value) {
@@ -545,8 +561,8 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
         }
       }
       if constexpr (decltype(scales)::value) {
-        sa2[f] = xs[(f * pairs + from) * 64];
-        if (f < T::FN) sb2[f] = ws[(f * pairs + from) * 64];
+        if (f < T::FM / 4) sa2[f] = xs[(f * pairs + from) * 64];
+        if (f < T::FN / 4) sb2[f] = ws[(f * pairs + from) * 64];
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -560,9 +576,9 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
   int id = blockIdx.x;
   start(id);
 #pragma unroll
-  for (int f = 0; f < T::FM; ++f) sa[f] = xs[(f * pairs + from) * 64];
+  for (int f = 0; f < T::FM / 4; ++f) sa[f] = xs[(f * pairs + from) * 64];
 #pragma unroll
-  for (int f = 0; f < T::FN; ++f) sb[f] = ws[(f * pairs + from) * 64];
+  for (int f = 0; f < T::FN / 4; ++f) sb[f] = ws[(f * pairs + from) * 64];
   sx.issue(x0b, true, nk);
   sy.issue(y0b, true, nk);
   sx.issue(x1b, true, nk);
@@ -598,9 +614,9 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
       // (within the loop: it may move sums right behind it)
       if (last) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-      for (int f = 0; f < T::FM; ++f) sa[f] = sa2[f];
+      for (int f = 0; f < T::FM / 4; ++f) sa[f] = sa2[f];
 #pragma unroll
-      for (int f = 0; f < T::FN; ++f) sb[f] = sb2[f];
+      for (int f = 0; f < T::FN / 4; ++f) sb[f] = sb2[f];
     }
     stored = m1 + T::BM <= P.N && n1 + T::BN <= P.V;
 #pragma unroll
@@ -635,9 +651,8 @@ template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel
 #endif
 }
 
-template <int FM, int SRC, int OT> void launch_held(const LogitsP &P, int64_t lds, hipStream_t st) {
-  constexpr int WAVES = 8;
-  const int64_t by = cdiv(P.groups, WAVES), most = sv_mx4_host::CUS * 2;
+template <int FM, int SRC, int OT, int WAVES> void launch_held(const LogitsP &P, int64_t lds, hipStream_t st) {
+  const int64_t by = cdiv(P.groups, WAVES), most = sv_mx4_host::CUS * (2 * lds <= sv_mx4_host::LDS_ROWS ? 2 : 1);
   // (more than 64 KB of LDS has to be asked for, once on each device)
   static std::atomic<uint64_t> asked{0};
   int dev = 0;
@@ -649,16 +664,9 @@ template <int FM, int SRC, int OT> void launch_held(const LogitsP &P, int64_t ld
   hipLaunchKernelGGL((held_kernel<FM, SRC, OT, WAVES>), dim3((unsigned)(by < most ? by : most)), dim3(64 * WAVES),
                      (unsigned)lds, st, P);
 }
-template <int FM> void launch_held(const LogitsP &P, int src, int ot, int64_t lds, hipStream_t st) {
-  if (ot == SV_BF16) {
-    if (src == SV_MX4) launch_held<FM, SV_MX4, SV_BF16>(P, lds, st);
-    else if (src == SV_BF16) launch_held<FM, SV_BF16, SV_BF16>(P, lds, st);
-    else launch_held<FM, SV_F32, SV_BF16>(P, lds, st);
-  } else {
-    if (src == SV_MX4) launch_held<FM, SV_MX4, SV_F32>(P, lds, st);
-    else if (src == SV_BF16) launch_held<FM, SV_BF16, SV_F32>(P, lds, st);
-    else launch_held<FM, SV_F32, SV_F32>(P, lds, st);
-  }
+template <int FM, int SRC, int WAVES = 8> void launch_held(const LogitsP &P, int ot, int64_t lds, hipStream_t st) {
+  if (ot == SV_BF16) launch_held<FM, SRC, SV_BF16, WAVES>(P, lds, st);
+  else launch_held<FM, SRC, SV_F32, WAVES>(P, lds, st);
 }
 
 template <class T> void launch_tiles(LogitsP P, int ot, hipStream_t st) {
@@ -703,9 +711,16 @@ extern "C" int sv_mx4_unpack(int32_t N, int32_t H, const uint8_t *codes, int64_t
   for (int64_t n = 0; n < N; n += most) {
     const int64_t rows = N - n < most ? N - n : most;
     R.items = rows * R.lanes;
-    const dim3 grid((unsigned)cdiv(R.items, 1024)), block(256);
-    if (y_dtype == SV_BF16) hipLaunchKernelGGL((unpack_kernel<SV_BF16>), grid, block, 0, (hipStream_t)stream, R, o);
-    else hipLaunchKernelGGL((unpack_kernel<SV_F32>), grid, block, 0, (hipStream_t)stream, R, o);
+    const bool few = R.items < FEW;
+    const dim3 grid((unsigned)cdiv(R.items, few ? 256 : 1024)), block(256);
+    const hipStream_t st = (hipStream_t)stream;
+    if (y_dtype == SV_BF16) {
+      if (few) hipLaunchKernelGGL((unpack_kernel<SV_BF16, 1>), grid, block, 0, st, R, o);
+      else hipLaunchKernelGGL((unpack_kernel<SV_BF16, 4>), grid, block, 0, st, R, o);
+    } else {
+      if (few) hipLaunchKernelGGL((unpack_kernel<SV_F32, 1>), grid, block, 0, st, R, o);
+      else hipLaunchKernelGGL((unpack_kernel<SV_F32, 4>), grid, block, 0, st, R, o);
+    }
     R.x += rows * R.x_ld;
     R.scale += rows * R.s_ld;
     o += rows * H * esize(y_dtype);
@@ -754,10 +769,21 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
       R.lanes = (int32_t)(L.nks * 16);
       launch_rows<HELD>(s.hidden_dtype, R, Out{ws + L.codes, ws + L.scales, 0, 0, s.N, 0, 0}, s.N, st);
     }
-    const int src = L.fused ? s.hidden_dtype : SV_MX4;
-    if (L.frags == 1) launch_held<1>(P, src, s.out_dtype, held_bytes(s.N, s.H), st);
-    else if (L.frags == 2) launch_held<2>(P, src, s.out_dtype, held_bytes(s.N, s.H), st);
-    else launch_held<4>(P, src, s.out_dtype, held_bytes(s.N, s.H), st);
+    const int64_t lds = held_bytes(s.N, s.H);
+    if (L.fused) {                       // (16 rows at most)
+      if (s.hidden_dtype == SV_BF16) launch_held<1, SV_BF16>(P, s.out_dtype, lds, st);
+      else launch_held<1, SV_F32>(P, s.out_dtype, lds, st);
+    } else {
+      switch (L.frags) {
+        case 1: launch_held<1, SV_MX4>(P, s.out_dtype, lds, st); break;
+        case 2: launch_held<2, SV_MX4>(P, s.out_dtype, lds, st); break;
+        case 3: launch_held<3, SV_MX4>(P, s.out_dtype, lds, st); break;
+        case 4: launch_held<4, SV_MX4>(P, s.out_dtype, lds, st); break;
+        case 5: launch_held<5, SV_MX4>(P, s.out_dtype, lds, st); break;
+        case 6: launch_held<6, SV_MX4>(P, s.out_dtype, lds, st); break;
+        default: launch_held<8, SV_MX4>(P, s.out_dtype, lds, st);
+      }
+    }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
   }
   {

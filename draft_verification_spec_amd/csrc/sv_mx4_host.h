@@ -21,7 +21,7 @@ using sv_head_host::up;
 
 constexpr int BLOCK = SV_MX4_BLOCK;
 constexpr int SPAN = 256;                // bytes of k of the tiled product's unrolled pair of steps
-constexpr int64_t LDS_ROWS = 144 << 10;  // bytes of hidden rows that a workgroup may hold
+constexpr int64_t LDS_ROWS = 160 << 10;  // bytes of hidden rows that a workgroup may hold
 
 inline int64_t code_bytes(int64_t H) { return cdiv(H, 2); }
 inline int64_t blocks(int64_t H) { return cdiv(H, BLOCK); }
@@ -81,9 +81,11 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
   Plan p = {};
   const int64_t N = s->N, H = s->H;
   p.nks = cdiv(H, 128);
-  p.held = N <= 64 && held_bytes(N, H) <= LDS_ROWS;
-  p.frags = N <= 16 ? 1 : N <= 32 ? 2 : 4;
-  p.fused = p.held && s->hidden_dtype != SV_MX4 && N * H <= 16384;
+  p.held = N <= 128 && held_bytes(N, H) <= LDS_ROWS;
+  p.frags = (int)cdiv(N, 16);
+  if (p.frags == 0) p.frags = 1;
+  if (p.frags == 7) p.frags = 8;
+  p.fused = p.held && s->hidden_dtype != SV_MX4 && N <= 16 && N * H <= 16384;
   p.Kp = up(code_bytes(H), SPAN);
   p.groups = p.Kp / SPAN;
   p.large = sv_head_host::large_tiles(N, s->V);

@@ -136,7 +136,7 @@ int main() {
     NEED(p.waves == 4 || p.waves == 16);
     NEED(p.batch == (int64_t)p.waves * 64 * VECS * (dt == SV_F32 ? 4 : 8));
     NEED(p.batches * p.batch >= V && (p.batches - 1) * p.batch < V);
-    NEED(p.parts >= 1 && p.parts <= 64 && p.parts <= p.batches);
+    NEED(p.parts >= 1 && p.parts <= 64 && p.parts <= p.batches && (p.parts == 1 || N < 128));
     NEED((int64_t)(N ? N : 1) * p.parts * 64 * p.waves <= 0xffffffffLL);
     if (p.parts > 1) {
       NEED(p.keys % 256 == 0 && p.keys >= (size_t)N * p.parts * 24);

@@ -132,10 +132,10 @@ int main() {
     const Plan p = plan_for(&s);
     if (p.held) {
       // a workgroup's hidden rows fit its LDS, in whole 16-byte pieces
-      NEED(N <= 16 * p.frags && (p.frags == 1 || p.frags == 2 || p.frags == 4));
+      NEED(N <= 16 * p.frags && p.frags >= 1 && p.frags <= 8 && p.frags != 7);
       NEED(held_bytes(N, H) <= LDS_ROWS && p.image + p.x_scales == held_bytes(N, H) && p.image % 16 == 0 && p.x_scales % 16 == 0);
       NEED(p.nks * 128 >= H && (p.nks - 1) * 128 < H);
-      NEED(!p.fused || (hd != SV_MX4 && p.total == 0));
+      NEED(!p.fused || (hd != SV_MX4 && p.total == 0 && p.frags == 1));
       if (!p.fused && N) NEED(p.scales - p.codes >= (size_t)p.image && p.total - p.scales >= (size_t)p.x_scales);
     } else {
       NEED(p.Kp % SPAN == 0 && 2 * p.Kp >= H && p.groups * SPAN == p.Kp && p.groups * 16 * BLOCK >= H);
