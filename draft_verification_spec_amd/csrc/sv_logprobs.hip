@@ -10,8 +10,9 @@
 //
 // Alternatives: a wave keeps the `top` best keys it has seen, a key holding value and
 // index so that larger is better and no two are equal.  A vector of logits costs one
-// comparison of its maximum, which the softmax needs anyway, with the worst kept; what
-// passes goes to a buffer in LDS, and a full buffer is sorted into the list.
+// comparison of its maximum, which the softmax needs anyway, with a border that at least
+// `top` entries reach; what passes goes to a buffer in LDS, and a full buffer is sorted into
+// the list, whose last key is the next border.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -124,18 +125,18 @@ __device__ __forceinline__ Key merge_lists(Key k) {
   return k;
 }
 
-// The best keys that a wave has seen: lanes 0 .. 31 hold them in descending order.
+// The best keys that a wave has seen: lanes 0 .. 31 hold them in descending order, beside what
+// has come since in a buffer.  Entries come in the order of their indices, so of equal ones
+// those that came first stay.
 struct Best {
   Key list;
-  Key worst;                             // the top-th of them: better ones are taken
-  float border;                          // its value
+  float border;                          // larger values are taken (at first those above -inf)
   int count;                             // keys in the buffer
   bool sorted;                           // whether any are in the list
   Key *buffer;                           // LIST keys in LDS, the wave's own
 
   __device__ __forceinline__ void start(Key *b) {
     list = 0;
-    worst = key_of(NEG_INF, 0);          // an entry of -inf is none
     border = NEG_INF;
     count = 0;
     sorted = false;
@@ -149,35 +150,29 @@ struct Best {
     list = sort_wave(k);
     count = 0;
     sorted = true;
-    const Key w = __shfl(list, top - 1);
-    if (w > worst) {
-      worst = w;
-      border = value_of(w);
-    }
+    const Key w = __shfl(list, top - 1); // the top-th best
+    if (w) border = fmax_nan(border, value_of(w));
   }
   // one entry of each lane
   __device__ __forceinline__ void offer(float v, uint32_t index, int top) {
-    if (!__ballot(v >= border)) return;
-    Key k = v >= border ? key_of(v, index) : 0;
-    uint64_t who = __ballot(k > worst);
+    uint64_t who = __ballot(v > border);
     while (who) {
       const int lane = threadIdx.x & 63, room = LIST - count;
-      const int place = __popcll(who & (((Key)1 << lane) - 1));
+      const int place = __popcll(who & (((Key)1 << lane) - 1)), n = __popcll(who);
       const bool mine = who >> lane & 1;
-      if (mine && place < room) buffer[count + place] = k;
-      const int n = __popcll(who);
+      if (mine && place < room) buffer[count + place] = key_of(v, index);
       count += n < room ? n : room;
       if (n <= room) break;
       flush(top);
-      who = __ballot(mine && place >= room && k > worst);
+      who = __ballot(mine && place >= room && v > border);
     }
   }
 };
 
-// The first border: of 64 groups of lanes (WAVES lanes each) the top-th largest maximum, cut to
-// 16 bits, so that at least `top` entries reach it and few others do (of random rows 24 for 20,
-// 44 for 32).  groups: 64 words in LDS, and one for the result.
-template <int WAVES> __device__ __forceinline__ void first_border(Best &b, float most, int top, uint32_t *groups) {
+// A border from the lanes' maxima so far: of 64 groups of lanes (WAVES lanes each) the top-th
+// largest maximum, cut to 16 bits, so that at least `top` entries reach it and few others do (of
+// random rows 24 for 20, 44 for 32).  groups: 64 words in LDS, and one for the result.
+template <int WAVES> __device__ __forceinline__ void raise_border(Best &b, float most, int top, uint32_t *groups) {
   static_assert(WAVES == 4 || WAVES == 16, "groups within a row of lanes");
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   uint32_t u = most > NEG_INF ? order_of(most) : 0;
@@ -202,10 +197,8 @@ template <int WAVES> __device__ __forceinline__ void first_border(Best &b, float
   }
   __syncthreads();
   const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)groups[64]);
-  if (at > order_of(NEG_INF)) {
-    b.worst = ((Key)at << 32) - 1;
-    b.border = value_of((Key)at << 32);
-  }
+  // the value below it (below 0 that is no zero)
+  if (at > order_of(NEG_INF)) b.border = fmax_nan(b.border, value_of((Key)(at - (at == 0x80000000u ? 2 : 1)) << 32));
 }
 
 // A thread's vectors of one step: entries at `at` + s * 64 * waves * W; past `end` -inf.
@@ -320,11 +313,15 @@ __device__ __forceinline__ Key join_best(Best &best, Key (*lists)[LIST], int32_t
   if (total <= FEW) {
     if (lane < best.count) all[before + lane] = lists[wid][lane];
     if (tid < LIST) all[FEW + tid] = 0;
+    if (tid < 8 && total + tid < FEW) all[total + tid] = 0;
     __syncthreads();
     if (tid < total) {
       const Key k = all[tid];
       int place = 0;
-      for (int j = 0; j < total; ++j) place += all[j] > k;
+      for (int j = 0; j < total; j += 8) {   // (eight reads under way together; zeros behind the last)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) place += all[j + i] > k;
+      }
       if (place < LIST) all[FEW + place] = k;
     }
     __syncthreads();
@@ -421,25 +418,18 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(LogprobsP P) {
       t.a += (double)a1;
     }
     if constexpr (TOP) {
-      if (b == b0) first_border<WAVES>(best, most, P.top, groups);
-      // few lanes' vectors have an entry to take: each of those is spread over the lanes
-      uint64_t who[VECS], some = 0;
+      // (again after 2, 4, 8 .. steps: 256 rows of 151936 fp32 with twenty alternatives 40.6 us to
+      // 36.0, without any 27.9)
+      if (((b - b0) & (b - b0 + 1)) == 0) raise_border<WAVES>(best, m, P.top, groups);
 #pragma unroll
-      for (int s = 0; s < VECS; ++s) some |= who[s] = __ballot(b == b0 ? top[s] >= best.border : top[s] > best.border);
-#pragma unroll 1
-      for (int s = 0; some && s < VECS; ++s) {
-        u32x4 v = r[0];
-        uint64_t w = who[0];
-#pragma unroll
-        for (int j = 1; j < VECS; ++j)
-          if (s == j) {
-            v = r[j];
-            w = who[j];
-          }
-        while (w) {
-          const int l = __builtin_ctzll(w);
-          w &= w - 1;
-          const uint32_t u0 = readlane(v[0], l), u1 = readlane(v[1], l), u2 = readlane(v[2], l), u3 = readlane(v[3], l);
+      for (int s = 0; s < VECS; ++s) {
+        // few lanes' vectors have an entry to take: each of those is spread over the lanes
+        uint64_t who = __ballot(top[s] > best.border);
+        while (who) {
+          const int l = __builtin_ctzll(who);
+          who &= who - 1;
+          const uint32_t u0 = readlane(r[s][0], l), u1 = readlane(r[s][1], l), u2 = readlane(r[s][2], l),
+                         u3 = readlane(r[s][3], l);
           const int q = DT == SV_BF16 ? lane >> 1 : lane;
           uint32_t u = q & 2 ? (q & 1 ? u3 : u2) : (q & 1 ? u1 : u0);
           if constexpr (DT == SV_BF16) u = lane & 1 ? u & 0xffff0000u : u << 16;
