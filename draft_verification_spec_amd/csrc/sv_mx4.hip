@@ -432,34 +432,39 @@ template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * 
 }
 
 // The weight's scales as the lanes of the tiled product take them (tiled_scale).  A thread takes
-// the 16 scales of a row: it turns four words of four blocks into four of every fourth.  0
-// past the rows' end (codes of the hidden rows are 0 there; what lies in memory might stand
-// for NaN).
+// 16 scales of four rows 16 apart: it turns four words of four blocks into four of every
+// fourth, and stores those of the four rows together (151936 rows of 128: a row a thread 13 us,
+// this 11).  0 past the rows' end (codes of the hidden rows are 0 there; what lies in
+// memory might stand for NaN).
 __global__ __launch_bounds__(256) void scales_kernel(const uint8_t *s, int64_t ld, int64_t V, int nb, int groups,
-                                                     int64_t items, uint32_t *o) {
+                                                     int64_t items, u32x4 *o) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= items) return;
-  // (neighbouring threads: rows of 64, which write together)
-  const int64_t at = i >> 6, tile = at / groups, group = at - tile * groups, row = tile * 64 + (threadIdx.x & 63);
-  const int b = (int)group * 16;
-  u32x4 v = 0;
-  if (row < V) {
-    const uint8_t *p = s + row * ld + b;
-    if (b + 16 <= nb) {
-      v = *(const u32x4_any *)p;
-    } else {
+  const int64_t rest = i / groups, row = rest / 16 * 64 + rest % 16;   // neighbours: groups of a row
+  const int group = (int)(i - rest * groups), b = group * 16;
+  u32x4 w[4];                            // w[q][f]: blocks 4 k + q of row 16 f
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (b + k < nb) v[k / 4] |= (uint32_t)p[k] << (k % 4 * 8);
+  for (int f = 0; f < 4; ++f) {
+    u32x4 v = 0;
+    if (row + 16 * f < V) {
+      const uint8_t *p = s + (row + 16 * f) * ld + b;
+      if (b + 16 <= nb) {
+        v = *(const u32x4_any *)p;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (b + k < nb) v[k / 4] |= (uint32_t)p[k] << (k % 4 * 8);
+      }
     }
+    const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x05010400), hi = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
+    const uint32_t lo2 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602), hi2 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
+    w[0][f] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+    w[1][f] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+    w[2][f] = __builtin_amdgcn_perm(hi2, lo2, 0x05040100);
+    w[3][f] = __builtin_amdgcn_perm(hi2, lo2, 0x07060302);
   }
-  o += tiled_scale(row, group, row & 15, groups);
-  const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x05010400), hi = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
-  const uint32_t lo2 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602), hi2 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
-  o[0] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
-  o[64] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-  o[128] = __builtin_amdgcn_perm(hi2, lo2, 0x05040100);
-  o[192] = __builtin_amdgcn_perm(hi2, lo2, 0x07060302);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[tiled_scale(row, group, 16 * q + row % 16, groups) / 4] = w[q];
 }
 
 #ifdef __HIP_DEVICE_COMPILE__
@@ -818,9 +823,9 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
       P.w_ld = L.x_ld;
       P.w_bytes = L.Kp;
     }
-    const int64_t items = up(P.V, 256) * L.groups;
+    const int64_t items = up(P.V, 256) / 4 * L.groups;
     hipLaunchKernelGGL(scales_kernel, dim3((unsigned)cdiv(items, 256)), dim3(256), 0, st, weight_scale + v0 * s_ld, s_ld,
-                       (int64_t)P.V, (int)blocks(s.H), (int)L.groups, items, (uint32_t *)(ws + L.wscale));
+                       (int64_t)P.V, (int)blocks(s.H), (int)L.groups, items, (u32x4 *)(ws + L.wscale));
     P.ws = ws + L.wscale;
     P.out = (char *)logits + v0 * oe;
     if (L.large) launch_tiles<Tile<8, 8, 2, 2, 2, 2>>(P, s.out_dtype, st);
