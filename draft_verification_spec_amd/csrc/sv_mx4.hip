@@ -301,8 +301,11 @@ struct Chunk {
 };
 
 // Few rows: each workgroup holds all of their codes in LDS, and each of its waves streams
-// 16 vocabulary rows at a time from memory to registers, a chunk ahead, with no barrier.
-// Bound by reading the head.
+// 16 vocabulary rows at a time from memory to registers, a chunk ahead, with no barrier;
+// rows lie at any address and distance.  Bound by reading the head: 32 rows of 4096 x 151936
+// 70 us (330 MB, 4.9 TB/s with the logits), 64 79, 128 of 2048 50; against tiles of 128 x 128,
+// with the scales that those have turned first, 90, 90 and 53.  Loads past the cache
+// (nontemporal) fetch each line's halves apart: 76 us for the 32 rows.
 template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * WAVES, FM > 4 ? 2 : 4) void held_kernel(LogitsP P) {
   extern __shared__ __align__(16) uint8_t held[];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
@@ -355,7 +358,16 @@ template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * 
   // the hidden rows
   if constexpr (SRC == SV_MX4) {
     const int n = (int)(N * P.nks * 4), m = (int)(N * ((P.nks + 3) / 4));
-    for (int j = tid; j < n; j += 64 * WAVES) ((u32x4 *)held)[j] = ((const u32x4 *)P.xc)[j];
+    // (eight loads under way together: 128 rows of 2048 x 151936 54 to 50 us)
+    for (int j = tid; j < n; j += 8 * 64 * WAVES) {
+      u32x4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i * 64 * WAVES < n) v[i] = ((const u32x4 *)P.xc)[j + i * 64 * WAVES];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i * 64 * WAVES < n) ((u32x4 *)held)[j + i * 64 * WAVES] = v[i];
+    }
     for (int j = tid; j < m; j += 64 * WAVES) ((u32x4 *)scales)[j] = ((const u32x4 *)P.xs)[j];
   } else {
     const Out o = {held, scales, 0, 0, N, 0, 0};
@@ -497,9 +509,13 @@ template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, 
 // buffers, which later loads may overwrite, and the next step's tiles have landed.
 //
 // A workgroup takes one tile after another, and its loads run on into the next: a tile's
-// results leave while the next one's first steps come in (1024 rows of 4096 x 151936 398 us
-// with a workgroup a tile).  Rows a power of two apart lie on few memory channels at any one
-// step, so neighbouring tiles of the vocabulary begin at different pairs.
+// results leave while the next one's first steps come in (1024 rows of 512 x 65536 54 to 45
+// us, of 4096 x 151936 398 to 379).  Rows a power of two apart lie on few memory channels at
+// any one step, so neighbouring tiles of the vocabulary begin at different pairs.
+//
+// 1024 rows of 4096 x 151936 take 375 us, 3.4 PFLOP/s: the main loop runs at 4.6, without its
+// loads it would at 6.1 (the instruction's own rate is 9 at the clock it runs at).  A third
+// buffer of the weight changed nothing, tiles of 128 x 128 take a quarter longer.
 template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel(LogitsP P) {
   __shared__ __align__(16) char lds[2 * (T::XBUF + T::YBUF)];
 #ifdef __HIP_DEVICE_COMPILE__
