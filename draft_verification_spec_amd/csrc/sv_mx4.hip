@@ -303,9 +303,8 @@ struct Chunk {
 // Few rows: each workgroup holds all of their codes in LDS, and each of its waves streams
 // 16 vocabulary rows at a time from memory to registers, a chunk ahead, with no barrier;
 // rows lie at any address and distance.  Bound by reading the head: 32 rows of 4096 x 151936
-// 70 us (330 MB, 4.9 TB/s with the logits), 64 79, 128 of 2048 50; against tiles of 128 x 128,
-// with the scales that those have turned first, 90, 90 and 53.  Loads past the cache
-// (nontemporal) fetch each line's halves apart: 76 us for the 32 rows.
+// 70 us (330 MB, 4.9 TB/s with the logits), 64 79.  Loads past the cache (nontemporal) fetch
+// each line's halves apart: 76 us for the 32 rows.
 template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * WAVES, FM > 4 ? 2 : 4) void held_kernel(LogitsP P) {
   extern __shared__ __align__(16) uint8_t held[];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;

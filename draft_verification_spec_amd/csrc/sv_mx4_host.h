@@ -81,7 +81,14 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
   Plan p = {};
   const int64_t N = s->N, H = s->H;
   p.nks = cdiv(H, 128);
-  p.held = N <= 128 && held_bytes(N, H) <= LDS_ROWS;
+  // Held: up to 128 rows that LDS holds, but for those beyond 64 of a large vocabulary whose
+  // results, which it stores 32 bytes at a time, count for much beside the weight, where tiles
+  // can read that in place (128 rows of 512 x 151936 32.8 us and 23.9 in tiles, of 2048 47.7
+  // and 42.7; 80 rows of 2048 x 151936 41.0 and 40.9, 128 of 1024 x 32000 13.2 and 13.7; 64 of
+  // 1024 x 151936 25.4 and 27.5, 8 rows 17.0 and 23.8).
+  const int64_t ld = s->weight_stride ? s->weight_stride : code_bytes(H);
+  const bool tiles = N > 64 && s->V > 65536 && 24 * N > H && ld % 16 == 0;
+  p.held = N <= 128 && held_bytes(N, H) <= LDS_ROWS && !tiles;
   p.frags = (int)cdiv(N, 16);
   if (p.frags == 0) p.frags = 1;
   if (p.frags == 7) p.frags = 8;

@@ -212,7 +212,7 @@ def test_rows_past_32_bits(sv):
 # -------------------------------------------------------------------- head logits
 LOGITS = [(1, 1, 1), (1, 1024, 1000), (3, 100, 77), (16, 128, 513), (17, 4096, 999), (31, 683, 3601), (32, 96, 260),
           (33, 256, 130), (64, 64, 4099), (64, 4096, 300), (65, 512, 2049), (65, 1000, 517), (70, 7, 131), (129, 200, 1021),
-          (300, 384, 2048), (200, 1056, 70001), (257, 512, 66001), (5, 20001, 50), (40, 12000, 333), (1, 131072, 18),
+          (300, 384, 2048), (200, 1056, 70001), (257, 512, 66001), (5, 20001, 50), (90, 480, 70000), (90, 512, 70000), (128, 2048, 33), (40, 12000, 333), (1, 131072, 18),
           (2, 131071, 130), (150, 97, 511)]
 
 
