@@ -828,7 +828,7 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
   for (int64_t v0 = 0; v0 < s.V; v0 += step) {
     P.V = (int32_t)(s.V - v0 < step ? s.V - v0 : step);
     if (direct) {
-      P.w = weight_codes;
+      P.w = weight_codes + v0 * w_ld;
       // a load's range is checked by whole dwords: the last one of a row counts if any of its
       // bytes does (aligned, so it lies in that byte's memory)
       P.w_bytes = up(code_bytes(s.H), 4);

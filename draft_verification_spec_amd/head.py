@@ -274,6 +274,8 @@ def _logits4(hidden, weight, out_dtype, workspace, stream):
     if len(lead) != 1:
         raise TypeError("weight must be an Mx4 with codes [V, (H + 1) // 2]")
     V = lead[0]
+    if isinstance(hidden, Act8):
+        raise TypeError("hidden rows in 8 bits need a weight in 8 bits")
     if isinstance(hidden, Mx4):
         h, rows, hdev = _mx4(hidden, "hidden")
         if h != H:
@@ -314,6 +316,8 @@ def _hidden(hidden, H, what="hidden"):
         if hidden.codes.dtype != torch.int8:
             raise TypeError(f"{what} codes must be int8")
         return hidden.codes, hidden.scale, hidden.codes.device
+    if isinstance(hidden, Mx4):
+        raise TypeError(f"{what} must be a tensor or an Act8")
     return hidden, None, hidden.device
 
 
@@ -331,6 +335,8 @@ def head_logits(hidden, weight, *, out_dtype=None, workspace=None, stream=None):
     import torch
     if isinstance(weight, Mx4):
         return _logits4(hidden, weight, out_dtype, workspace, stream)
+    if isinstance(hidden, Mx4):
+        raise TypeError("hidden rows in 4 bits need a weight in 4 bits")
     if not isinstance(weight, Act8) or weight.codes.dim() != 2 or weight.codes.dtype != torch.int8:
         raise TypeError("weight must be an Act8 with int8 codes [V, H]")
     V, H = weight.codes.shape

@@ -301,6 +301,27 @@ def test_logits_guards(sv):
             assert torch.equal(out[:n, :v], want) and (out[:, v:] == 7).all() and (out[n] == 7).all()
 
 
+@pytest.mark.parametrize("n,h,v,step", [(3, 131072, 65900, 65536), (70, 20001, 13100, 13056), (130, 20000, 13100, None)])
+def test_logits_in_pieces(sv, n, h, v, step):
+    """Vocabularies that are taken in pieces: of staged scales (a weight read in place), and of
+    copied rows (one at no 16-byte distance); and one that is not.  The columns about the pieces'
+    borders against 64 bits."""
+    log(f"head_logits4 in pieces n={n} h={h} v={v}")
+    g = gen(v)
+    codes = torch.randint(0, 256, (v, (h + 1) // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.randint(120, 128, (v, (h + 31) // 32), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(n, h, generator=g, device="cuda")
+    got = sv.head_logits(x, sv.Mx4(codes, scale, h), out_dtype=F)
+    cols = {0, 1, v // 2, *range(v - 60, v)}
+    cols |= set(range(step - 3, step + 40)) if step else set()
+    cols = torch.tensor(sorted(cols), device="cuda")
+    code = torch.stack((codes[cols] & 15, codes[cols] >> 4), -1).flatten(1)[:, :h]
+    a, b = values(*plain_pack(x)), values(code, scale[cols])
+    want = a @ b.T
+    tol = (a.abs() @ b.abs().T) * h * 2.0 ** -24 + HALF[F] * want.abs()
+    within(got[:, cols], want, tol, "columns about the borders")
+
+
 def test_logits_do_not_depend_on_the_stream(sv):
     x, w = torch.randn(20, 640, generator=gen(1), device="cuda"), torch.randn(5000, 640, generator=gen(2), device="cuda")
     a = sv.mx4_pack(w)

@@ -105,6 +105,13 @@ def test_front_end_refusals():
         sv.head_logits(x, a, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         sv.head_logits(sv.Mx4(a.codes[:, :31], a.scale, 62), a)
+    a8 = sv.Act8(torch.zeros(10, 64, dtype=torch.int8), torch.zeros(10))
+    with pytest.raises(TypeError):
+        sv.head_logits(a8, a)
+    with pytest.raises(TypeError):
+        sv.head_logits(a, a8)
+    with pytest.raises(TypeError):
+        sv.head_ce(a, x, torch.zeros(10, dtype=torch.int64))
 
 
 DRIVER = r"""
