@@ -382,6 +382,21 @@ def test_offsets_past_32_bits(sv):
     assert not got[:-40].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_longest_rows(sv, dtype):
+    v = 1 << 24
+    z = torch.randn(2, v, generator=gen(1), device="cuda").to(dtype)
+    t = torch.tensor([v - 1, 0], device="cuda")
+    r = sv.logprobs(z, t, 0.9, top=32)
+    w = Want(z, t, 0.9)
+    w.check(r, "longest rows")
+    check_top(r, w, z, 32, "longest rows")
+    none = sv.logprobs(z, t, 0.9)
+    w.check(none, "longest rows without alternatives")
+    g, h = torch.tensor([1.0, -2.0], device="cuda"), torch.tensor([0.5, 0.0], device="cuda")
+    within(sv.logprobs_grad(z, t, r, g, h, 0.9), *w.grad(t, g, h, dtype), "longest rows")
+
+
 def test_many_short_rows(sv):
     n = 1 << 20
     z = torch.randn(n, 3, generator=gen(1), device="cuda")

@@ -360,6 +360,36 @@ def test_graphs(sv):
             assert torch.equal(r, want) and torch.equal(p, back)
 
 
+def test_first_call_captured(sv):
+    """A call that asks for more than 64 KB of LDS, captured before any like it was made."""
+    x, w = torch.randn(90, 2048, generator=gen(1), device="cuda"), torch.randn(700, 2048, generator=gen(2), device="cuda")
+    a, b = sv.mx4_pack(w), sv.mx4_pack(x)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        r = sv.head_logits(b, a, out_dtype=F)
+    for turn in range(3):
+        r.zero_()
+        gr.replay()
+        want = sv.head_logits(x, a, out_dtype=F)
+        torch.cuda.synchronize()
+        assert torch.equal(r, want)
+
+
+def test_largest_vocabulary(sv):
+    v, h = 1 << 24, 33
+    w = torch.randn(v, h, generator=gen(1), device="cuda")
+    a = sv.mx4_pack(w)
+    del w
+    for n in (2, 66):
+        x = torch.randn(n, h, generator=gen(n), device="cuda")
+        got = sv.head_logits(x, a, out_dtype=BF)
+        cols = torch.cat([torch.arange(50, device="cuda"), torch.arange(v - 50, v, device="cuda")])
+        wf = sv.mx4_unpack(sv.Mx4(a.codes[cols], a.scale[cols], h), F).double()
+        xf = values(*plain_pack(x))
+        want = xf @ wf.T
+        within(got[:, cols], want, (xf.abs() @ wf.abs().T) * h * 2.0 ** -24 + HALF[BF] * want.abs(), "ends of the vocabulary")
+
+
 def test_draft_step(sv):
     """A rollout step with a drafter's head in 4 bits and the target's in 8: drafted tokens
     verified against the target, then scored, and the policy gradient of what came out."""
