@@ -82,8 +82,12 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
         n = r.shape[0]
         k = n * top
         f = torch.empty(6 * n + 2 * k, dtype=torch.float32, device=dev)
-        logp, entropy, lse, norm, status, tv, ti = f.split_with_sizes((n, n, n, 2 * n, n, k, k))
-        status, ti = status.view(torch.int32), ti.view(torch.int32)
+        if top:
+            logp, entropy, lse, norm, status, tv, ti = f.split_with_sizes((n, n, n, 2 * n, n, k, k))
+            ti = ti.view(torch.int32)
+        else:
+            logp, entropy, lse, norm, status = f.split_with_sizes((n, n, n, 2 * n, n))
+        status = status.view(torch.int32)
         shape = sv_logprobs_shape_t(n, V, dt, top, ld, float(temperature), ignore)
         lib = _lib()
         need = lib.sv_logprobs_workspace_bytes(ctypes.byref(shape))
@@ -127,10 +131,14 @@ def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entrop
         h = None if grad_entropy is None else _float(grad_entropy, dev, "grad_entropy", lead)
         e = None if h is None else _float(result.entropy, dev, "entropy", lead)
         norm = norm.contiguous()
-        grad = torch.empty(logits.shape, dtype=odt, device=dev) if out is None else out
-        o, old = _rows(grad, V, "out")
-        if o.data_ptr() != grad.data_ptr():
-            raise ValueError("out must have unit element stride and rows one stride apart")
+        if out is None:
+            grad = o = torch.empty(logits.shape, dtype=odt, device=dev)
+            old = V
+        else:
+            grad = out
+            o, old = _rows(out, V, "out")
+            if o.data_ptr() != out.data_ptr():
+                raise ValueError("out must have unit element stride and rows one stride apart")
         shape = sv_logprobs_grad_shape_t(r.shape[0], V, dt, gt, ld, old, float(temperature), ignore)
         _check(_lib().sv_logprobs_grad(ctypes.byref(shape), r.data_ptr(), t.data_ptr(), norm.data_ptr(),
                                        None if e is None else e.data_ptr(), g.data_ptr(),
