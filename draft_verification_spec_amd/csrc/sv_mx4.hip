@@ -512,9 +512,10 @@ template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, 
 // us, of 4096 x 151936 398 to 379).  Rows a power of two apart lie on few memory channels at
 // any one step, so neighbouring tiles of the vocabulary begin at different pairs.
 //
-// 1024 rows of 4096 x 151936 take 375 us, 3.4 PFLOP/s: the main loop runs at 4.6, without its
-// loads it would at 6.1 (the instruction's own rate is 9 at the clock it runs at).  A third
-// buffer of the weight changed nothing, tiles of 128 x 128 take a quarter longer.
+// 1024 rows of 4096 x 151936 take 370 us, 3.4 PFLOP/s; without the loads 290 (230 of them the
+// matrix instructions, 23 cycles each, 60 the results' ways out).  A third buffer of the
+// weight, eight waves of half the size, stores of 128 bytes a row and workgroups begun at
+// times of their own each changed it by 1% or less; tiles of 128 x 128 take a quarter longer.
 template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel(LogitsP P) {
   __shared__ __align__(16) char lds[2 * (T::XBUF + T::YBUF)];
 #ifdef __HIP_DEVICE_COMPILE__
