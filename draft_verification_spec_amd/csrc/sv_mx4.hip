@@ -19,6 +19,7 @@ namespace {
 
 using namespace sv_gemm;
 using sv_mx4_host::cdiv;
+using sv_mx4_host::tiled_scale;
 
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
@@ -107,12 +108,6 @@ struct Out {
 __device__ __forceinline__ int64_t held_piece(int64_t block, int64_t row, int64_t N) { return block * N + row; }
 __device__ __forceinline__ int64_t held_scale(int64_t block, int64_t row, int64_t N) {
   return ((block / 16 * 4 + block % 4) * N + row) * 4 + block / 4 % 4;
-}
-
-// TILED: the scales of a row's 16 blocks are four words, blocks 4 k + q, k = 0 .. 3, in lane 16 q +
-// row % 16's; a lane's words of four times 16 rows lie together.
-__device__ __forceinline__ int64_t tiled_scale(int64_t row, int64_t group, int64_t lane, int64_t groups) {
-  return ((row / 64 * groups + group) * 64 + lane) * 4 + row / 16 % 4;
 }
 
 template <int FORM>
@@ -811,9 +806,8 @@ extern "C" int sv_head_logits4(const sv_logits4_shape_t *shape, const void *hidd
     Rows R = P.x;
     R.lanes = (int32_t)(L.Kp / 4);
     Out O = {ws + L.codes, ws + L.scales, L.x_ld, 0, s.N, 0, L.groups};
-    const int64_t most = sv_head_host::max_groups(256) * 1024 / R.lanes / 16 * 16;
-    for (int64_t n = 0; n < s.N; n += most) {
-      const int64_t rows = s.N - n < most ? s.N - n : most;
+    for (int64_t n = 0; n < s.N; n += L.rows) {
+      const int64_t rows = s.N - n < L.rows ? s.N - n : L.rows;
       launch_rows<TILED>(s.hidden_dtype, R, O, rows, st);
       R.x += rows * R.x_ld;
       if (given) R.scale += rows * R.s_ld;

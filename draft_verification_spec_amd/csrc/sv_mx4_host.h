@@ -47,6 +47,7 @@ struct Plan {
   int64_t image, x_scales;               // bytes of the hidden rows' codes and scales, as staged
   int64_t Kp, x_ld;                      // tiles: bytes of a staged code row, and between two
   int64_t groups;                        // tiles: 16-block groups of scales
+  int64_t rows;                          // tiles: hidden rows that a launch stages, whole groups of scales
   bool large;                            // tiles of 256 x 256
   // tiles: vocabulary entries per product where the weight is copied, and where only its
   // scales are staged
@@ -73,6 +74,15 @@ inline bool shape_ok(const sv_logits4_shape_t *s) {
   return cdiv(s->N, 128) * cdiv(s->V, 128) <= sv_head_host::max_groups(256);
 }
 
+// Where the tiled product's lanes take their scales.  Those of a row's 16 blocks are four words,
+// blocks 4 k + q, k = 0 .. 3, in lane 16 q + row % 16's; a lane's words of four times 16 rows lie
+// together.  So 64 rows are a group, and memory that begins with the first of one goes on as the
+// whole's does.
+constexpr int SCALE_ROWS = 64;
+constexpr int64_t tiled_scale(int64_t row, int64_t group, int64_t lane, int64_t groups) {
+  return ((row / SCALE_ROWS * groups + group) * 64 + lane) * 4 + row / 16 % 4;
+}
+
 // Whether weight code rows can be read in 16-byte pieces where they lie (what lies behind
 // a row's end meets zeros of the hidden rows).
 inline bool codes_direct(int64_t stride, uintptr_t base) { return stride % 16 == 0 && stride <= MAX_LD && base % 16 == 0; }
@@ -95,6 +105,7 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
   p.fused = p.held && s->hidden_dtype != SV_MX4 && N <= 16 && N * H <= 16384;
   p.Kp = up(code_bytes(H), SPAN);
   p.groups = p.Kp / SPAN;
+  p.rows = sv_head_host::max_groups(256) * 1024 / (p.Kp / 4) / SCALE_ROWS * SCALE_ROWS;
   p.large = sv_head_host::large_tiles(N, s->V);
   size_t o = 0;
   auto take = [&](int64_t bytes) { const size_t at = o; o = (o + bytes + 255) & ~(size_t)255; return at; };
