@@ -381,7 +381,7 @@ def _int32(t, dev, what, shape, ignore=-1):
     """Integer indices as int32, values outside its range held at its ends, unless an
     end is the index to ignore: then they become another that is no entry."""
     import torch
-    if t.dtype not in (torch.int32, torch.int64) or tuple(t.shape) != tuple(shape) or t.device != dev:
+    if t.dtype not in (torch.int32, torch.int64) or t.shape != shape or t.device != dev:
         raise ValueError(f"{what} must be int32 or int64 {list(shape)} on the rows' device")
     if t.dtype == torch.int64:
         low, high = -(1 << 31), (1 << 31) - 1

@@ -44,18 +44,19 @@ def bind(lib):
 
 def _logits(logits):
     """(dtype code, vocabulary, leading shape) of logits [..., V]."""
-    dt = _code(logits.dtype, "logits")
-    if logits.dim() < 1 or logits.shape[-1] < 1:
+    dt, shape = _code(logits.dtype, "logits"), logits.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("logits must be [..., V]")
-    V, lead = logits.shape[-1], logits.shape[:-1]
+    V, lead = shape[-1], shape[:-1]
     _fits(V | logits.numel() // V)
     return dt, V, lead
 
 
 def _index(ignore_index):
-    if not -(1 << 31) <= int(ignore_index) < (1 << 31):
+    ignore = int(ignore_index)
+    if not -(1 << 31) <= ignore < (1 << 31):
         raise ValueError("ignore_index must fit in 32 bits")
-    return int(ignore_index)
+    return ignore
 
 
 def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_index: int = -1, workspace=None,
@@ -67,8 +68,10 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
     value, equal ones by index; tokens of probability 0 (logits of -inf) are none, and what a
     row lacks is (-inf, -1).  Rows whose token is ignore_index are left out and not read: 0,
     and no alternatives.  A row with a data error (its token outside the vocabulary, a logit
-    NaN or +inf, or all -inf) has its HEAD_* bits in status and NaN results.  workspace:
-    uint8 scratch of at least sv_logprobs_workspace_bytes, 256-byte aligned."""
+    NaN or +inf, or all -inf) has its HEAD_* bits in status and NaN results.  Each result is a
+    tensor of its own, which may be changed in place; the rows' (24 bytes a row) share one
+    piece of memory, which the last of them frees.  workspace: uint8 scratch of at least
+    sv_logprobs_workspace_bytes, 256-byte aligned."""
     import torch
     dt, V, lead = _logits(logits)
     top, ignore, dev = int(top), _index(ignore_index), logits.device
@@ -78,30 +81,28 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
     with here:
         r, ld = _rows(logits, V, "logits")
         t = _int32(tokens, dev, "tokens", lead, ignore)
-        # one piece of memory for all results (a tensor of its own costs the host three views)
+        # One piece of memory for the rows' results: a tensor of its own costs the host three of
+        # the pieces that this split gives, which autograd takes for tensors of their own too
+        # (views of one, it refuses to change in place).
         n = r.shape[0]
-        k = n * top
-        f = torch.empty(6 * n + 2 * k, dtype=torch.float32, device=dev)
+        f = torch.empty(6 * n, dtype=torch.float32, device=dev)
+        logp, entropy, lse, norm, status = torch.unsafe_split_with_sizes(f, (n, n, n, 2 * n, n))
+        p, tv, ti = f.data_ptr(), None, None
         if top:
-            logp, entropy, lse, norm, status, tv, ti = f.split_with_sizes((n, n, n, 2 * n, n, k, k))
-            ti = ti.view(torch.int32)
-        else:
-            logp, entropy, lse, norm, status = f.split_with_sizes((n, n, n, 2 * n, n))
-        status = status.view(torch.int32)
+            tv = torch.empty((*lead, top), dtype=torch.float32, device=dev)
+            ti = torch.empty((*lead, top), dtype=torch.int32, device=dev)
         shape = sv_logprobs_shape_t(n, V, dt, top, ld, float(temperature), ignore)
-        lib = _lib()
-        need = lib.sv_logprobs_workspace_bytes(ctypes.byref(shape))
+        lib, at = _lib(), ctypes.byref(shape)
+        need = lib.sv_logprobs_workspace_bytes(at)
         buf = _scratch(workspace, need, dev) if need or workspace is not None else None
-        p = f.data_ptr()
-        at = p + 24 * n
-        _check(lib.sv_logprobs(ctypes.byref(shape), r.data_ptr(), t.data_ptr(), p, p + 4 * n, p + 8 * n, p + 12 * n,
-                               p + 20 * n, at if top else None, at + 4 * k if top else None,
+        _check(lib.sv_logprobs(at, r.data_ptr(), t.data_ptr(), p, p + 4 * n, p + 8 * n, p + 12 * n, p + 20 * n,
+                               tv.data_ptr() if top else None, ti.data_ptr() if top else None,
                                None if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(), st))
+    # (.data: the tensor as it is shaped here, no view of the one before)
     if len(lead) != 1:
-        logp, entropy, lse, status = logp.view(lead), entropy.view(lead), lse.view(lead), status.view(lead)
-    if not top:
-        return LogprobsResult(logp, entropy, lse, norm.view(2, *lead), status, None, None)
-    return LogprobsResult(logp, entropy, lse, norm.view(2, *lead), status, tv.view(*lead, top), ti.view(*lead, top))
+        logp, entropy, lse, status = (x.view(lead).data for x in (logp, entropy, lse, status))
+    norm, status = norm.view(2, *lead).data, status.view(torch.int32).data
+    return LogprobsResult(logp, entropy, lse, norm, status, tv, ti)
 
 
 def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entropy=None, temperature: float = 1.0, *,
