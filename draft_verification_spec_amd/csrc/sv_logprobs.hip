@@ -522,6 +522,8 @@ struct GradP {
   float T;
 };
 
+constexpr float LEAST = 160.f;           // 2^-LEAST and less are 0 in fp32
+
 // One tile of a row: 256 threads, VECS vectors each.  A thread has read its entries before
 // it writes them, so the gradient may lie where the logits do.
 template <int DT, int GT> __global__ __launch_bounds__(256) void grad_kernel(GradP P) {
@@ -543,7 +545,11 @@ template <int DT, int GT> __global__ __launch_bounds__(256) void grad_kernel(Gra
   if (used) {
     load_step<DT, 4>(P.z + n * P.z_ld, at, P.V, r);
   }
-  const float k0 = -(g + hs) * inv, k1 = -h * (float)LN2 * inv, l2 = ls * LOG2E;
+  // 1 / T is in the factors, unless they would leave fp32 (T below 1e-34, say, where entries of
+  // probability 0 would be 0 times infinity): then it comes to the results.
+  const bool fits = (fabsf(g) + fabsf(hs) + LEAST * fabsf(h)) * inv < __builtin_inff();
+  const float before = fits ? inv : 1.f, behind = fits ? 1.f : inv;
+  const float k0 = -(g + hs) * before, k1 = -h * (float)LN2 * before, l2 = ls * LOG2E;
   char *o = P.grad + n * P.g_ld;
 #pragma unroll
   for (int s = 0; s < VECS; ++s) {
@@ -553,15 +559,17 @@ template <int DT, int GT> __global__ __launch_bounds__(256) void grad_kernel(Gra
     for (int w = 0; w < W; ++w) {
       v[w] = 0.f;
       if (used) {
-        const float t = __builtin_fmaxf(fmaf(unpack<DT>(r[s], w) - m, c, -l2), -1e4f);   // log2 p
+        const float t = __builtin_fmaxf(fmaf(unpack<DT>(r[s], w) - m, c, -l2), -LEAST);   // log2 p
         v[w] = __builtin_amdgcn_exp2f(t) * fmaf(t, k1, k0);
       }
     }
     if (used && token >= e && token < e + W) {
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if (token == e + w) v[w] += g * inv;
+        if (token == e + w) v[w] += g * before;
     }
+#pragma unroll
+    for (int w = 0; w < W; ++w) v[w] *= behind;
     if (e + W <= P.V) {
       if constexpr (GT == SV_BF16) {
         uint32_t u[W / 2];

@@ -78,7 +78,8 @@ int sv_logprobs(const sv_logprobs_shape_t *shape, const void *logits, const int3
  * with p from norm, all of the same logits, tokens and temperature as in sv_logprobs.  Rows
  * that are left out, rows whose token is outside the vocabulary and rows whose norm is not
  * finite (those with a data error) have a gradient of 0 whatever their g and h, and are not
- * read.  Of other rows a g or h that is not finite makes every entry NaN or infinite.
+ * read.  Of other rows a g or h that is not finite makes every entry NaN or infinite; entries
+ * beyond the gradient's type are infinite (magnitudes of g and h up to 1e36, at any temperature).
  */
 typedef struct {
     int32_t N, V;           /* as above */
