@@ -105,6 +105,22 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
     return LogprobsResult(logp, entropy, lse, norm, status, tv, ti)
 
 
+def _shared(a, lda, b, ldb):
+    """Whether rows a [N, V] and b [N, V], lda and ldb elements apart, share memory otherwise than
+    element by element."""
+    n, V = a.shape
+    ea, eb, d = a.element_size(), b.element_size(), b.data_ptr() - a.data_ptr()
+    if not n or d >= ((n - 1) * lda + V) * ea or -d >= ((n - 1) * ldb + V) * eb:
+        return False
+    step = lda * ea
+    if n == 1 or step != ldb * eb:
+        return d != 0 or a.dtype is not b.dtype or n > 1
+    if d == 0 and a.dtype is b.dtype:
+        return False
+    d %= step                                         # b's rows lie in the gaps of a's, or meet them
+    return d < V * ea or d + V * eb > step
+
+
 def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entropy=None, temperature: float = 1.0, *,
                   ignore_index: int = -1, out=None, out_dtype=None, stream=None):
     """The gradient of the logits [..., V] from those of the log-probabilities (grad_logp) and
@@ -113,7 +129,8 @@ def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entrop
     logits, tokens, temperature and ignore_index as logprobs was given them, result what it
     returned.  Rows left out and rows with a data error get zeros.  out_dtype: the logits'
     unless given.  out: memory for the gradient, of its shape and type with unit element
-    stride, the logits themselves among it (they are then lost)."""
+    stride, the logits themselves among it (they are then lost); it may not overlap them
+    otherwise."""
     import torch
     dt, V, lead = _logits(logits)
     ignore, dev = _index(ignore_index), logits.device
@@ -140,6 +157,8 @@ def logprobs_grad(logits, tokens, result: LogprobsResult, grad_logp, grad_entrop
             o, old = _rows(out, V, "out")
             if o.data_ptr() != out.data_ptr():
                 raise ValueError("out must have unit element stride and rows one stride apart")
+            if _shared(r, ld, o, old):
+                raise ValueError("out must be the logits' own memory, element by element, or lie apart from it")
         shape = sv_logprobs_grad_shape_t(r.shape[0], V, dt, gt, ld, old, float(temperature), ignore)
         _check(_lib().sv_logprobs_grad(ctypes.byref(shape), r.data_ptr(), t.data_ptr(), norm.data_ptr(),
                                        None if e is None else e.data_ptr(), g.data_ptr(),
