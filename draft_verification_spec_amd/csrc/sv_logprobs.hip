@@ -354,7 +354,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(LogprobsP P) {
   Best best;
   u32x4 r[VECS], next[VECS];
   load_step<DT, WAVES>(row, at, end, r);
-  // the first loads go out before the token is known
+  // the first loads go out before the token is known, also those of rows that are left out
   const int token = P.tokens[n];
   if (token == P.ignore) {
     if (part == 0) left_out(P, n);

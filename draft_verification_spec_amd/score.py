@@ -66,7 +66,7 @@ def logprobs(logits, tokens, temperature: float = 1.0, *, top: int = 0, ignore_i
 
     logits [..., V] float32 or bfloat16, tokens [...] int32 or int64.  Alternatives come by
     value, equal ones by index; tokens of probability 0 (logits of -inf) are none, and what a
-    row lacks is (-inf, -1).  Rows whose token is ignore_index are left out and not read: 0,
+    row lacks is (-inf, -1).  Rows whose token is ignore_index are left out, whatever they hold: 0,
     and no alternatives.  A row with a data error (its token outside the vocabulary, a logit
     NaN or +inf, or all -inf) has its HEAD_* bits in status and NaN results.  Each result is a
     tensor of its own, which may be changed in place; the rows' (24 bytes a row) share one

@@ -45,8 +45,9 @@ extern "C" {
  * norm is the normaliser in two parts, the rows' largest logits and then their ln sum_v exp((logits[n,v] -
  * largest) / T): unlike lse, their sum, it keeps its precision where logits are large, and
  * the gradient reads it.
- * Rows whose token is ignore_index are left out and not read: logp = entropy = lse = norm =
- * 0, status 0, alternatives (-inf, -1).  A row with a data error (its token outside the
+ * Rows whose token is ignore_index are left out, whatever they hold (their first entries are read
+ * all the same, before the token is known): logp = entropy = lse = norm = 0, status 0,
+ * alternatives (-inf, -1).  A row with a data error (its token outside the
  * vocabulary, a logit NaN or +inf, or all -inf) has its bits in status, NaN in logp, entropy,
  * lse, norm and top_logp, and -1 in top_idx.  Sums are fp32 over at most 32 terms and fp64
  * beyond.
