@@ -19,7 +19,8 @@ using sv_head_host::real_dtype;
 
 constexpr int VECS = 4;                  // 16-byte vectors of a thread at a time
 constexpr int LIST = 32;                 // alternatives that a list holds
-constexpr int64_t MAX_GROUPS = sv_head_host::max_groups(1024);
+// a launch holds every shape's workgroups: one a row, or at most 64 each of fewer than 128 rows
+static_assert(SV_HEAD_MAX_N <= sv_head_host::max_groups(1024) && 128 * 64 <= sv_head_host::max_groups(1024), "one launch");
 
 // A row's share of the launch: waves of a workgroup, workgroups of a row.
 struct Plan {

@@ -24,7 +24,6 @@ using sv_mx4_host::tiled_scale;
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------ rows to codes
 constexpr int64_t FEW = 8 * sv_mx4_host::CUS * 1024;     // items (lanes' shares) that take a thread each
