@@ -34,9 +34,12 @@ inline Plan plan_for(const sv_logprobs_shape_t *s) {
   const int64_t w = 16 / esize(s->dtype);
   // Few rows are cut into parts, joined in a launch of their own, where a row is more than
   // three steps of 16 waves (that launch costs the host 3 us too): into many small ones without
-  // alternatives (one row of 151936 bf16 7.1 us, 16 uncut), into fewer with them, whose lists
-  // take longer to join (17 with waves in sixteens, 24 uncut; 32 rows 18 and 26).  From 128
-  // rows on (20.5 us and 29) uncut rows fill the chip, from 1024 on with four waves each.
+  // alternatives, into fewer with them, whose lists take longer to join.  Rows of 151936 bf16, cut
+  // and uncut: one 7.1 and 16 us, 64 11.4 and 18.7, 127 17.1 and 19.2, 192 21.7 and 20.7, 256
+  // 24.3 and 21.4; with twenty alternatives one 16.3 and 20.6, 64 18.7 and 24.3, 127 23.5 and
+  // 25.2, 192 26.7 and 26.3.  The border at 128 rows is lower than these put it (128 to 160 rows
+  // would gain a tenth to a twentieth), and rows that begin a second round on 256 CUs would gain
+  // from a cut as well (300 27.6 and 35.5).  From 1024 rows on four waves a row fill the chip.
   const int64_t N = s->N < 1 ? 1 : s->N, step = 16 * 64 * VECS * w;
   const bool cut = N < 128 && s->V > 3 * step;
   p.waves = (cut && !s->top) || N >= 1024 ? 4 : 16;

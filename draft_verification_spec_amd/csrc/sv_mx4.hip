@@ -298,7 +298,8 @@ struct Chunk {
 // 16 vocabulary rows at a time from memory to registers, a chunk ahead, with no barrier;
 // rows lie at any address and distance.  Bound by reading the head: 32 rows of 4096 x 151936
 // 70 us (330 MB, 4.9 TB/s with the logits), 64 79.  Loads past the cache (nontemporal) fetch
-// each line's halves apart: 76 us for the 32 rows.
+// each line's halves apart: 76 us for the 32 rows.  Beyond 64 rows the registers (140 and more)
+// leave a CU one workgroup, though LDS may hold two.
 template <int FM, int SRC, int OT, int WAVES> __global__ __launch_bounds__(64 * WAVES, FM > 4 ? 2 : 4) void held_kernel(LogitsP P) {
   extern __shared__ __align__(16) uint8_t held[];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
@@ -506,10 +507,12 @@ template <int K> __device__ __forceinline__ void mul4(f32x4 *c, const u32x4 *y, 
 // us, of 4096 x 151936 398 to 379).  Rows a power of two apart lie on few memory channels at
 // any one step, so neighbouring tiles of the vocabulary begin at different pairs.
 //
-// 1024 rows of 4096 x 151936 take 370 us, 3.4 PFLOP/s; without the loads 290 (230 of them the
+// 1024 rows of 4096 x 151936 take 363 to 382 us (on several GPUs), 3.4 PFLOP/s; without the loads 290 (230 of them the
 // matrix instructions, 23 cycles each, 60 the results' ways out).  A third buffer of the
 // weight, eight waves of half the size, stores of 128 bytes a row and workgroups begun at
 // times of their own each changed it by 1% or less; tiles of 128 x 128 take a quarter longer.
+// With bf16 results the large tiles' wave is 7 registers beyond its 512: they are spilled and read
+// again outside the loop over k, where results leave.
 template <class T, int OT> __global__ __launch_bounds__(T::TPB) void tile_kernel(LogitsP P) {
   __shared__ __align__(16) char lds[2 * (T::XBUF + T::YBUF)];
 #ifdef __HIP_DEVICE_COMPILE__

@@ -95,7 +95,8 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
   // results, which it stores 32 bytes at a time, count for much beside the weight, where tiles
   // can read that in place (128 rows of 512 x 151936 32.8 us and 23.9 in tiles, of 2048 47.7
   // and 42.7; 80 rows of 2048 x 151936 41.0 and 40.9, 128 of 1024 x 32000 13.2 and 13.7; 64 of
-  // 1024 x 151936 25.4 and 27.5, 8 rows 17.0 and 23.8).
+  // 1024 x 151936 25.4 and 27.5, 8 rows 17.0 and 23.8).  Measured at 32000 and 151936 entries;
+  // where between them the border lies was not.
   const int64_t ld = s->weight_stride ? s->weight_stride : code_bytes(H);
   const bool tiles = N > 64 && s->V > 65536 && 24 * N > H && ld % 16 == 0;
   p.held = N <= 128 && held_bytes(N, H) <= LDS_ROWS && !tiles;
@@ -128,7 +129,9 @@ inline Plan plan_for(const sv_logits4_shape_t *s) {
   if (p.scaled > up(s->V, 256)) p.scaled = up(s->V, 256);
   p.codes = take(p.image);
   p.scales = take(p.x_scales);
-  p.weight = take(p.piece * p.x_ld);       // (an aligned stride may still meet an unaligned address)
+  // (Copied rows have their place also where the stride is aligned: the address, which a size
+  // must do for whatever it is, may not be, and such a weight is copied as well.)
+  p.weight = take(p.piece * p.x_ld);
   p.wscale = take((p.scaled > p.piece ? p.scaled : p.piece) * p.groups * 16);
   p.total = o;
   return p;
